@@ -83,6 +83,7 @@ typedef struct moe_ctx* moe_ctx_t;
 /* Limits (UNSUPPORTED beyond them). */
 #define MOE_MAX_EXPERTS 1024
 #define MOE_MAX_TOPK 32
+#define MOE_MAX_ROUTE_GROUPS 64
 
 /* ------------------------------------------------------------------------
  * Context.  moe_ctx_create checks that `device` is a gfx950 GPU, records its
@@ -224,6 +225,92 @@ moe_status_t moe_route_topk(moe_ctx_t ctx, const float* logits, int64_t T,
                             int32_t* topk_idx, float* topk_w, void* stream);
 
 /* ------------------------------------------------------------------------
+ * moe_route_scored -- router top-k with a score function, a balance bias,
+ * expert groups and scaled weights; moe_route_scored_bwd -- its backward.
+ * [PG3, practical-implications paragraph: Top-k routing, load imbalance.]
+ * The page names top-k routing and load balance but no formula; the library
+ * takes these.  Per token, in float64:
+ *   score  s_e = softmax over all E logits, or sigmoid of the logit
+ *   key    c_e = s_e + bias_e; without a bias the logit (it orders alike)
+ *   groups the E experts in n_group consecutive runs of E / n_group; a run
+ *          scores its largest key (MOE_GROUP_MAX) or the sum of the two
+ *          largest c_e (MOE_GROUP_TOP2; without a bias c_e = s_e); the
+ *          topk_group best runs stay, equal scores to the lower run
+ *   topk_idx  the k largest keys of the runs that stay, slot 0 the largest,
+ *          equal keys to the lower expert id (+0 and -0 are equal)
+ *   topk_w scale * s_j, or with renormalize scale * s_j / sum over the
+ *          chosen (softmax: the softmax restricted to the chosen experts;
+ *          sigmoid: 0 where every chosen score underflows to 0); rounded to
+ *          float32.  The bias takes no part in the weights.
+ * Backward (the selection passes no gradient; the bias gets none): with
+ * g = scale * dtopk_w and, renormalised, h_j = s_j / sum_i s_i
+ *   renormalised      dl_j = h_j (g_j - sum_i h_i g_i) on the chosen
+ *                     experts (sigmoid: times 1 - s_j), 0 elsewhere
+ *   sigmoid           dl_j = s_j (1 - s_j) g_j on the chosen, 0 elsewhere
+ *   softmax           dl_e = s_e (G_e - sum_i s_i g_i), G_e = g on the
+ *                     chosen experts and 0 elsewhere
+ * every element of dlogits is written.
+ *
+ *  logits   float32 [T, E];  bias float32 [E] or NULL (the forward only)
+ *  topk_idx int32 [T, k];  topk_w, dtopk_w float32 [T, k];
+ *  dlogits  float32 [T, E]
+ *  T >= 0 (T = 0 is a no-op), 1 <= k <= min(E, 32), E <= 1024,
+ *  1 <= topk_group <= n_group <= 64, E % n_group == 0, the kept runs hold
+ *  at least k experts, two experts per run for MOE_GROUP_TOP2, scale
+ *  finite.  n_group, topk_group and group_score do not matter to the
+ *  backward but are checked alike.
+ * A bias of -infinity masks an expert (it is chosen only where fewer than k
+ * others can be).  A NaN or infinite logit, or a bias that is NaN or
+ * +infinity, records MOE_DEVERR_LOGITS and leaves the selection of the
+ * tokens it concerns unspecified (expert ids stay in [0, E)).  In the
+ * backward an expert id outside [0, E) records MOE_DEVERR_EXPERT_ID and
+ * contributes nothing.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (E, k, n_group, T >=
+ * 2^25), MOE_ERR_HIP.
+ * ---------------------------------------------------------------------- */
+typedef enum moe_score {
+  MOE_SCORE_SOFTMAX = 0,
+  MOE_SCORE_SIGMOID = 1
+} moe_score_t;
+typedef enum moe_group_score {
+  MOE_GROUP_MAX = 0,     /* the largest key of the group */
+  MOE_GROUP_TOP2 = 1     /* the sum of its two largest */
+} moe_group_score_t;
+typedef struct moe_route_opts {
+  moe_score_t score;
+  int32_t n_group;       /* 1: no groups */
+  int32_t topk_group;
+  moe_group_score_t group_score;
+  int32_t renormalize;
+  float scale;
+} moe_route_opts;
+
+moe_status_t moe_route_scored(moe_ctx_t ctx, const float* logits,
+                              const float* bias, int64_t T, int32_t E,
+                              int32_t k, const moe_route_opts* opts,
+                              int32_t* topk_idx, float* topk_w, void* stream);
+moe_status_t moe_route_scored_bwd(moe_ctx_t ctx, const float* logits,
+                                  const int32_t* topk_idx,
+                                  const float* dtopk_w, int64_t T, int32_t E,
+                                  int32_t k, const moe_route_opts* opts,
+                                  float* dlogits, void* stream);
+
+/* moe_router_proj_bwd -- the second half of moe_router_bwd, for logit
+ * gradients that come from elsewhere (moe_route_scored_bwd, an auxiliary
+ * loss): dW_r = dlogits^T x and dx = dlogits W_r, float32 with a fixed
+ * summation order.
+ *  dlogits float32 [T, E];  x bf16 [T, H];  w_r bf16 [E, H]
+ *  dw_r float32 [E, H] or NULL;  dx float32 [T, H] or NULL
+ *  ws: moe_router_bwd_workspace_size bytes (NULL when that is 0)
+ *  T = 0: dw_r is set to zero.  With dx, T <= 64 * 65535.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE,
+ * MOE_ERR_HIP. */
+moe_status_t moe_router_proj_bwd(moe_ctx_t ctx, const float* dlogits,
+                                 const void* x, const void* w_r, int64_t T,
+                                 int32_t H, int32_t E, float* dw_r, float* dx,
+                                 void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * moe_permute -- expert-order permutation and row gather.
  * [PG1, section "Grouped experts instead of a Python loop", and PG2, section
  *  "1) Fragmented expert kernels": the grouped GEMM gathers the tokens of
@@ -317,6 +404,127 @@ moe_status_t moe_unpermute(moe_ctx_t ctx, const void* z_perm,
 moe_status_t moe_unpermute_probs_grad(moe_ctx_t ctx, const float* dw_perm,
                                       const int32_t* row_map, int64_t T,
                                       int32_t k, float* dprobs, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_unpermute_dropout -- combine with dropout and residual;
+ * moe_unpermute_dropout_bwd -- its backward.
+ * [PG4, section "Sources of speedup": the combine that follows the expert
+ *  compute.]  The page gives no dropout; it is the training form of the
+ * residual branch.
+ *   y[t] = residual[t] + M[t] * sum_j c_j z_perm[row_map[t*k+j]]
+ *   dz_perm[row_map[t*k+j]] = c_j M[t] dy[t]
+ *   dtopk_w[t, j] = sum_h z_perm[row_map[t*k+j], h] M[t, h] dy[t, h]
+ * (dresidual = dy).  M[t, h] = 0 where value v = t H + h is dropped, else
+ * 65536 / (65536 - thr), thr = round(65536 p), half up: the share dropped is
+ * p to the nearest multiple of 2^-16, and the mean is kept exactly for that
+ * share.  p < 2^-17 drops nothing, thr = 65536 everything (y = residual).
+ * Value v is dropped where its 16 random bits are below thr: bits
+ * 16 (v % 8) .. + 15 of the 128-bit output of the Philox 4x32-10 generator
+ * (Salmon, Moraes, Dror and Shaw, 2011) with key = seed and counter = v / 8
+ * (low 64 bits), offset + *step (high 64 bits).  The mask is not stored: the
+ * backward is given the same p, seed, offset and step and evaluates it
+ * again.  `step` (nullable) is a device word added to offset, so that a
+ * captured graph can draw another mask at every replay; calls that must
+ * draw different masks need different (seed, offset + *step).
+ * Sums are float32 in ascending j; each output is rounded to bf16 once.
+ *
+ *  z_perm   bf16 [T*k, H];  row_map int32 [T*k], or NULL with k = 1 for
+ *           rows in token order (a dense layer's dropout).  Pairs with
+ *           row_map outside [0, T*k) contribute nothing (their dtopk_w is
+ *           0); rows of dz_perm that no pair maps to are left as they were;
+ *           two pairs must not map to one row (the backward's row is then
+ *           that of one of them).
+ *  topk_w   float32 [T, k] or NULL (c_j = 1)
+ *  residual bf16 [T, H] or NULL (0); y may be the residual itself
+ *  y, dy    bf16 [T, H];  dz_perm bf16 [T*k, H]
+ *  dtopk_w  float32 [T, k] or NULL; needs z_perm (else nullable)
+ *  T >= 0, H % 8 == 0, k <= 32, 0 <= p <= 1; rows 16-byte aligned.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_HIP.
+ * ---------------------------------------------------------------------- */
+moe_status_t moe_unpermute_dropout(moe_ctx_t ctx, const void* z_perm,
+                                   const int32_t* row_map,
+                                   const float* topk_w, const void* residual,
+                                   int64_t T, int32_t H, int32_t k, double p,
+                                   uint64_t seed, uint64_t offset,
+                                   const uint64_t* step, void* y,
+                                   void* stream);
+moe_status_t moe_unpermute_dropout_bwd(moe_ctx_t ctx, const void* dy,
+                                       const int32_t* row_map,
+                                       const float* topk_w,
+                                       const void* z_perm, int64_t T,
+                                       int32_t H, int32_t k, double p,
+                                       uint64_t seed, uint64_t offset,
+                                       const uint64_t* step, void* dz_perm,
+                                       float* dtopk_w, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_linear_fwd -- dense linear layer with bias, activation and residual;
+ * moe_linear_bwd -- its gradients.
+ * [PG2, section "Why dense and MoE models differ": the dense feed-forward
+ *  layers beside the MoE ones (projections, shared branches).]
+ *   z = x W^T + bias,  y = act(z) + residual
+ *   dz = dy act'(z),  dx = dz W,  dW = dz^T x,  db = sum over rows of dz
+ * (dresidual = dy).  act: none, relu (0 at 0, like its gradient), gelu
+ * z Phi(z), gelu_tanh 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))), silu
+ * z / (1 + e^-z).  Products are accumulated in float32; bias, activation
+ * and residual are applied to the float32 value and y is rounded to bf16
+ * once.  z_save is z rounded to bf16; the backward takes it, rounds dz to
+ * bf16 for the two products and sums db from the float32 values.
+ * Summation orders are fixed: the same inputs and sizes give the same bits.
+ *
+ *  x bf16 [M, K];  w bf16 [N, K];  bias, db float32 [N];
+ *  residual, y, z_save, z, dy bf16 [M, N];  dx bf16 [M, K];  dw bf16 [N, K]
+ *  M >= 0, N >= 1, K >= 8 with K % 8 == 0 (any M and N), N and K <= 2^22,
+ *  M * (max(N, K) + 256) and N * K <= 2^36; tensors 16-byte aligned (bias,
+ *  db: 4).  M = 0: the forward is a no-op, dw and db are set to zero.
+ *  y may be the residual itself.  Other outputs must not overlap inputs.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE (ws
+ * missing or smaller than the _workspace_size of the same arguments),
+ * MOE_ERR_HIP.
+ * ---------------------------------------------------------------------- */
+typedef enum moe_activation {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_GELU = 2,
+  MOE_ACT_GELU_TANH = 3,
+  MOE_ACT_SILU = 4
+} moe_activation_t;
+typedef struct moe_linear_fwd_args {
+  int64_t M;
+  int32_t N, K;
+  moe_activation_t act;
+  const void* x;
+  const void* w;
+  const float* bias;             /* nullable */
+  const void* residual;          /* nullable */
+  void* y;                       /* out */
+  void* z_save;                  /* out, nullable */
+  void* ws;                      /* workspace (NULL when its size is 0) */
+  size_t ws_bytes;
+} moe_linear_fwd_args;
+typedef struct moe_linear_bwd_args {
+  int64_t M;
+  int32_t N, K;
+  moe_activation_t act;
+  const void* dy;
+  const void* x;                 /* needed for dw */
+  const void* w;                 /* needed for dx */
+  const void* z;                 /* the forward's z_save; unused for none */
+  void* dx;                      /* out, nullable */
+  void* dw;                      /* out, nullable */
+  float* db;                     /* out, nullable */
+  void* ws;
+  size_t ws_bytes;
+} moe_linear_bwd_args;
+
+moe_status_t moe_linear_fwd_workspace_size(const moe_linear_fwd_args* args,
+                                           size_t* bytes);
+moe_status_t moe_linear_fwd(moe_ctx_t ctx, const moe_linear_fwd_args* args,
+                            void* stream);
+moe_status_t moe_linear_bwd_workspace_size(const moe_linear_bwd_args* args,
+                                           size_t* bytes);
+moe_status_t moe_linear_bwd(moe_ctx_t ctx, const moe_linear_bwd_args* args,
+                            void* stream);
 
 /* ------------------------------------------------------------------------
  * mxfp8_quantize -- MXFP8 quantisation of a bf16 tensor.

@@ -20,8 +20,14 @@ __all__ = [
     "lib_path", "load_library", "MoEError", "PREC_BF16", "PREC_MXFP8",
     "PREC_FP8_TENSOR", "fp8_tensor_quantize",
     "ROWWISE", "COLWISE", "moe_router_logits", "moe_router_bwd",
-    "moe_route_topk", "moe_permute", "moe_permute_noalloc",
+    "moe_route_topk", "moe_route_scored", "moe_route_scored_bwd",
+    "moe_router_proj_bwd", "SCORE_SOFTMAX", "SCORE_SIGMOID", "GROUP_MAX",
+    "GROUP_TOP2",
+    "moe_permute", "moe_permute_noalloc",
     "moe_gather_rows",
+    "moe_unpermute_dropout", "moe_unpermute_dropout_bwd",
+    "moe_linear_fwd", "moe_linear_bwd", "ACT_NONE", "ACT_RELU", "ACT_GELU",
+    "ACT_GELU_TANH", "ACT_SILU",
     "moe_unpermute", "moe_unpermute_probs_grad", "mxfp8_quantize",
     "mxfp8_quantize_f32",
     "moe_grouped_mlp_fwd", "moe_expert_loop_mlp_fwd", "moe_grouped_mlp_bwd",
@@ -38,11 +44,22 @@ PREC_MXFP8 = 1
 PREC_FP8_TENSOR = 2
 ROWWISE = 0
 COLWISE = 1
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
+GROUP_MAX = 0
+GROUP_TOP2 = 1
+ACT_NONE = 0
+ACT_RELU = 1
+ACT_GELU = 2
+ACT_GELU_TANH = 3
+ACT_SILU = 4
 
 _c_i32 = ctypes.c_int32
 _c_i64 = ctypes.c_int64
 _c_p = ctypes.c_void_p
 _c_sz = ctypes.c_size_t
+_c_u64 = ctypes.c_uint64
+_c_f64 = ctypes.c_double
 
 
 class MoEError(RuntimeError):
@@ -80,12 +97,55 @@ class _BwdArgs(ctypes.Structure):
     ]
 
 
+class _RouteOpts(ctypes.Structure):
+    _fields_ = [
+        ("score", ctypes.c_int), ("n_group", _c_i32), ("topk_group", _c_i32),
+        ("group_score", ctypes.c_int), ("renormalize", _c_i32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class _LinearFwdArgs(ctypes.Structure):
+    _fields_ = [
+        ("M", _c_i64), ("N", _c_i32), ("K", _c_i32), ("act", ctypes.c_int),
+        ("x", _c_p), ("w", _c_p), ("bias", _c_p), ("residual", _c_p),
+        ("y", _c_p), ("z_save", _c_p), ("ws", _c_p), ("ws_bytes", _c_sz),
+    ]
+
+
+class _LinearBwdArgs(ctypes.Structure):
+    _fields_ = [
+        ("M", _c_i64), ("N", _c_i32), ("K", _c_i32), ("act", ctypes.c_int),
+        ("dy", _c_p), ("x", _c_p), ("w", _c_p), ("z", _c_p),
+        ("dx", _c_p), ("dw", _c_p), ("db", _c_p),
+        ("ws", _c_p), ("ws_bytes", _c_sz),
+    ]
+
+
 _SIGS = {
     "moe_ctx_create": [ctypes.c_int, ctypes.POINTER(_c_p)],
     "moe_ctx_destroy": [_c_p],
     "moe_ctx_check_device_status": [_c_p, _c_p, ctypes.POINTER(_c_i32)],
     "moe_route_topk": [_c_p, _c_p, _c_i64, _c_i32, _c_i32, _c_i32, _c_p, _c_p,
                        _c_p],
+    "moe_route_scored": [_c_p, _c_p, _c_p, _c_i64, _c_i32, _c_i32,
+                         ctypes.POINTER(_RouteOpts), _c_p, _c_p, _c_p],
+    "moe_route_scored_bwd": [_c_p, _c_p, _c_p, _c_p, _c_i64, _c_i32, _c_i32,
+                             ctypes.POINTER(_RouteOpts), _c_p, _c_p],
+    "moe_router_proj_bwd": [_c_p, _c_p, _c_p, _c_p, _c_i64, _c_i32, _c_i32,
+                            _c_p, _c_p, _c_p, _c_sz, _c_p],
+    "moe_unpermute_dropout": [_c_p, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_i32,
+                              _c_i32, _c_f64, _c_u64, _c_u64, _c_p, _c_p,
+                              _c_p],
+    "moe_unpermute_dropout_bwd": [_c_p, _c_p, _c_p, _c_p, _c_p, _c_i64,
+                                  _c_i32, _c_i32, _c_f64, _c_u64, _c_u64,
+                                  _c_p, _c_p, _c_p, _c_p],
+    "moe_linear_fwd_workspace_size": [ctypes.POINTER(_LinearFwdArgs),
+                                      ctypes.POINTER(_c_sz)],
+    "moe_linear_fwd": [_c_p, ctypes.POINTER(_LinearFwdArgs), _c_p],
+    "moe_linear_bwd_workspace_size": [ctypes.POINTER(_LinearBwdArgs),
+                                      ctypes.POINTER(_c_sz)],
+    "moe_linear_bwd": [_c_p, ctypes.POINTER(_LinearBwdArgs), _c_p],
     "moe_router_logits": [_c_p, _c_p, _c_p, _c_p, _c_i64, _c_i32, _c_i32,
                           _c_p, _c_p],
     "moe_fp8_tensor_quantize_workspace_size": [_c_i64, ctypes.POINTER(_c_sz)],
@@ -193,6 +253,40 @@ def _need(t: torch.Tensor, dtype, shape, name: str) -> None:
         raise ValueError(f"{name}: must be a device tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
+
+
+def _need_on(dev: torch.device, t: Optional[torch.Tensor], dtype, shape,
+             name: str) -> None:
+    """_need for an optional tensor that must be on ``dev``."""
+    if t is None:
+        return
+    _need(t, dtype, shape, name)
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, expected {dev}")
+
+
+def _out_or_new(out: Optional[torch.Tensor], shape, dtype,
+                dev: torch.device) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need_on(dev, out, dtype, shape, "out")
+    return out
+
+
+def _u64(v: int, name: str) -> int:
+    v = int(v)
+    if not 0 <= v < 1 << 64:
+        raise ValueError(f"{name}: {v} is not an unsigned 64-bit number")
+    return v
+
+
+def _workspace(ws: Optional[torch.Tensor], need: int, dev: torch.device
+               ) -> Optional[torch.Tensor]:
+    """The caller's workspace if it is large enough, else a new one."""
+    if ws is not None and ws.device == dev and ws.is_contiguous() and \
+            ws.dtype == torch.uint8 and ws.numel() >= need:
+        return ws
+    return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
 
 
 def check_device_status(device=None) -> int:
@@ -326,6 +420,88 @@ def moe_router_bwd(logits: torch.Tensor, topk_idx: torch.Tensor,
     return res
 
 
+def _route_opts(score: int, n_group: int, topk_group: int, group_score: int,
+                renormalize: bool, scale: float) -> _RouteOpts:
+    return _RouteOpts(int(score), int(n_group), int(topk_group),
+                      int(group_score), int(bool(renormalize)), float(scale))
+
+
+def moe_route_scored(logits: torch.Tensor, k: int,
+                     bias: Optional[torch.Tensor] = None,
+                     score: int = SCORE_SOFTMAX, n_group: int = 1,
+                     topk_group: int = 1, group_score: int = GROUP_MAX,
+                     renormalize: bool = True, scale: float = 1.0
+                     ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Router top-k by softmax or sigmoid scores plus an optional balance
+    bias (float32 [E], selection only), among the topk_group best of n_group
+    expert groups: logits float32 [T, E] -> (topk_idx int32 [T, k], topk_w
+    float32 [T, k])."""
+    T, E = logits.shape
+    dev = logits.device
+    _need(logits, torch.float32, (T, E), "logits")
+    _need_on(dev, bias, torch.float32, (E,), "bias")
+    if k < 1:
+        raise ValueError("k must be positive")
+    idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+    w = torch.empty((T, k), dtype=torch.float32, device=dev)
+    o = _route_opts(score, n_group, topk_group, group_score, renormalize,
+                    scale)
+    _check(load_library().moe_route_scored(
+        _context(dev), _ptr(logits), _ptr(bias), T, E, k, ctypes.byref(o),
+        _ptr(idx), _ptr(w), _stream()))
+    return idx, w
+
+
+def moe_route_scored_bwd(logits: torch.Tensor, topk_idx: torch.Tensor,
+                         dtopk_w: torch.Tensor, score: int = SCORE_SOFTMAX,
+                         renormalize: bool = True, scale: float = 1.0
+                         ) -> torch.Tensor:
+    """Gradient of the logits (float32 [T, E]) from the gradient of
+    moe_route_scored's weights (float32 [T, k])."""
+    T, E = logits.shape
+    k = topk_idx.shape[1]
+    dev = logits.device
+    _need(logits, torch.float32, (T, E), "logits")
+    _need_on(dev, topk_idx, torch.int32, (T, k), "topk_idx")
+    _need_on(dev, dtopk_w, torch.float32, (T, k), "dtopk_w")
+    dl = torch.empty((T, E), dtype=torch.float32, device=dev)
+    o = _route_opts(score, 1, 1, GROUP_MAX, renormalize, scale)
+    _check(load_library().moe_route_scored_bwd(
+        _context(dev), _ptr(logits), _ptr(topk_idx), _ptr(dtopk_w), T, E, k,
+        ctypes.byref(o), _ptr(dl), _stream()))
+    return dl
+
+
+def moe_router_proj_bwd(dlogits: torch.Tensor, x: torch.Tensor,
+                        w_r: torch.Tensor, want_dw: bool = True,
+                        want_dx: bool = True) -> Dict[str, torch.Tensor]:
+    """Gradients of the router projection from dlogits float32 [T, E]:
+    "dw_r" [E, H] and "dx" [T, H], float32."""
+    T, E = dlogits.shape
+    H = x.shape[1]
+    dev = dlogits.device
+    _need(dlogits, torch.float32, (T, E), "dlogits")
+    _need_on(dev, x, torch.bfloat16, (T, H), "x")
+    _need_on(dev, w_r, torch.bfloat16, (E, H), "w_r")
+    dw = torch.empty((E, H), dtype=torch.float32, device=dev) \
+        if want_dw else None
+    dx = torch.empty((T, H), dtype=torch.float32, device=dev) \
+        if want_dx else None
+    lib = load_library()
+    n = _c_sz(0)
+    _check(lib.moe_router_bwd_workspace_size(T, H, E, ctypes.byref(n)))
+    ws = torch.empty(max(int(n.value), 256), dtype=torch.uint8, device=dev)
+    _check(lib.moe_router_proj_bwd(_context(dev), _ptr(dlogits), _ptr(x),
+                                   _ptr(w_r), T, H, E, _ptr(dw), _ptr(dx),
+                                   _ptr(ws), ws.numel(), _stream()))
+    res = {}
+    if want_dw:
+        res["dw_r"] = dw
+    if want_dx:
+        res["dx"] = dx
+    return res
+
+
 def moe_permute(x: torch.Tensor, topk_idx: torch.Tensor, E: int,
                 topk_w: Optional[torch.Tensor] = None,
                 precision: int = PREC_BF16) -> Dict[str, torch.Tensor]:
@@ -435,6 +611,152 @@ def moe_unpermute(z_perm: torch.Tensor, row_map: torch.Tensor, k: int,
                              _ptr(row_map), _ptr(topk_w), T, H, k, _ptr(y),
                              _stream()))
     return y
+
+
+def moe_unpermute_dropout(z_perm: torch.Tensor,
+                          row_map: Optional[torch.Tensor], k: int, p: float,
+                          seed: int, offset: int = 0,
+                          step: Optional[torch.Tensor] = None,
+                          topk_w: Optional[torch.Tensor] = None,
+                          residual: Optional[torch.Tensor] = None,
+                          out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y[t] = residual[t] + dropout(sum_j c_j z_perm[row_map[t*k+j]]) with
+    the mask of (seed, offset + step); row_map None (k = 1): rows in token
+    order.  step: int64 tensor of one element on the device, or None.  out
+    may be the residual."""
+    if k < 1:
+        raise ValueError("k must be positive")
+    rows, H = z_perm.shape
+    if rows % k:
+        raise ValueError("z_perm must hold k rows per token")
+    T = rows // k
+    dev = z_perm.device
+    _need(z_perm, torch.bfloat16, (rows, H), "z_perm")
+    _need_on(dev, row_map, torch.int32, (rows,), "row_map")
+    _need_on(dev, topk_w, torch.float32, (T, k), "topk_w")
+    _need_on(dev, residual, torch.bfloat16, (T, H), "residual")
+    _need_on(dev, step, torch.int64, (1,), "step")
+    y = _out_or_new(out, (T, H), torch.bfloat16, dev)
+    _check(load_library().moe_unpermute_dropout(
+        _context(dev), _ptr(z_perm), _ptr(row_map), _ptr(topk_w),
+        _ptr(residual), T, H, k, float(p), _u64(seed, "seed"),
+        _u64(offset, "offset"), _ptr(step), _ptr(y), _stream()))
+    return y
+
+
+def moe_unpermute_dropout_bwd(dy: torch.Tensor,
+                              row_map: Optional[torch.Tensor], k: int,
+                              p: float, seed: int, offset: int = 0,
+                              step: Optional[torch.Tensor] = None,
+                              topk_w: Optional[torch.Tensor] = None,
+                              z_perm: Optional[torch.Tensor] = None,
+                              out: Optional[torch.Tensor] = None
+                              ) -> Dict[str, torch.Tensor]:
+    """Backward of moe_unpermute_dropout with the same p, seed, offset and
+    step: {"dz": bf16 [T*k, H]} (rows that row_map does not name keep what
+    ``out`` held) and, with z_perm, "dtopk_w" float32 [T, k]."""
+    if k < 1:
+        raise ValueError("k must be positive")
+    T, H = dy.shape
+    dev = dy.device
+    _need(dy, torch.bfloat16, (T, H), "dy")
+    _need_on(dev, row_map, torch.int32, (T * k,), "row_map")
+    _need_on(dev, topk_w, torch.float32, (T, k), "topk_w")
+    _need_on(dev, z_perm, torch.bfloat16, (T * k, H), "z_perm")
+    _need_on(dev, step, torch.int64, (1,), "step")
+    dz = _out_or_new(out, (T * k, H), torch.bfloat16, dev)
+    dw = torch.empty((T, k), dtype=torch.float32, device=dev) \
+        if z_perm is not None else None
+    _check(load_library().moe_unpermute_dropout_bwd(
+        _context(dev), _ptr(dy), _ptr(row_map), _ptr(topk_w), _ptr(z_perm),
+        T, H, k, float(p), _u64(seed, "seed"), _u64(offset, "offset"),
+        _ptr(step), _ptr(dz), _ptr(dw), _stream()))
+    res = {"dz": dz}
+    if dw is not None:
+        res["dtopk_w"] = dw
+    return res
+
+
+def moe_linear_fwd(x: torch.Tensor, w: torch.Tensor,
+                   bias: Optional[torch.Tensor] = None, act: int = ACT_NONE,
+                   residual: Optional[torch.Tensor] = None,
+                   save: bool = False, out: Optional[torch.Tensor] = None,
+                   ws: Optional[torch.Tensor] = None
+                   ) -> Dict[str, torch.Tensor]:
+    """y = act(x w^T + bias) + residual: x bf16 [M, K], w bf16 [N, K], bias
+    float32 [N], residual bf16 [M, N] -> {"y": bf16 [M, N]} (+ "z", the
+    value before the activation, when save=True).  out may be the
+    residual."""
+    M, K = x.shape
+    N = w.shape[0]
+    dev = x.device
+    _need(x, torch.bfloat16, (M, K), "x")
+    _need_on(dev, w, torch.bfloat16, (N, K), "w")
+    _need_on(dev, bias, torch.float32, (N,), "bias")
+    _need_on(dev, residual, torch.bfloat16, (M, N), "residual")
+    y = _out_or_new(out, (M, N), torch.bfloat16, dev)
+    z = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if save else None
+    a = _LinearFwdArgs()
+    a.M, a.N, a.K, a.act = M, N, K, int(act)
+    a.x, a.w, a.bias, a.residual = _ptr(x), _ptr(w), _ptr(bias), \
+        _ptr(residual)
+    a.y, a.z_save = _ptr(y), _ptr(z)
+    lib = load_library()
+    n = _c_sz(0)
+    _check(lib.moe_linear_fwd_workspace_size(ctypes.byref(a),
+                                             ctypes.byref(n)))
+    ws = _workspace(ws, int(n.value), dev)
+    a.ws, a.ws_bytes = _ptr(ws), 0 if ws is None else ws.numel()
+    _check(lib.moe_linear_fwd(_context(dev), ctypes.byref(a), _stream()))
+    return {"y": y, "z": z} if save else {"y": y}
+
+
+def moe_linear_bwd(dy: torch.Tensor, x: Optional[torch.Tensor],
+                   w: Optional[torch.Tensor], act: int = ACT_NONE,
+                   z: Optional[torch.Tensor] = None, want_dx: bool = True,
+                   want_dw: bool = True, want_db: bool = False,
+                   ws: Optional[torch.Tensor] = None
+                   ) -> Dict[str, torch.Tensor]:
+    """Gradients of moe_linear_fwd: {"dx" bf16 [M, K], "dw" bf16 [N, K],
+    "db" float32 [N]} as asked for.  z: the forward's saved value before the
+    activation (not needed for ACT_NONE); x may be None without dw, w
+    without dx."""
+    M, N = dy.shape
+    dev = dy.device
+    if (want_dw and x is None) or (want_dx and w is None):
+        raise ValueError("dw needs x, dx needs w")
+    ref = x if x is not None else w
+    if ref is None and not want_db:
+        raise ValueError("no gradient asked for")
+    K = ref.shape[1] if ref is not None else 8
+    _need(dy, torch.bfloat16, (M, N), "dy")
+    _need_on(dev, x, torch.bfloat16, (M, K), "x")
+    _need_on(dev, w, torch.bfloat16, (N, K), "w")
+    _need_on(dev, z, torch.bfloat16, (M, N), "z")
+    dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev) \
+        if want_dx else None
+    dw = torch.empty((N, K), dtype=torch.bfloat16, device=dev) \
+        if want_dw else None
+    db = torch.empty(N, dtype=torch.float32, device=dev) if want_db else None
+    a = _LinearBwdArgs()
+    a.M, a.N, a.K, a.act = M, N, K, int(act)
+    a.dy, a.x, a.w, a.z = _ptr(dy), _ptr(x), _ptr(w), _ptr(z)
+    a.dx, a.dw, a.db = _ptr(dx), _ptr(dw), _ptr(db)
+    lib = load_library()
+    n = _c_sz(0)
+    _check(lib.moe_linear_bwd_workspace_size(ctypes.byref(a),
+                                             ctypes.byref(n)))
+    ws = _workspace(ws, int(n.value), dev)
+    a.ws, a.ws_bytes = _ptr(ws), 0 if ws is None else ws.numel()
+    _check(lib.moe_linear_bwd(_context(dev), ctypes.byref(a), _stream()))
+    res = {}
+    if want_dx:
+        res["dx"] = dx
+    if want_dw:
+        res["dw"] = dw
+    if want_db:
+        res["db"] = db
+    return res
 
 
 def moe_unpermute_probs_grad(dw_perm: torch.Tensor, row_map: torch.Tensor,

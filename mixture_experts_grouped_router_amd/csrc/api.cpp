@@ -3,6 +3,7 @@
 #include <vector>
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -322,6 +323,41 @@ moe_status_t moe_router_bwd(moe_ctx_t ctx, const float* logits,
                     "router_bwd launch");
 }
 
+moe_status_t moe_router_proj_bwd(moe_ctx_t ctx, const float* dlogits,
+                                 const void* x, const void* w_r, int64_t T,
+                                 int32_t H, int32_t E, float* dw_r, float* dx,
+                                 void* ws, size_t ws_bytes, void* stream) {
+  MOE_REQUIRE(T >= 0 && H >= 1 && E >= 1, MOE_ERR_INVALID_ARG, "bad sizes");
+  MOE_REQUIRE(E <= MOE_MAX_EXPERTS, MOE_ERR_UNSUPPORTED, "E <= %d required",
+              MOE_MAX_EXPERTS);
+  // the token tiles of the dx product are the grid's y dimension
+  MOE_REQUIRE((T + 63) / 64 <= 65535 || dx == nullptr, MOE_ERR_UNSUPPORTED,
+              "T too large");
+  MOE_REQUIRE(T < ((int64_t)1 << 62) / (H > E ? H : E), MOE_ERR_UNSUPPORTED,
+              "T too large");
+  const size_t need = moe::router_bwd_ws_bytes(T, H, E);
+  MOE_REQUIRE(T == 0 || (dlogits && (!dw_r || x) && (!dx || w_r)),
+              MOE_ERR_INVALID_ARG, "null tensor pointer");
+  MOE_REQUIRE(T == 0 || dw_r == nullptr || need == 0 ||
+                  (ws && ws_bytes >= need),
+              MOE_ERR_WORKSPACE, "router_proj_bwd workspace needs %zu bytes",
+              need);
+  const moe_status_t s = check_ctx(ctx);
+  if (s != MOE_OK) return s;
+  TimerGuard tg(ctx);
+  if (T == 0) {   // an empty sum
+    if (dw_r == nullptr) return ok();
+    return hip_status(moe::launch_zero_u32(reinterpret_cast<uint32_t*>(dw_r),
+                                           (int64_t)E * H, as_stream(stream),
+                                           "router_dw_zero"),
+                      "router_proj_bwd zero");
+  }
+  return hip_status(moe::launch_router_proj_bwd(dlogits, x, w_r, T, H, E,
+                                                dw_r, dx, ws,
+                                                as_stream(stream)),
+                    "router_proj_bwd launch");
+}
+
 moe_status_t moe_route_topk(moe_ctx_t ctx, const float* logits, int64_t T,
                             int32_t E, int32_t k, int32_t renormalize,
                             int32_t* topk_idx, float* topk_w, void* stream) {
@@ -341,6 +377,92 @@ moe_status_t moe_route_topk(moe_ctx_t ctx, const float* logits, int64_t T,
                                            topk_idx, topk_w, ctx->status,
                                            as_stream(stream)),
                     "route_topk launch");
+}
+
+namespace {
+
+moe_status_t check_route(int64_t T, int32_t E, int32_t k,
+                         const moe_route_opts* o, moe::RouteOpts* out) {
+  MOE_REQUIRE(o != nullptr, MOE_ERR_INVALID_ARG, "null options");
+  MOE_REQUIRE(T >= 0, MOE_ERR_INVALID_ARG, "T < 0");
+  MOE_REQUIRE(E >= 1 && k >= 1 && k <= E, MOE_ERR_INVALID_ARG,
+              "need 1 <= k <= E (k=%d, E=%d)", k, E);
+  MOE_REQUIRE(E <= MOE_MAX_EXPERTS && k <= MOE_MAX_TOPK, MOE_ERR_UNSUPPORTED,
+              "E <= %d and k <= %d required", MOE_MAX_EXPERTS, MOE_MAX_TOPK);
+  MOE_REQUIRE(T <= (int64_t)INT32_MAX / 64, MOE_ERR_UNSUPPORTED, "T too large");
+  MOE_REQUIRE(o->score == MOE_SCORE_SOFTMAX || o->score == MOE_SCORE_SIGMOID,
+              MOE_ERR_INVALID_ARG, "bad score function");
+  MOE_REQUIRE(o->group_score == MOE_GROUP_MAX ||
+                  o->group_score == MOE_GROUP_TOP2,
+              MOE_ERR_INVALID_ARG, "bad group score");
+  MOE_REQUIRE(o->n_group >= 1 && o->topk_group >= 1 &&
+                  o->topk_group <= o->n_group && E % o->n_group == 0,
+              MOE_ERR_INVALID_ARG,
+              "need 1 <= topk_group <= n_group and E %% n_group == 0 "
+              "(n_group=%d, topk_group=%d, E=%d)",
+              o->n_group, o->topk_group, E);
+  MOE_REQUIRE(o->n_group <= MOE_MAX_ROUTE_GROUPS, MOE_ERR_UNSUPPORTED,
+              "n_group <= %d required", MOE_MAX_ROUTE_GROUPS);
+  MOE_REQUIRE((int64_t)o->topk_group * (E / o->n_group) >= k,
+              MOE_ERR_INVALID_ARG,
+              "the kept groups hold %d experts, fewer than k = %d",
+              o->topk_group * (E / o->n_group), k);
+  MOE_REQUIRE(o->n_group == 1 || o->group_score == MOE_GROUP_MAX ||
+                  E / o->n_group >= 2,
+              MOE_ERR_INVALID_ARG,
+              "MOE_GROUP_TOP2 needs two experts per group");
+  MOE_REQUIRE(std::isfinite(o->scale), MOE_ERR_INVALID_ARG,
+              "scale must be finite");
+  out->score = o->score == MOE_SCORE_SIGMOID;
+  out->n_group = o->n_group;
+  out->topk_group = o->topk_group;
+  out->group_score = o->group_score == MOE_GROUP_TOP2;
+  out->renormalize = o->renormalize != 0;
+  out->scale = (double)o->scale;
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status_t moe_route_scored(moe_ctx_t ctx, const float* logits,
+                              const float* bias, int64_t T, int32_t E,
+                              int32_t k, const moe_route_opts* opts,
+                              int32_t* topk_idx, float* topk_w,
+                              void* stream) {
+  moe::RouteOpts o;
+  moe_status_t s = check_route(T, E, k, opts, &o);
+  if (s != MOE_OK) return s;
+  MOE_REQUIRE(T == 0 || (logits && topk_idx && topk_w), MOE_ERR_INVALID_ARG,
+              "null tensor pointer");
+  s = check_ctx(ctx);
+  if (s != MOE_OK) return s;
+  TimerGuard tg(ctx);
+  if (T == 0) return ok();
+  return hip_status(moe::launch_route_scored(logits, bias, T, E, k, o,
+                                             topk_idx, topk_w, ctx->status,
+                                             as_stream(stream)),
+                    "route_scored launch");
+}
+
+moe_status_t moe_route_scored_bwd(moe_ctx_t ctx, const float* logits,
+                                  const int32_t* topk_idx,
+                                  const float* dtopk_w, int64_t T, int32_t E,
+                                  int32_t k, const moe_route_opts* opts,
+                                  float* dlogits, void* stream) {
+  moe::RouteOpts o;
+  moe_status_t s = check_route(T, E, k, opts, &o);
+  if (s != MOE_OK) return s;
+  MOE_REQUIRE(T == 0 || (logits && topk_idx && dtopk_w && dlogits), MOE_ERR_INVALID_ARG,
+              "null tensor pointer");
+  s = check_ctx(ctx);
+  if (s != MOE_OK) return s;
+  TimerGuard tg(ctx);
+  if (T == 0) return ok();
+  return hip_status(moe::launch_route_scored_bwd(logits, topk_idx, dtopk_w, T,
+                                                 E, k, o, dlogits,
+                                                 ctx->status,
+                                                 as_stream(stream)),
+                    "route_scored_bwd launch");
 }
 
 moe_status_t moe_permute_workspace_size(int64_t T, int32_t E, int32_t k,
@@ -503,6 +625,83 @@ moe_status_t moe_unpermute_probs_grad(moe_ctx_t ctx, const float* dw_perm,
   return hip_status(moe::launch_probs_grad(dw_perm, row_map, T, k, dprobs,
                                            as_stream(stream)),
                     "probs grad");
+}
+
+namespace {
+
+moe_status_t check_dropout(const int32_t* row_map, int64_t T, int32_t H,
+                           int32_t k, double p) {
+  MOE_REQUIRE(T >= 0 && H >= 1 && k >= 1, MOE_ERR_INVALID_ARG, "bad sizes");
+  MOE_REQUIRE(p >= 0.0 && p <= 1.0, MOE_ERR_INVALID_ARG,
+              "need 0 <= p <= 1 (p=%g)", p);
+  MOE_REQUIRE(row_map != nullptr || k == 1 || T == 0, MOE_ERR_INVALID_ARG,
+              "k > 1 needs a row_map");
+  MOE_REQUIRE(k <= MOE_MAX_TOPK, MOE_ERR_UNSUPPORTED, "k <= %d required",
+              MOE_MAX_TOPK);
+  MOE_REQUIRE(H % 8 == 0, MOE_ERR_UNSUPPORTED, "H %% 8 != 0");
+  MOE_REQUIRE(T <= (int64_t)INT32_MAX / k, MOE_ERR_UNSUPPORTED,
+              "T*k must fit in int32");
+  // a launch holds fewer than 2^32 threads, up to 256 of them per token
+  MOE_REQUIRE(T < ((int64_t)1 << 32) / (H >= 1024 ? 256 : H / 8 * 2),
+              MOE_ERR_UNSUPPORTED, "T too large");
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status_t moe_unpermute_dropout(moe_ctx_t ctx, const void* z_perm,
+                                   const int32_t* row_map,
+                                   const float* topk_w, const void* residual,
+                                   int64_t T, int32_t H, int32_t k, double p,
+                                   uint64_t seed, uint64_t offset,
+                                   const uint64_t* step, void* y,
+                                   void* stream) {
+  moe_status_t s = check_dropout(row_map, T, H, k, p);
+  if (s != MOE_OK) return s;
+  MOE_REQUIRE(T == 0 || (z_perm && y), MOE_ERR_INVALID_ARG, "null pointer");
+  MOE_REQUIRE(aligned16(z_perm) && aligned16(y) && aligned16(residual),
+              MOE_ERR_UNSUPPORTED,
+              "z_perm / residual / y must be 16-byte aligned");
+  MOE_REQUIRE((reinterpret_cast<uintptr_t>(step) & 7u) == 0,
+              MOE_ERR_UNSUPPORTED, "step must be 8-byte aligned");
+  s = check_ctx(ctx);
+  if (s != MOE_OK) return s;
+  TimerGuard tg(ctx);
+  if (T == 0) return ok();
+  return hip_status(
+      moe::launch_unpermute_dropout(z_perm, row_map, topk_w, residual, T, H,
+                                    k, moe::drop_args(p, seed, offset, step),
+                                    y, as_stream(stream)),
+      "unpermute_dropout");
+}
+
+moe_status_t moe_unpermute_dropout_bwd(moe_ctx_t ctx, const void* dy,
+                                       const int32_t* row_map,
+                                       const float* topk_w,
+                                       const void* z_perm, int64_t T,
+                                       int32_t H, int32_t k, double p,
+                                       uint64_t seed, uint64_t offset,
+                                       const uint64_t* step, void* dz_perm,
+                                       float* dtopk_w, void* stream) {
+  moe_status_t s = check_dropout(row_map, T, H, k, p);
+  if (s != MOE_OK) return s;
+  MOE_REQUIRE(T == 0 || (dy && dz_perm), MOE_ERR_INVALID_ARG, "null pointer");
+  MOE_REQUIRE(T == 0 || dtopk_w == nullptr || z_perm != nullptr, MOE_ERR_INVALID_ARG,
+              "dtopk_w needs z_perm");
+  MOE_REQUIRE(aligned16(dy) && aligned16(dz_perm) && aligned16(z_perm),
+              MOE_ERR_UNSUPPORTED,
+              "dy / z_perm / dz_perm must be 16-byte aligned");
+  MOE_REQUIRE((reinterpret_cast<uintptr_t>(step) & 7u) == 0,
+              MOE_ERR_UNSUPPORTED, "step must be 8-byte aligned");
+  s = check_ctx(ctx);
+  if (s != MOE_OK) return s;
+  TimerGuard tg(ctx);
+  if (T == 0) return ok();
+  return hip_status(moe::launch_unpermute_dropout_bwd(
+                        dy, row_map, topk_w, z_perm, T, H, k,
+                        moe::drop_args(p, seed, offset, step), dz_perm,
+                        dtopk_w, as_stream(stream)),
+                    "unpermute_dropout_bwd");
 }
 
 moe_status_t mxfp8_quantize(moe_ctx_t ctx, const void* src, int64_t batch,
@@ -823,6 +1022,101 @@ moe_status_t moe_grouped_mlp_bwd(moe_ctx_t ctx, const moe_mlp_bwd_args* a,
                                a->w_dn_st, a->ws, ctx->status,
                                as_stream(stream));
   return hip_status(e, "grouped_mlp_bwd");
+}
+
+namespace {
+
+moe_status_t check_linear(int64_t M, int32_t N, int32_t K,
+                          moe_activation_t act) {
+  MOE_REQUIRE(M >= 0 && N >= 1 && K >= 1, MOE_ERR_INVALID_ARG,
+              "bad sizes (M=%lld N=%d K=%d)", (long long)M, N, K);
+  MOE_REQUIRE(act >= MOE_ACT_NONE && act <= MOE_ACT_SILU, MOE_ERR_INVALID_ARG,
+              "bad activation");
+  MOE_REQUIRE(K % 8 == 0, MOE_ERR_UNSUPPORTED, "K %% 8 != 0");
+  MOE_REQUIRE(N <= (1 << 22) && K <= (1 << 22), MOE_ERR_UNSUPPORTED,
+              "N and K up to 2^22");
+  // a launch holds fewer than 2^32 threads
+  const int64_t wide = (N > K ? N : K) + (int64_t)256;
+  MOE_REQUIRE(M <= ((int64_t)1 << 36) / wide &&
+                  (int64_t)N * K <= (int64_t)1 << 36,
+              MOE_ERR_UNSUPPORTED, "tensor too large");
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status_t moe_linear_fwd_workspace_size(const moe_linear_fwd_args* a,
+                                           size_t* bytes) {
+  MOE_REQUIRE(a && bytes, MOE_ERR_INVALID_ARG, "null pointer");
+  moe_status_t s = check_linear(a->M, a->N, a->K, a->act);
+  if (s != MOE_OK) return s;
+  *bytes = moe::linear_fwd_ws_bytes(a->M, a->N, a->K);
+  return ok();
+}
+
+moe_status_t moe_linear_fwd(moe_ctx_t ctx, const moe_linear_fwd_args* a,
+                            void* stream) {
+  size_t need = 0;
+  moe_status_t s = moe_linear_fwd_workspace_size(a, &need);
+  if (s != MOE_OK) return s;
+  MOE_REQUIRE(a->M == 0 || (a->x && a->w && a->y), MOE_ERR_INVALID_ARG, "null pointer");
+  MOE_REQUIRE(aligned16(a->x) && aligned16(a->w) && aligned16(a->y) &&
+                  aligned16(a->residual) && aligned16(a->z_save),
+              MOE_ERR_UNSUPPORTED, "operands must be 16-byte aligned");
+  MOE_REQUIRE(need == 0 || (a->ws && a->ws_bytes >= need), MOE_ERR_WORKSPACE,
+              "linear_fwd workspace needs %zu bytes", need);
+  MOE_REQUIRE(need == 0 || aligned16(a->ws), MOE_ERR_UNSUPPORTED,
+              "the workspace must be 16-byte aligned");
+  s = check_ctx(ctx);
+  if (s != MOE_OK) return s;
+  TimerGuard tg(ctx);
+  if (a->M == 0) return ok();
+  return hip_status(
+      moe::launch_linear_fwd(a->M, a->N, a->K, (int)a->act, a->x, a->w,
+                             a->bias, a->residual, a->y, a->z_save, a->ws,
+                             as_stream(stream)),
+      "linear_fwd");
+}
+
+moe_status_t moe_linear_bwd_workspace_size(const moe_linear_bwd_args* a,
+                                           size_t* bytes) {
+  MOE_REQUIRE(a && bytes, MOE_ERR_INVALID_ARG, "null pointer");
+  moe_status_t s = check_linear(a->M, a->N, a->K, a->act);
+  if (s != MOE_OK) return s;
+  *bytes = moe::linear_bwd_ws_bytes(a->M, a->N, a->K, (int)a->act,
+                                    a->dx != nullptr, a->dw != nullptr,
+                                    a->db != nullptr);
+  return ok();
+}
+
+moe_status_t moe_linear_bwd(moe_ctx_t ctx, const moe_linear_bwd_args* a,
+                            void* stream) {
+  size_t need = 0;
+  moe_status_t s = moe_linear_bwd_workspace_size(a, &need);
+  if (s != MOE_OK) return s;
+  MOE_REQUIRE(aligned16(a->dy) && aligned16(a->x) && aligned16(a->w) &&
+                  aligned16(a->z) && aligned16(a->dx) && aligned16(a->dw),
+              MOE_ERR_UNSUPPORTED, "operands must be 16-byte aligned");
+  if (a->M > 0) {
+    MOE_REQUIRE(a->dy != nullptr, MOE_ERR_INVALID_ARG, "null dy");
+    MOE_REQUIRE((!a->dx || a->w) && (!a->dw || a->x), MOE_ERR_INVALID_ARG,
+                "dx needs w, dw needs x");
+    MOE_REQUIRE(a->act == MOE_ACT_NONE || a->z, MOE_ERR_INVALID_ARG,
+                "the activation's backward needs the saved z");
+    MOE_REQUIRE(need == 0 || (a->ws && a->ws_bytes >= need),
+                MOE_ERR_WORKSPACE, "linear_bwd workspace needs %zu bytes",
+                need);
+    MOE_REQUIRE(need == 0 || aligned16(a->ws), MOE_ERR_UNSUPPORTED,
+                "the workspace must be 16-byte aligned");
+  }
+  s = check_ctx(ctx);
+  if (s != MOE_OK) return s;
+  TimerGuard tg(ctx);
+  return hip_status(
+      moe::launch_linear_bwd(a->M, a->N, a->K, (int)a->act, a->dy, a->x,
+                             a->w, a->z, a->dx, a->dw, a->db, a->ws,
+                             as_stream(stream)),
+      "linear_bwd");
 }
 
 }  // extern "C"

@@ -16,9 +16,11 @@
 namespace moe {
 namespace {
 
-__global__ __launch_bounds__(256) void zero_u32_kernel(uint32_t* p, int n) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i < n) p[i] = 0u;
+__global__ __launch_bounds__(256) void zero_u32_kernel(uint32_t* p,
+                                                       int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n;
+       i += (int64_t)gridDim.x * 256)
+    p[i] = 0u;
 }
 
 // amax (as float32 bits of a non-negative value) of each segment; blocks
@@ -91,11 +93,14 @@ unsigned blocks_per_seg(int64_t seg_elems, int n_seg) {
 
 }  // namespace
 
-hipError_t launch_zero_u32(uint32_t* p, int n, hipStream_t stream) {
+hipError_t launch_zero_u32(uint32_t* p, int64_t n, hipStream_t stream,
+                           const char* name) {
   if (n <= 0) return hipSuccess;
-  KernelScope ks("fp8_amax_clear", stream);
-  hipLaunchKernelGGL(zero_u32_kernel, dim3((n + 255) / 256), dim3(256), 0,
-                     stream, p, n);
+  KernelScope ks(name, stream);
+  const int64_t blocks = (n + 255) / 256;
+  hipLaunchKernelGGL(zero_u32_kernel,
+                     dim3((unsigned)(blocks < 65536 ? blocks : 65536)),
+                     dim3(256), 0, stream, p, n);
   return hipGetLastError();
 }
 

@@ -11,6 +11,24 @@ hipError_t launch_route_topk(const float* logits, int64_t T, int E, int k,
                              int renorm, int32_t* idx, float* w,
                              int32_t* status, hipStream_t stream);
 
+// scored router top-k (route_scored.hip)
+struct RouteOpts {
+  int score;         // 0 softmax, 1 sigmoid
+  int n_group, topk_group;
+  int group_score;   // 0 largest, 1 sum of the two largest
+  int renormalize;
+  double scale;
+};
+hipError_t launch_route_scored(const float* logits, const float* bias,
+                               int64_t T, int E, int k, const RouteOpts& o,
+                               int32_t* idx, float* w, int32_t* status,
+                               hipStream_t stream);
+hipError_t launch_route_scored_bwd(const float* logits,
+                                   const int32_t* topk_idx,
+                                   const float* dtopk_w, int64_t T, int E,
+                                   int k, const RouteOpts& o, float* dlogits,
+                                   int32_t* status, hipStream_t stream);
+
 // permutation
 size_t permute_ws_bytes(int64_t T, int E, int k);
 // the static scratch of moe_permute_noalloc: its size, and its device address
@@ -33,6 +51,41 @@ hipError_t launch_unpermute(const void* z, const int32_t* row_map,
                             void* y, hipStream_t stream);
 hipError_t launch_probs_grad(const float* dw_perm, const int32_t* row_map,
                              int64_t T, int k, float* dprobs,
+                             hipStream_t stream);
+
+// combine with dropout and residual (dropout.hip): a value is dropped where
+// its 16 random bits are below thr, the others are scaled
+struct DropArgs {
+  uint32_t thr;
+  float scale;
+  uint64_t seed, offset;
+  const uint64_t* step;   // nullable device word added to offset
+};
+DropArgs drop_args(double p, uint64_t seed, uint64_t offset,
+                   const uint64_t* step);
+hipError_t launch_unpermute_dropout(const void* z, const int32_t* row_map,
+                                    const float* topk_w, const void* residual,
+                                    int64_t T, int H, int k,
+                                    const DropArgs& d, void* y,
+                                    hipStream_t stream);
+hipError_t launch_unpermute_dropout_bwd(const void* dy,
+                                        const int32_t* row_map,
+                                        const float* topk_w, const void* z,
+                                        int64_t T, int H, int k,
+                                        const DropArgs& d, void* dz,
+                                        float* dtopk_w, hipStream_t stream);
+
+// dense linear layer (linear.hip); act: moe_activation_t
+size_t linear_fwd_ws_bytes(int64_t M, int N, int K);
+hipError_t launch_linear_fwd(int64_t M, int N, int K, int act, const void* x,
+                             const void* w, const float* bias,
+                             const void* residual, void* y, void* z_save,
+                             void* ws, hipStream_t stream);
+size_t linear_bwd_ws_bytes(int64_t M, int N, int K, int act, bool want_dx,
+                           bool want_dw, bool want_db);
+hipError_t launch_linear_bwd(int64_t M, int N, int K, int act, const void* dy,
+                             const void* x, const void* w, const void* z,
+                             void* dx, void* dw, float* db, void* ws,
                              hipStream_t stream);
 
 // MXFP8 quantisation.  tiled: scales in the GEMM layout (mx_tile_off;
@@ -83,7 +136,8 @@ hipError_t launch_mlp_fwd_bf16(int E, int H, int F, int64_t rows,
                                int cu_count, int32_t* status,
                                hipStream_t stream);
 // tensor-scaled FP8
-hipError_t launch_zero_u32(uint32_t* p, int n, hipStream_t stream);
+hipError_t launch_zero_u32(uint32_t* p, int64_t n, hipStream_t stream,
+                           const char* name = "fp8_amax_clear");
 hipError_t launch_seg_amax(const void* src, int64_t seg_elems, int n_seg,
                            uint32_t* amax_bits, hipStream_t stream);
 hipError_t launch_tensor_quant(const void* src, int64_t seg_elems, int n_seg,
@@ -113,6 +167,11 @@ hipError_t launch_router_bwd(const float* logits, const int32_t* topk_idx,
                              const void* w_r, int64_t T, int H, int E, int k,
                              bool renorm, float* dlogits, float* dw_r,
                              float* dx, void* ws, hipStream_t stream);
+// its second half: dW_r and the router's dx from dlogits
+hipError_t launch_router_proj_bwd(const float* dlogits, const void* x,
+                                  const void* w_r, int64_t T, int H, int E,
+                                  float* dw_r, float* dx, void* ws,
+                                  hipStream_t stream);
 
 // per-expert loop (baseline of the grouped path), bf16; offsets_host is
 // the host copy of offsets

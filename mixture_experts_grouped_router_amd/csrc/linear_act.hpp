@@ -1,0 +1,98 @@
+// Activations of the linear layer and their derivatives, float32.
+#pragma once
+#include <hip/hip_runtime.h>
+
+namespace moe {
+namespace lin {
+
+enum Act { ACT_NONE = 0, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU };
+
+// 1 / (1 + e^-x) with the hardware exponential and reciprocal (1 ulp each):
+// the results are rounded to bf16 afterwards
+__device__ __forceinline__ float sigm(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __expf(-x));
+}
+
+// Normal distribution function of x (0.5 erfc(-x / sqrt 2)).
+__device__ __forceinline__ float ndtr(float x) {
+  return 0.5f * erfcf(x * -0.70710678118654752f);
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_fwd(float z) {
+  if constexpr (ACT == ACT_RELU) {
+    return fmaxf(z, 0.0f);
+  } else if constexpr (ACT == ACT_GELU) {
+    return z * ndtr(z);
+  } else if constexpr (ACT == ACT_GELU_TANH) {
+    // 0.5 z (1 + tanh u) = z sigmoid(2 u), 2 u = 2 sqrt(2 / pi) (z + ...)
+    const float u2 = 1.5957691216057308f * (z + 0.044715f * z * z * z);
+    return z * sigm(u2);
+  } else if constexpr (ACT == ACT_SILU) {
+    return z * sigm(z);
+  } else {
+    return z;
+  }
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_grad(float z) {
+  if constexpr (ACT == ACT_RELU) {
+    return z > 0.0f ? 1.0f : 0.0f;
+  } else if constexpr (ACT == ACT_GELU) {
+    return ndtr(z) + z * 0.3989422804014327f * __expf(-0.5f * z * z);
+  } else if constexpr (ACT == ACT_GELU_TANH) {
+    const float u2 = 1.5957691216057308f * (z + 0.044715f * z * z * z);
+    const float du2 = 1.5957691216057308f * (1.0f + 0.134145f * z * z);
+    const float s = sigm(u2);
+    return s + z * s * (1.0f - s) * du2;
+  } else if constexpr (ACT == ACT_SILU) {
+    const float s = sigm(z);
+    return s * (1.0f + z * (1.0f - s));
+  } else {
+    return 1.0f;
+  }
+}
+
+// y = act(z) for 8 values; act is uniform
+__device__ __forceinline__ void act_fwd8(int act, const float (&z)[8],
+                                         float (&y)[8]) {
+#define MOE_ACT_CASE(A)                                 \
+  case A:                                               \
+    _Pragma("unroll") for (int i = 0; i < 8; ++i)       \
+        y[i] = act_fwd<A>(z[i]);                        \
+    break;
+  switch (act) {
+    MOE_ACT_CASE(ACT_RELU)
+    MOE_ACT_CASE(ACT_GELU)
+    MOE_ACT_CASE(ACT_GELU_TANH)
+    MOE_ACT_CASE(ACT_SILU)
+    default:
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = z[i];
+  }
+#undef MOE_ACT_CASE
+}
+
+// d = act'(z) for 8 values
+__device__ __forceinline__ void act_grad8(int act, const float (&z)[8],
+                                          float (&d)[8]) {
+#define MOE_ACT_CASE(A)                                 \
+  case A:                                               \
+    _Pragma("unroll") for (int i = 0; i < 8; ++i)       \
+        d[i] = act_grad<A>(z[i]);                       \
+    break;
+  switch (act) {
+    MOE_ACT_CASE(ACT_RELU)
+    MOE_ACT_CASE(ACT_GELU)
+    MOE_ACT_CASE(ACT_GELU_TANH)
+    MOE_ACT_CASE(ACT_SILU)
+    default:
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[i] = 1.0f;
+  }
+#undef MOE_ACT_CASE
+}
+
+}  // namespace lin
+}  // namespace moe

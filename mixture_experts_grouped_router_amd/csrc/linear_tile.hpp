@@ -1,0 +1,505 @@
+// Dense bf16 matrix product C = op(A) op(B) with a fused epilogue, for the
+// linear layer's forward and gradients.
+//
+// C[m, n] = sum_k A(m, k) B(n, k), float32 accumulation, 32x32x16 bf16
+// MFMAs.  Operands are K-contiguous (KC: [mn][k]) or MN-contiguous (MC:
+// [k][mn]); both go global -> LDS directly and, like in the grouped GEMMs
+// (grouped_gemm_w8b.hpp), through five operand buffers in rotation: B is
+// loaded two K steps ahead, A one, one barrier per step.
+//
+// Tiles: T = 256 (eight waves, 128 x 64 each, one work-group per CU) where
+// the product fills the chip with them, T = 128 (four waves, 64 x 64 each,
+// 80 KiB of LDS: two work-groups per CU) otherwise; either may split K over
+// S work-groups that write float32 partial tiles.
+//
+// Any M and N; K in multiples of 8 (16-byte chunks).  Rows past the end and
+// the K tail of the last step read as zeros: their byte offsets lie past the
+// buffer descriptor's range, which covers the tile's own rows only, so no
+// 32-bit offset grows with the matrix.  (Masking both operands' K tail
+// matters: the bytes behind a row's end are the next row's, and a NaN there
+// times zero would still be a NaN.)
+#pragma once
+
+#include <type_traits>
+
+#include "grouped_gemm.hpp"
+#include "linear_act.hpp"
+
+namespace moe {
+namespace lin {
+
+using gg::bf16x8_t;
+using gg::f32x16_t;
+using gg::KC;
+using gg::MC;
+
+struct TileParams {
+  const char* a;
+  const char* b;
+  int64_t lda, ldb;     // bytes between rows (KC) or k rows (MC)
+  int64_t M;
+  int N;
+  int64_t K;            // reduction length
+  int tiles_m, tiles_n;
+  int splits;           // > 1: float32 partials, no epilogue
+  uint16_t* c;          // bf16 [M][ldc]
+  int64_t ldc;
+  const float* bias;    // nullable [N]
+  const uint16_t* res;  // nullable [M][ldc]
+  uint16_t* z;          // nullable [M][ldc]: value before the activation
+  int act;
+  int vec;              // rows of c / res / z / bias take 16-byte accesses
+  float* part;          // [splits][M][ldp]
+  int64_t ldp;
+};
+
+constexpr uint32_t kFar = 0xfffffff0u;   // an offset no descriptor covers
+
+// K-contiguous operand, T rows x 64 k per stage: wave w, instruction j (of
+// 4) fills KiB NW j + w = rows 8 (NW j + w) + lane / 8, each lane loading
+// the 16-byte chunk that belongs at its LDS slot (swz32).
+template <int T>
+struct KcLoad {
+  static constexpr int NW = T / 32;
+  const char* base;   // row 0 of the tile, k = 0
+  uint32_t rec;       // bytes of the tile's valid rows
+  uint32_t kbytes;    // 2 K
+  uint32_t cl16;      // byte offset of the lane's chunk in the step
+  uint32_t off[4];
+  __device__ __forceinline__ void init(const char* p, int64_t ld, int64_t r0,
+                                       int64_t rows, int64_t K, int wave,
+                                       int lane) {
+    base = p + r0 * ld;
+    const int64_t left = rows - r0;
+    rec = (uint32_t)((left < T ? left : (int64_t)T) * ld);
+    kbytes = (uint32_t)(2 * K);
+    const int q = 8 * (wave & 3) + (lane >> 3);
+    const int cl = (lane & 7) ^ gg::swz32(q);
+    cl16 = (uint32_t)(cl * 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      off[j] = (uint32_t)(8 * (NW * j + wave) + (lane >> 3)) * (uint32_t)ld +
+               cl16;
+  }
+  __device__ __forceinline__ void issue(char* lds, int kt, bool real,
+                                        int wave) const {
+    const uint32_t kb = (uint32_t)kt * 128u;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(base + kb), (short)0, (int)(real ? rec - kb : 0u),
+        gg::kBufFlags);
+    const bool in = kb + cl16 < kbytes;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      MOE_LDS void* dst = (MOE_LDS void*)(lds + (NW * j + wave) * 1024);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, dst, 16,
+                                               in ? off[j] : kFar, 0, 0, 0);
+    }
+  }
+};
+
+// MN-contiguous operand, 64 k rows x T values per stage; 16-byte chunk c of
+// row k sits at chunk c ^ 4 (k & 3) (fragments: transposing LDS reads).
+// k rows past the end read as zeros; mn past the operand's last column reads
+// the next row or zeros and only reaches outputs that are never stored.
+template <int T>
+struct McLoad {
+  static constexpr int NW = T / 32;
+  static constexpr int RB = 2 * T;            // bytes per stage row
+  static constexpr int RPK = 1024 / RB;       // rows per KiB
+  static constexpr int LPR = 64 / RPK;        // lanes (chunks) per row
+  const char* base;   // k = 0, first mn of the tile
+  int64_t ld;
+  int64_t kdim;
+  uint32_t skip;      // bytes of a row before the tile
+  uint32_t off[4];
+  __device__ __forceinline__ void init(const char* p, int64_t ld_, int64_t mn0,
+                                       int64_t K, int wave, int lane) {
+    base = p + 2 * mn0;
+    ld = ld_;
+    kdim = K;
+    skip = (uint32_t)(2 * mn0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = RPK * (NW * j + wave) + lane / LPR;
+      const int c = (lane & (LPR - 1)) ^ (4 * (row & 3));
+      off[j] = (uint32_t)row * (uint32_t)ld + (uint32_t)(c * 16);
+    }
+  }
+  __device__ __forceinline__ void issue(char* lds, int kt, bool real,
+                                        int wave) const {
+    const int64_t k0 = (int64_t)kt * 64;
+    const int64_t left = kdim - k0;
+    const uint32_t rec =
+        (uint32_t)((left < 64 ? left : (int64_t)64) * ld) - skip;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(base + k0 * ld), (short)0, (int)(real ? rec : 0u),
+        gg::kBufFlags);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      MOE_LDS void* dst = (MOE_LDS void*)(lds + (NW * j + wave) * 1024);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, dst, 16, off[j], 0, 0, 0);
+    }
+  }
+  // 8 k values of a lane: two transposed 8-byte reads, k and k + 4
+  static __device__ __forceinline__ bf16x8_t tr8(const char* p) {
+    const gg::i16x4_t lo =
+        __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS gg::i16x4_t*)(p));
+    const gg::i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (MOE_LDS gg::i16x4_t*)(p + 4 * RB));
+    const gg::i16x8_t v =
+        __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_bit_cast(bf16x8_t, v);
+  }
+  // the lane's offsets of NB 32-wide blocks from mn chunk xb on (slice 0)
+  template <int NB>
+  static __device__ __forceinline__ void frag_offsets(int xb, int lane,
+                                                      uint32_t (&o)[NB]) {
+    const int G = lane >> 4, s = lane & 15, j = s >> 2, q = s & 3;
+    const int k0 = 8 * (G >> 1) + j;
+    const int x = 2 * (G & 1) + (q >> 1) + xb;   // chunk, bits 2-3 clear
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+      o[i] = (uint32_t)(k0 * RB + (((x + 4 * i) ^ (4 * j)) * 16) +
+                        (q & 1) * 8);
+  }
+};
+
+// Reads pinned ahead of the MFMAs they hide under: RPM per MFMA.
+template <int NV, int NR, int NM, int VPM, int I = 0>
+__device__ __forceinline__ void sched_slice() {
+  constexpr int RPM = (NR + NM - 1) / NM;
+  if constexpr (I < NM) {
+    constexpr int v = NV - I * VPM;
+    if constexpr (v > 0)
+      __builtin_amdgcn_sched_group_barrier(0x010, v < VPM ? v : VPM, 0);
+    constexpr int r = NR - I * RPM;
+    if constexpr (r > 0)
+      __builtin_amdgcn_sched_group_barrier(0x100, r < RPM ? r : RPM, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    sched_slice<NV, NR, NM, VPM, I + 1>();
+  }
+}
+
+// Work-groups b = x mod 8 run on XCD x; each XCD takes one contiguous run of
+// the tile list, in bands of 8 M tiles with M fastest: the 32 tiles in
+// flight on an XCD are 8 x 4 and share their panels in its L2.
+__device__ __forceinline__ bool tile_of(const TileParams& p, int& tm, int& tn,
+                                        int& split) {
+  const int tiles = p.tiles_m * p.tiles_n;
+  const int total = tiles * p.splits;
+  const int per = (total + gg::kXcds - 1) / gg::kXcds;
+  const int idx = blockIdx.x / gg::kXcds;
+  const int L = (blockIdx.x % gg::kXcds) * per + idx;
+  if (idx >= per || L >= total) return false;
+  split = L / tiles;
+  const int l = L - split * tiles;
+  const int band = l / (8 * p.tiles_n);
+  const int in = l - band * 8 * p.tiles_n;
+  const int gm = min(8, p.tiles_m - 8 * band);
+  tn = in / gm;
+  tm = 8 * band + in - tn * gm;
+  return true;
+}
+
+// One 8-value run of an output row: bias, activation, residual, rounding.
+// The activation is applied to the float32 value; the sum with the residual
+// is rounded to bf16 once.
+__device__ __forceinline__ void finish8(const TileParams& p, int64_t row,
+                                        int col, const float (&v)[8]) {
+  const int64_t at = row * p.ldc + col;
+  if (p.vec) {   // N % 8 == 0: the run is whole
+    if (col >= p.N) return;
+    float z[8], y[8];
+    float4 b0 = make_float4(0, 0, 0, 0), b1 = b0;
+    if (p.bias) {
+      b0 = *reinterpret_cast<const float4*>(p.bias + col);
+      b1 = *reinterpret_cast<const float4*>(p.bias + col + 4);
+    }
+    uint4 r = make_uint4(0, 0, 0, 0);
+    if (p.res) r = *reinterpret_cast<const uint4*>(p.res + at);
+    z[0] = v[0] + b0.x; z[1] = v[1] + b0.y;
+    z[2] = v[2] + b0.z; z[3] = v[3] + b0.w;
+    z[4] = v[4] + b1.x; z[5] = v[5] + b1.y;
+    z[6] = v[6] + b1.z; z[7] = v[7] + b1.w;
+    if (p.z)
+      *reinterpret_cast<uint4*>(p.z + at) =
+          make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]),
+                     pack_bf16x2(z[4], z[5]), pack_bf16x2(z[6], z[7]));
+    act_fwd8(p.act, z, y);
+    if (p.res) {
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[2 * i] += bf16lo(w[i]);
+        y[2 * i + 1] += bf16hi(w[i]);
+      }
+    }
+    *reinterpret_cast<uint4*>(p.c + at) =
+        make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                   pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+  } else {
+    float z[8], y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      z[i] = v[i] + (p.bias && col + i < p.N ? p.bias[col + i] : 0.0f);
+    act_fwd8(p.act, z, y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (col + i >= p.N) break;
+      if (p.z) p.z[at + i] = (uint16_t)f32_to_bf16(z[i]);
+      const float r = p.res ? bf16_to_f32(p.res[at + i]) : 0.0f;
+      p.c[at + i] = (uint16_t)f32_to_bf16(y[i] + r);
+    }
+  }
+}
+
+template <int T, int LA, int LB>
+__global__ __launch_bounds__(2 * T, 2) void linear_tile_kernel(TileParams p) {
+  constexpr int MI = T / 64, NJ = 2;   // 32-row A / 32-column B blocks
+  constexpr int WN = T / 64;           // waves along N (two along M)
+  constexpr int kSl = 4;               // 16-wide K slices per 64-wide step
+  constexpr int kStage = T * 128;
+  __shared__ __attribute__((aligned(1024))) char s0[kStage];
+  __shared__ __attribute__((aligned(1024))) char s1[kStage];
+  __shared__ __attribute__((aligned(1024))) char s2[kStage];
+  __shared__ __attribute__((aligned(1024))) char s3[kStage];
+  __shared__ __attribute__((aligned(1024))) char s4[kStage];
+  int tm, tn, split;
+  if (!tile_of(p, tm, tn, split)) return;
+  const int t = threadIdx.x;
+  const int lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int64_t m0 = (int64_t)tm * T;
+  const int n0 = tn * T;
+
+  // K steps [ks, ke) of this work-group
+  const int nk_all = (int)((p.K + 63) / 64);
+  const int ks = (int)((int64_t)split * nk_all / p.splits);
+  const int ke = (int)((int64_t)(split + 1) * nk_all / p.splits);
+  const int nk = ke - ks;
+
+  std::conditional_t<LA == KC, KcLoad<T>, McLoad<T>> da;
+  std::conditional_t<LB == KC, KcLoad<T>, McLoad<T>> db;
+  if constexpr (LA == KC) da.init(p.a, p.lda, m0, p.M, p.K, wave, lane);
+  else da.init(p.a, p.lda, m0, p.K, wave, lane);
+  if constexpr (LB == KC) db.init(p.b, p.ldb, n0, p.N, p.K, wave, lane);
+  else db.init(p.b, p.ldb, n0, p.K, wave, lane);
+  auto issue_a = [&](char* dst, int kt) {
+    da.issue(dst, ks + kt, kt < nk, wave);
+  };
+  auto issue_b = [&](char* dst, int kt) {
+    db.issue(dst, ks + kt, kt < nk, wave);
+  };
+
+  f32x16_t acc[MI][NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x16_t{};
+
+  using std::integral_constant;
+  auto buf = [&](auto nc) -> char* {
+    constexpr int n = decltype(nc)::value % 5;
+    if constexpr (n == 0) return s0;
+    else if constexpr (n == 1) return s1;
+    else if constexpr (n == 2) return s2;
+    else if constexpr (n == 3) return s3;
+    else return s4;
+  };
+  // Fragment offsets, passed through an empty asm at each use so that the
+  // compiler forms addresses when they are needed instead of holding one
+  // per buffer, slice and operand.
+  uint32_t fa[kSl], fb[kSl], ta[MI], tb[NJ];
+  if constexpr (LA == KC) {
+#pragma unroll
+    for (int kk = 0; kk < kSl; ++kk)
+      fa[kk] = (uint32_t)(wm * (MI * 32 * 128) +
+                          gg::frag_off(lane & 31, kk * 2 + (lane >> 5)));
+  } else {
+    McLoad<T>::template frag_offsets<MI>(MI * 4 * wm, lane, ta);
+  }
+  if constexpr (LB == KC) {
+#pragma unroll
+    for (int kk = 0; kk < kSl; ++kk)
+      fb[kk] = (uint32_t)(wn * (NJ * 32 * 128) +
+                          gg::frag_off(lane & 31, kk * 2 + (lane >> 5)));
+  } else {
+    McLoad<T>::template frag_offsets<NJ>(NJ * 4 * wn, lane, tb);
+  }
+  struct Frg { bf16x8_t a[MI], b[NJ]; };
+  auto read = [&](Frg& f, const char* sa, const char* sb, int kk) {
+    if constexpr (LA == KC) {
+      uint32_t o = fa[kk];
+      asm volatile("" : "+v"(o));
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+        f.a[i] = *reinterpret_cast<const bf16x8_t*>(sa + o + i * 32 * 128);
+    } else {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        uint32_t o = ta[i];
+        asm volatile("" : "+v"(o));
+        f.a[i] = McLoad<T>::tr8(sa + kk * 16 * McLoad<T>::RB + o);
+      }
+    }
+    if constexpr (LB == KC) {
+      uint32_t o = fb[kk];
+      asm volatile("" : "+v"(o));
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        f.b[j] = *reinterpret_cast<const bf16x8_t*>(sb + o + j * 32 * 128);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        uint32_t o = tb[j];
+        asm volatile("" : "+v"(o));
+        f.b[j] = McLoad<T>::tr8(sb + kk * 16 * McLoad<T>::RB + o);
+      }
+    }
+  };
+  auto mma = [&](const Frg& f, auto i0c, auto i1c) {
+    constexpr int I0 = decltype(i0c)::value, I1 = decltype(i1c)::value;
+#pragma unroll
+    for (int i = I0; i < I1; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i], f.b[j],
+                                                            acc[i][j], 0, 0, 0);
+  };
+  using Z0 = integral_constant<int, 0>;
+  using ZH = integral_constant<int, MI / 2>;
+  using ZF = integral_constant<int, MI>;
+  constexpr int kNR = (LA == KC ? MI : 2 * MI) + (LB == KC ? NJ : 2 * NJ);
+  constexpr int kNM = MI * NJ;
+  // this wave's loads but the last four (B two steps ahead) have landed and
+  // its reads of the step's buffers are done, then every wave's
+  constexpr int kWait = (4 & 0xf) | (0x7 << 4);   // vmcnt(4) lgkmcnt(0)
+  auto publish = [&]() {
+    __builtin_amdgcn_s_waitcnt(kWait);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  Frg cur, nxt;
+  int k = 0;
+  // Step k: B_k in buffer 2 j, A_k in 2 j + 1 (j = k % 5); A_{k+1} goes to
+  // 2 j + 3 over the first slice, B_{k+2} to 2 j + 4 over the second.
+  auto rstep = [&](auto jc) {
+    constexpr int j = decltype(jc)::value;
+    char* const b = buf(integral_constant<int, 2 * j>{});
+    char* const a = buf(integral_constant<int, 2 * j + 1>{});
+    char* const bn = buf(integral_constant<int, 2 * j + 2>{});
+    char* const an = buf(integral_constant<int, 2 * j + 3>{});
+    char* const bn2 = buf(integral_constant<int, 2 * j + 4>{});
+#pragma unroll
+    for (int kk = 0; kk < kSl - 1; ++kk) {
+      if (kk == 0) issue_a(an, k + 1);
+      if (kk == 1) issue_b(bn2, k + 2);
+      read(nxt, a, b, kk + 1);
+      mma(cur, Z0{}, ZF{});
+      cur = nxt;
+      if (kk <= 1) sched_slice<4, kNR, kNM, 2>();
+      else sched_slice<0, kNR, kNM, 1>();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // last slice: half the MFMAs, publish step k + 1, its first fragments
+    // under the other half
+    mma(cur, Z0{}, ZH{});
+    __builtin_amdgcn_sched_barrier(0);
+    publish();
+    read(nxt, an, bn, 0);
+    mma(cur, ZH{}, ZF{});
+    cur = nxt;
+    sched_slice<0, kNR, kNM / 2, 1>();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // prologue: B_0 into buffer 0, A_0 into buffer 1, then B_1 into buffer 2
+  // (left in flight)
+  issue_b(s0, 0);
+  issue_a(s1, 0);
+  issue_b(s2, 1);
+  publish();
+  read(cur, s1, s0, 0);
+  const int trips = nk / 5, rem = nk - 5 * trips;
+  for (int tr = 0; tr < trips; ++tr) {
+    rstep(integral_constant<int, 0>{});
+    ++k;
+    rstep(integral_constant<int, 1>{});
+    ++k;
+    rstep(integral_constant<int, 2>{});
+    ++k;
+    rstep(integral_constant<int, 3>{});
+    ++k;
+    rstep(integral_constant<int, 4>{});
+    ++k;
+  }
+  if (rem > 0) {
+    rstep(integral_constant<int, 0>{});
+    ++k;
+    if (rem > 1) {
+      rstep(integral_constant<int, 1>{});
+      ++k;
+      if (rem > 2) {
+        rstep(integral_constant<int, 2>{});
+        ++k;
+        if (rem > 3) rstep(integral_constant<int, 3>{});
+      }
+    }
+  }
+
+  // every wave is past its last read of the buffers (and every direct load
+  // has landed) before they become epilogue staging
+  __syncthreads();
+  // Two passes of 32 columns through the wave's own LDS: float32, 128-byte
+  // rows, 16-byte chunk c of row r at c ^ (r & 7); on readback lane l takes
+  // columns 8 (l % 4) .. + 7 of row 16 q + l / 4.
+  constexpr int kRows = 32 * MI;
+  constexpr int kWaveBytes = kRows * 128;
+  constexpr int kPerBuf = kStage / kWaveBytes;
+  char* const wbuf =
+      (wave / kPerBuf == 0 ? s0 : wave / kPerBuf == 1 ? s1
+       : wave / kPerBuf == 2 ? s2 : s3) + (wave % kPerBuf) * kWaveBytes;
+  const int colw = lane & 31, c4 = lane & 3;
+  const int64_t rw = m0 + wm * kRows;
+  float* const part = p.splits > 1 ? p.part + (int64_t)split * p.M * p.ldp
+                                   : nullptr;
+#pragma unroll
+  for (int pass = 0; pass < NJ; ++pass) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int row = gg::acc_row(i, r, lane);
+        *reinterpret_cast<float*>(wbuf + row * 128 +
+                                  (((colw >> 2) ^ (row & 7)) << 4) +
+                                  (colw & 3) * 4) = acc[i][pass][r];
+      }
+    __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): staging written
+    const int col = n0 + wn * 64 + 32 * pass + 8 * c4;
+#pragma unroll 2
+    for (int q = 0; q < kRows / 16; ++q) {
+      const int lr = 16 * q + (lane >> 2);
+      const float4 v0 = *reinterpret_cast<const float4*>(
+          wbuf + lr * 128 + (((2 * c4) ^ (lr & 7)) << 4));
+      const float4 v1 = *reinterpret_cast<const float4*>(
+          wbuf + lr * 128 + (((2 * c4 + 1) ^ (lr & 7)) << 4));
+      const int64_t row = rw + lr;
+      if (row >= p.M) continue;
+      if (part) {
+        if (col < p.ldp) {   // ldp % 8 == 0
+          float* o = part + row * p.ldp + col;
+          *reinterpret_cast<float4*>(o) = v0;
+          *reinterpret_cast<float4*>(o + 4) = v1;
+        }
+      } else {
+        const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        finish8(p, row, col, v);
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0xc07f);   // readback done before reuse
+  }
+}
+
+}  // namespace lin
+}  // namespace moe

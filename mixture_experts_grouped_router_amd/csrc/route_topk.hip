@@ -15,6 +15,7 @@
 // status word.
 #include "common.hpp"
 #include "kernels.hpp"
+#include "lanes.hpp"
 #include "timer.hpp"
 
 namespace moe {
@@ -115,31 +116,8 @@ __global__ __launch_bounds__(256) void route_topk_kernel(
 
 // ---- 16 lanes per token (k <= 16, E <= 256) -------------------------------
 // Four tokens per wave.  Lane s of a token's 16 holds the logits of experts
-// s, s + 16, ...; the reductions across the 16 lanes use DPP lane moves
-// (VALU only): quad swaps (xor 1, xor 2), then the half-row and row
-// mirrors.  Each step pairs lanes that hold equal partial results, so every
-// lane ends with the same value, bit for bit, also for the float64 sum.
-constexpr int kDppXor1 = 0xB1;          // quad_perm [1, 0, 3, 2]
-constexpr int kDppXor2 = 0x4E;          // quad_perm [2, 3, 0, 1]
-constexpr int kDppHalfMirror = 0x141;   // lane i <- 7 - i within 8
-constexpr int kDppMirror = 0x140;       // lane i <- 15 - i within 16
-
-template <int CTRL>
-__device__ __forceinline__ int dpp_i(int x) {
-  return __builtin_amdgcn_mov_dpp(x, CTRL, 0xf, 0xf, false);
-}
-template <int CTRL>
-__device__ __forceinline__ float dpp_f(float x) {
-  return __int_as_float(dpp_i<CTRL>(__float_as_int(x)));
-}
-template <int CTRL>
-__device__ __forceinline__ double dpp_d(double x) {
-  const uint64_t u = __double_as_longlong(x);
-  const int lo = dpp_i<CTRL>((int)(uint32_t)u);
-  const int hi = dpp_i<CTRL>((int)(uint32_t)(u >> 32));
-  return __longlong_as_double((long long)(((uint64_t)(uint32_t)hi << 32) |
-                                          (uint32_t)lo));
-}
+// s, s + 16, ...; the reductions across the 16 lanes use the DPP lane moves
+// of lanes.hpp.
 // (bv, be) <- the better of it and the candidate of the lane CTRL names
 template <int CTRL>
 __device__ __forceinline__ void best_step(float& bv, int& be) {

@@ -315,6 +315,14 @@ hipError_t launch_router_bwd(const float* logits, const int32_t* topk_idx,
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
+  return launch_router_proj_bwd(dlogits, x, w_r, T, H, E, dw_r, dx, ws,
+                                stream);
+}
+
+hipError_t launch_router_proj_bwd(const float* dlogits, const void* x,
+                                  const void* w_r, int64_t T, int H, int E,
+                                  float* dw_r, float* dx, void* ws,
+                                  hipStream_t stream) {
   if (dx) {
     // dx[t, h] = sum_e dl[t, e] W_r[e, h]
     KernelScope ks("router_dx", stream);
