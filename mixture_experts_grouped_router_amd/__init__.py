@@ -236,7 +236,14 @@ def _context(device: torch.device) -> int:
     return _ctx[idx]
 
 
+# the current stream's handle without building a torch.cuda.Stream object
+# (2.6 us of a 10 us call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream() -> int:
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
 
 

@@ -11,6 +11,7 @@
 #include <algorithm>
 
 #include "kernels.hpp"
+#include "linear_skinny.hpp"
 #include "linear_tile.hpp"
 #include "timer.hpp"
 
@@ -29,34 +30,51 @@ int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct Plan {
-  int T;        // tile edge
+  int tm, tn;   // tile
   int S;        // K splits
   size_t part_bytes(int64_t M, int64_t N) const {
     return S > 1 ? align256((size_t)S * M * pad8(N) * sizeof(float)) : 0;
   }
 };
 
-// Tile and split of an M x N x K product: the least estimated time.  Per K
-// step a CU takes about 1.75 us for a 256 tile and 1.1 us for two 128 tiles
-// side by side; a split writes and reads float32 partials and adds a launch.
+// Tile and split of an M x N x K product: the least estimated time.  A round
+// of work-groups that puts c of them on a CU takes
+//   steps * max(lat, thr c) + fix c
+// microseconds (lat: one K step with a CU to itself, thr: its share of a
+// busy CU, fix: prologue and epilogue); a split adds a launch and the
+// float32 partials' round trip at 8 TB/s (they mostly stay in the caches).
+// The constants are a least-squares fit to 900 timed (shape, tile, split)
+// combinations of the three products; the choice is then 2.4% slower than the
+// best combination on average, 24% at worst (a 14 us call).
 Plan plan_product(int64_t M, int64_t N, int64_t K) {
+  static const struct {
+    int tm, tn, per_cu;
+    double lat, thr, fix;
+  } kTiles[] = {{256, 256, 1, 1.17, 0.0, 9.0},
+                {128, 128, 2, 0.51, 0.43, 2.8},
+                {64, 128, 2, 0.42, 0.31, 1.9}};
   const int64_t steps = cdiv(K, 64);
-  Plan best{128, 1};
+  Plan best{128, 128, 1};
   double best_us = 1e30;
-  for (int T : {256, 128}) {
-    const int64_t tiles = cdiv(M, T) * cdiv(N, T);
-    const int64_t slots = T == 256 ? kCus : 2 * kCus;
-    const double step_us = T == 256 ? 1.75 : 1.1;
+  for (const auto& c : kTiles) {
+    const int64_t tiles = cdiv(M, c.tm) * cdiv(N, c.tn);
+    const int64_t slots = (int64_t)kCus * c.per_cu;
     for (int S = 1; S <= kMaxSplits; ++S) {
-      if (S > 1 && (S * 4 > steps ||
+      if (S > 1 && (S * 2 > steps ||
                     (int64_t)S * M * pad8(N) * 4 > kMaxPartBytes))
         break;
-      const int64_t rounds = cdiv(tiles * S, slots);
-      double us = (double)rounds * ((double)cdiv(steps, S) * step_us + 4.0);
-      if (S > 1) us += 4.0 + (double)S * M * N * 8.0 / 4e6;
+      const double st = (double)cdiv(steps, S);
+      auto round_us = [&](int64_t groups) {
+        const double occ = (double)cdiv(groups, kCus);
+        return st * std::max(c.lat, c.thr * occ) + c.fix * occ;
+      };
+      const int64_t last = tiles * S % slots;
+      double us = (double)(tiles * S / slots) * round_us(slots);
+      if (last) us += round_us(last);
+      if (S > 1) us += 3.2 + (double)S * M * N * 1e-6;
       if (us < best_us) {
         best_us = us;
-        best = Plan{T, S};
+        best = Plan{c.tm, c.tn, S};
       }
     }
   }
@@ -80,14 +98,16 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(TileParams p) {
     v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
     src += p.M * p.ldp;
   }
-  finish8(p, row, col, v);
+  float b[8];
+  bias8(p, col, b);
+  finish8(p, row * p.ldc + col, col, v, b);
 }
 
 template <int LA, int LB>
 hipError_t launch_product(const char* name, TileParams p, const Plan& pl,
                           void* part, hipStream_t stream) {
-  p.tiles_m = (int)cdiv(p.M, pl.T);
-  p.tiles_n = (int)cdiv(p.N, pl.T);
+  p.tiles_m = (int)cdiv(p.M, pl.tm);
+  p.tiles_n = (int)cdiv(p.N, pl.tn);
   p.splits = pl.S;
   p.part = static_cast<float*>(part);
   p.ldp = pad8(p.N);
@@ -95,11 +115,14 @@ hipError_t launch_product(const char* name, TileParams p, const Plan& pl,
   const unsigned grid = (unsigned)(cdiv(total, gg::kXcds) * gg::kXcds);
   {
     KernelScope ks(name, stream);
-    if (pl.T == 256)
-      hipLaunchKernelGGL((linear_tile_kernel<256, LA, LB>), dim3(grid),
+    if (pl.tm == 256)
+      hipLaunchKernelGGL((linear_tile_kernel<256, 256, LA, LB>), dim3(grid),
                          dim3(512), 0, stream, p);
+    else if (pl.tm == 128)
+      hipLaunchKernelGGL((linear_tile_kernel<128, 128, LA, LB>), dim3(grid),
+                         dim3(256), 0, stream, p);
     else
-      hipLaunchKernelGGL((linear_tile_kernel<128, LA, LB>), dim3(grid),
+      hipLaunchKernelGGL((linear_tile_kernel<64, 128, LA, LB>), dim3(grid),
                          dim3(256), 0, stream, p);
   }
   hipError_t e = hipGetLastError();
@@ -112,60 +135,113 @@ hipError_t launch_product(const char* name, TileParams p, const Plan& pl,
   return hipGetLastError();
 }
 
+// Few rows: one pass over the weights.  Up to 16 rows the MFMA form saves
+// the tile kernel's second launch (4 x 768 x 2048: 5.0 against 8.5 us; 16 x
+// 4096 x 4096: 11.6 against 14.1), but reads large weights more slowly (16 x
+// 14336 x 4096: 40.9 against 28.1).
+bool is_skinny(int64_t M, int64_t N, int64_t K) {
+  return M <= 2 || (M <= kSkinnyMaxM && N * K <= (int64_t)1 << 24);
+}
+hipError_t launch_skinny(const TileParams& p, hipStream_t stream) {
+  KernelScope ks("linear_skinny", stream);
+  auto go = [&](auto kern, int rows, int wv) {
+    hipLaunchKernelGGL(kern, dim3((unsigned)cdiv(p.N, rows)), dim3(64 * wv),
+                       0, stream, p);
+  };
+  if (p.M == 1) {
+    if (p.N >= 4 * kCus) go(linear_dot_kernel<1, 1>, 4, 4);
+    else go(linear_dot_kernel<1, 4>, 1, 4);
+  } else if (p.M == 2) {
+    if (p.N >= 4 * kCus) go(linear_dot_kernel<2, 1>, 4, 4);
+    else go(linear_dot_kernel<2, 4>, 1, 4);
+  } else {
+    go(linear_skinny_kernel<1, 1, 8, 4>, 16, 8);
+  }
+  return hipGetLastError();
+}
+
 // dz = dy act'(z) (bf16, rows padded with zeros to ldz) and, with db_part,
 // the float32 column sums of a chunk of rows.  32 lanes x 8 columns, 8 rows
-// at a time; grid (column blocks, row chunks).
+// of threads; a thread loads kDzU rows before it uses them (rows past the
+// chunk load its last row: a branch around a load would make the next one
+// wait for it).  HBM-bound; grid (column blocks, row chunks).
+constexpr int kDzU = 4;
+
+template <int ACT>
 __global__ __launch_bounds__(256) void linear_dz_kernel(
     const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z,
-    int64_t M, int N, int64_t rows_per_chunk, int act, int vec,
-    uint16_t* __restrict__ dz, int64_t ldz, float* __restrict__ db_part) {
+    int64_t M, int N, int64_t rows_per_chunk, uint16_t* __restrict__ dz,
+    int64_t ldz, float* __restrict__ db_part) {
   __shared__ float red[8][32 * 8 + 4];
   const int lane = threadIdx.x & 31, rt = threadIdx.x >> 5;
   const int col = (blockIdx.x * 32 + lane) * 8;
   const int64_t r0 = (int64_t)blockIdx.y * rows_per_chunk;
   const int64_t r1 = min(M, r0 + rows_per_chunk);
   float sum[8] = {};
-  if (col < ldz) {
-    for (int64_t r = r0 + rt; r < r1; r += 8) {
-      float g[8], zz[8];
-      const int64_t at = r * N + col;
-      if (vec) {
-        const uint4 a = *reinterpret_cast<const uint4*>(dy + at);
-        const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
+  auto row = [&](int64_t r, const float (&g0)[8], const float (&zz)[8]) {
+    float g[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      g[i] = ACT == ACT_NONE ? g0[i] : g0[i] * act_grad<ACT>(zz[i]);
+      sum[i] += g[i];
+    }
+    if (dz)
+      *reinterpret_cast<uint4*>(dz + r * ldz + col) =
+          make_uint4(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]),
+                     pack_bf16x2(g[4], g[5]), pack_bf16x2(g[6], g[7]));
+  };
+  if (col + 8 <= N) {
+    for (int64_t rb = r0 + rt; rb < r1; rb += 8 * kDzU) {
+      u32x4_a2_t a[kDzU], b[kDzU];
+#pragma unroll
+      for (int u = 0; u < kDzU; ++u) {
+        const int64_t at = min(rb + 8 * u, r1 - 1) * N + col;
+        a[u] = *reinterpret_cast<const u32x4_a2_t*>(dy + at);
+        if constexpr (ACT != ACT_NONE)
+          b[u] = *reinterpret_cast<const u32x4_a2_t*>(z + at);
+      }
+#pragma unroll
+      for (int u = 0; u < kDzU; ++u) {
+        if (rb + 8 * u >= r1) break;
+        float g[8], zz[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          g[2 * i] = bf16lo(aw[i]);
-          g[2 * i + 1] = bf16hi(aw[i]);
-        }
-        if (act != ACT_NONE) {
-          const uint4 b = *reinterpret_cast<const uint4*>(z + at);
-          const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            zz[2 * i] = bf16lo(bw[i]);
-            zz[2 * i + 1] = bf16hi(bw[i]);
+          g[2 * i] = bf16lo(a[u][i]);
+          g[2 * i + 1] = bf16hi(a[u][i]);
+          if constexpr (ACT != ACT_NONE) {
+            zz[2 * i] = bf16lo(b[u][i]);
+            zz[2 * i + 1] = bf16hi(b[u][i]);
           }
         }
-      } else {
+        row(rb + 8 * u, g, zz);
+      }
+    }
+  } else if (col < ldz) {   // the row's tail (loads clamped, then masked)
+    for (int64_t rb = r0 + rt; rb < r1; rb += 8 * kDzU) {
+      uint16_t a[kDzU][8], b[kDzU][8];
+#pragma unroll
+      for (int u = 0; u < kDzU; ++u) {
+        const int64_t r = min(rb + 8 * u, r1 - 1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int64_t at = r * N + min(col + i, N - 1);
+          a[u][i] = dy[at];
+          if constexpr (ACT != ACT_NONE) b[u][i] = z[at];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kDzU; ++u) {
+        if (rb + 8 * u >= r1) break;
+        float g[8], zz[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const bool in = col + i < N;
-          g[i] = in ? bf16_to_f32(dy[at + i]) : 0.0f;
-          zz[i] = in && act != ACT_NONE ? bf16_to_f32(z[at + i]) : 0.0f;
+          g[i] = in ? bf16_to_f32(a[u][i]) : 0.0f;
+          if constexpr (ACT != ACT_NONE)
+            zz[i] = in ? bf16_to_f32(b[u][i]) : 0.0f;
         }
+        row(rb + 8 * u, g, zz);
       }
-      if (act != ACT_NONE) {
-        float d[8];
-        act_grad8(act, zz, d);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] *= d[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += g[i];
-      if (dz)
-        *reinterpret_cast<uint4*>(dz + r * ldz + col) =
-            make_uint4(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]),
-                       pack_bf16x2(g[4], g[5]), pack_bf16x2(g[6], g[7]));
     }
   }
   if (!db_part) return;
@@ -181,23 +257,32 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(
   }
 }
 
-// db[c] = sum over the row chunks, 32 columns x 8 chunk strides per block
-__global__ __launch_bounds__(256) void linear_db_kernel(
+// db[c] = sum over the row chunks: 16 columns per block, 64 strided partial
+// sums each (a thread loads four chunks before it adds them), then a tree
+__global__ __launch_bounds__(1024) void linear_db_kernel(
     const float* __restrict__ part, int chunks, int N,
     float* __restrict__ db) {
-  __shared__ float red[8][33];
-  const int lane = threadIdx.x & 31, ct = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
+  __shared__ float red[64][17];
+  const int lane = threadIdx.x & 15, ct = threadIdx.x >> 4;
+  const int c = blockIdx.x * 16 + lane;
   float s = 0.0f;
-  if (c < N)
-    for (int i = ct; i < chunks; i += 8) s += part[(int64_t)i * N + c];
+  for (int i0 = ct; i0 < chunks; i0 += 256) {
+    float v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + 64 * u;
+      v[u] = i < chunks && c < N ? part[(int64_t)i * N + c] : 0.0f;
+    }
+    s += (v[0] + v[1]) + (v[2] + v[3]);
+  }
   red[ct][lane] = s;
   __syncthreads();
-  if (ct == 0 && c < N) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += red[i][lane];
-    db[c] = s;
+  for (int h = 32; h >= 1; h >>= 1) {
+    if (ct < h) red[ct][lane] += red[ct + h][lane];
+    __syncthreads();
   }
+  if (ct == 0 && c < N) db[c] = red[0][lane];
 }
 
 // row chunks of the dz pass: about four blocks per CU, 32 rows at least
@@ -207,14 +292,10 @@ int64_t dz_chunks(int64_t M, int N) {
       1, std::min<int64_t>(cdiv(M, 32), cdiv(4 * kCus, cb)));
 }
 
-bool al16(const void* p) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
-}
-
 }  // namespace
 
 size_t linear_fwd_ws_bytes(int64_t M, int N, int K) {
-  return M == 0 ? 0 : plan_product(M, N, K).part_bytes(M, N);
+  return M == 0 || is_skinny(M, N, K) ? 0 : plan_product(M, N, K).part_bytes(M, N);
 }
 
 hipError_t launch_linear_fwd(int64_t M, int N, int K, int act, const void* x,
@@ -236,7 +317,7 @@ hipError_t launch_linear_fwd(int64_t M, int N, int K, int act, const void* x,
   p.res = static_cast<const uint16_t*>(residual);
   p.z = static_cast<uint16_t*>(z_save);
   p.act = act;
-  p.vec = N % 8 == 0 && al16(bias);
+  if (is_skinny(M, N, K)) return launch_skinny(p, stream);
   return launch_product<KC, KC>("linear_fwd", p, plan_product(M, N, K), ws,
                                 stream);
 }
@@ -289,20 +370,28 @@ hipError_t launch_linear_bwd(int64_t M, int N, int K, int act, const void* dy,
   if ((own_dz && products) || db) {
     KernelScope ks("linear_dz", stream);
     const int64_t rpc = cdiv(cdiv(M, chunks), 8) * 8;
-    const int vec = N % 8 == 0;
-    hipLaunchKernelGGL(linear_dz_kernel,
-                       dim3((unsigned)cdiv(pad8(N), 256), (unsigned)chunks),
-                       dim3(256), 0, stream,
-                       static_cast<const uint16_t*>(dy),
-                       static_cast<const uint16_t*>(z), M, N, rpc, act, vec,
-                       products ? dz : nullptr, ldz, db_part);
+    auto go = [&](auto kern) {
+      hipLaunchKernelGGL(kern,
+                         dim3((unsigned)cdiv(pad8(N), 256), (unsigned)chunks),
+                         dim3(256), 0, stream,
+                         static_cast<const uint16_t*>(dy),
+                         static_cast<const uint16_t*>(z), M, N, rpc,
+                         products ? dz : nullptr, ldz, db_part);
+    };
+    switch (act) {
+      case ACT_RELU: go(linear_dz_kernel<ACT_RELU>); break;
+      case ACT_GELU: go(linear_dz_kernel<ACT_GELU>); break;
+      case ACT_GELU_TANH: go(linear_dz_kernel<ACT_GELU_TANH>); break;
+      case ACT_SILU: go(linear_dz_kernel<ACT_SILU>); break;
+      default: go(linear_dz_kernel<ACT_NONE>);
+    }
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (db) {
     KernelScope ks("linear_db", stream);
-    hipLaunchKernelGGL(linear_db_kernel, dim3((unsigned)cdiv(N, 32)),
-                       dim3(256), 0, stream, db_part, (int)chunks, N, db);
+    hipLaunchKernelGGL(linear_db_kernel, dim3((unsigned)cdiv(N, 16)),
+                       dim3(1024), 0, stream, db_part, (int)chunks, N, db);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -319,7 +408,6 @@ hipError_t launch_linear_bwd(int64_t M, int N, int K, int act, const void* dy,
     p.K = N;
     p.c = static_cast<uint16_t*>(dx);
     p.ldc = K;
-    p.vec = 1;
     e = launch_product<KC, MC>("linear_dgrad", p, plan_product(M, K, N), wp,
                                stream);
     if (e != hipSuccess) return e;
@@ -335,7 +423,6 @@ hipError_t launch_linear_bwd(int64_t M, int N, int K, int act, const void* dy,
     p.K = M;
     p.c = static_cast<uint16_t*>(dw);
     p.ldc = K;
-    p.vec = 1;
     e = launch_product<MC, MC>("linear_wgrad", p, plan_product(N, K, M), wp,
                                stream);
   }

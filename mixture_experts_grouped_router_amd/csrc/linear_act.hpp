@@ -13,9 +13,27 @@ __device__ __forceinline__ float sigm(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __expf(-x));
 }
 
-// Normal distribution function of x (0.5 erfc(-x / sqrt 2)).
-__device__ __forceinline__ float ndtr(float x) {
-  return 0.5f * erfcf(x * -0.70710678118654752f);
+// Normal distribution function Phi(z), and e^(-z^2 / 2) in *e.  The tail
+// Phi(-a), a = |z|, is e^(-a^2 / 2) times a function that is smooth in
+// t = 1 / (1 + 0.3 a): a degree-8 polynomial in t without constant term,
+// fitted to erfcx (relative error 1.5e-7 for a <= 14; 4e-6 in float32, from
+// the exponential's argument).  The form keeps the tail's relative accuracy,
+// which z Phi(z) shows for negative z.  The library's erfc gave the same
+// bf16 outputs and took 13% of a 8192 x 14336 x 4096 product's time.
+__device__ __forceinline__ float ndtr(float z, float* e) {
+  const float a = fabsf(z);
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3f, a, 1.0f));
+  float q = 0.03567507490515709f;
+  q = fmaf(q, t, -0.15720432996749878f);
+  q = fmaf(q, t, 0.20635563135147095f);
+  q = fmaf(q, t, -0.053685590624809265f);
+  q = fmaf(q, t, 0.12856264412403107f);
+  q = fmaf(q, t, 0.09991317987442017f);
+  q = fmaf(q, t, 0.12075400352478027f);
+  q = fmaf(q, t, 0.11962929368019104f);
+  *e = __expf(-0.5f * z * z);
+  const float tail = *e * (q * t);
+  return z < 0.0f ? tail : 1.0f - tail;
 }
 
 template <int ACT>
@@ -23,7 +41,8 @@ __device__ __forceinline__ float act_fwd(float z) {
   if constexpr (ACT == ACT_RELU) {
     return fmaxf(z, 0.0f);
   } else if constexpr (ACT == ACT_GELU) {
-    return z * ndtr(z);
+    float e;
+    return z * ndtr(z, &e);
   } else if constexpr (ACT == ACT_GELU_TANH) {
     // 0.5 z (1 + tanh u) = z sigmoid(2 u), 2 u = 2 sqrt(2 / pi) (z + ...)
     const float u2 = 1.5957691216057308f * (z + 0.044715f * z * z * z);
@@ -40,7 +59,9 @@ __device__ __forceinline__ float act_grad(float z) {
   if constexpr (ACT == ACT_RELU) {
     return z > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (ACT == ACT_GELU) {
-    return ndtr(z) + z * 0.3989422804014327f * __expf(-0.5f * z * z);
+    float e;
+    const float c = ndtr(z, &e);
+    return c + z * 0.3989422804014327f * e;
   } else if constexpr (ACT == ACT_GELU_TANH) {
     const float u2 = 1.5957691216057308f * (z + 0.044715f * z * z * z);
     const float du2 = 1.5957691216057308f * (1.0f + 0.134145f * z * z);
@@ -72,6 +93,16 @@ __device__ __forceinline__ void act_fwd8(int act, const float (&z)[8],
       for (int i = 0; i < 8; ++i) y[i] = z[i];
   }
 #undef MOE_ACT_CASE
+}
+
+__device__ __forceinline__ float act_fwd1(int act, float z) {
+  switch (act) {
+    case ACT_RELU: return act_fwd<ACT_RELU>(z);
+    case ACT_GELU: return act_fwd<ACT_GELU>(z);
+    case ACT_GELU_TANH: return act_fwd<ACT_GELU_TANH>(z);
+    case ACT_SILU: return act_fwd<ACT_SILU>(z);
+    default: return z;
+  }
 }
 
 // d = act'(z) for 8 values

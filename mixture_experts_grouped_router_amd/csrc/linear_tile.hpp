@@ -4,13 +4,13 @@
 // C[m, n] = sum_k A(m, k) B(n, k), float32 accumulation, 32x32x16 bf16
 // MFMAs.  Operands are K-contiguous (KC: [mn][k]) or MN-contiguous (MC:
 // [k][mn]); both go global -> LDS directly and, like in the grouped GEMMs
-// (grouped_gemm_w8b.hpp), through five operand buffers in rotation: B is
-// loaded two K steps ahead, A one, one barrier per step.
+// (grouped_gemm_w8b.hpp), B is loaded two K steps ahead (three buffers) and
+// A one (two buffers), with one barrier per step.
 //
-// Tiles: T = 256 (eight waves, 128 x 64 each, one work-group per CU) where
-// the product fills the chip with them, T = 128 (four waves, 64 x 64 each,
-// 80 KiB of LDS: two work-groups per CU) otherwise; either may split K over
-// S work-groups that write float32 partial tiles.
+// Tiles: 256 x 256 (eight waves, one work-group per CU) where the product
+// fills the chip with them, else 128 x 128 or 64 x 128 (four waves, two
+// work-groups per CU); each may split K over S work-groups that write
+// float32 partial tiles.
 //
 // Any M and N; K in multiples of 8 (16-byte chunks).  Rows past the end and
 // the K tail of the last step read as zeros: their byte offsets lie past the
@@ -48,36 +48,35 @@ struct TileParams {
   const uint16_t* res;  // nullable [M][ldc]
   uint16_t* z;          // nullable [M][ldc]: value before the activation
   int act;
-  int vec;              // rows of c / res / z / bias take 16-byte accesses
   float* part;          // [splits][M][ldp]
   int64_t ldp;
 };
 
 constexpr uint32_t kFar = 0xfffffff0u;   // an offset no descriptor covers
 
-// K-contiguous operand, T rows x 64 k per stage: wave w, instruction j (of
-// 4) fills KiB NW j + w = rows 8 (NW j + w) + lane / 8, each lane loading
-// the 16-byte chunk that belongs at its LDS slot (swz32).
-template <int T>
+// K-contiguous operand, R rows x 64 k per stage, NW waves: wave w,
+// instruction j fills KiB NW j + w = rows 8 (NW j + w) + lane / 8, each lane
+// loading the 16-byte chunk that belongs at its LDS slot (swz32).
+template <int R, int NW>
 struct KcLoad {
-  static constexpr int NW = T / 32;
+  static constexpr int J = R / (8 * NW);   // instructions per stage
   const char* base;   // row 0 of the tile, k = 0
   uint32_t rec;       // bytes of the tile's valid rows
   uint32_t kbytes;    // 2 K
   uint32_t cl16;      // byte offset of the lane's chunk in the step
-  uint32_t off[4];
+  uint32_t off[J];
   __device__ __forceinline__ void init(const char* p, int64_t ld, int64_t r0,
                                        int64_t rows, int64_t K, int wave,
                                        int lane) {
     base = p + r0 * ld;
     const int64_t left = rows - r0;
-    rec = (uint32_t)((left < T ? left : (int64_t)T) * ld);
+    rec = (uint32_t)((left < R ? left : (int64_t)R) * ld);
     kbytes = (uint32_t)(2 * K);
-    const int q = 8 * (wave & 3) + (lane >> 3);
+    const int q = 8 * (wave & 3) + (lane >> 3);   // NW % 4 == 0
     const int cl = (lane & 7) ^ gg::swz32(q);
     cl16 = (uint32_t)(cl * 16);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < J; ++j)
       off[j] = (uint32_t)(8 * (NW * j + wave) + (lane >> 3)) * (uint32_t)ld +
                cl16;
   }
@@ -89,7 +88,7 @@ struct KcLoad {
         gg::kBufFlags);
     const bool in = kb + cl16 < kbytes;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < J; ++j) {
       MOE_LDS void* dst = (MOE_LDS void*)(lds + (NW * j + wave) * 1024);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, dst, 16,
                                                in ? off[j] : kFar, 0, 0, 0);
@@ -97,21 +96,26 @@ struct KcLoad {
   }
 };
 
-// MN-contiguous operand, 64 k rows x T values per stage; 16-byte chunk c of
-// row k sits at chunk c ^ 4 (k & 3) (fragments: transposing LDS reads).
+// MN-contiguous operand, 64 k rows x R values per stage; fragments come
+// from transposing LDS reads.  16-byte chunk c of row k sits at c ^ 4 sw(k):
+// the four k rows of a read then fall on different banks (rows are 2 R
+// bytes: with R = 64 two of them fill the 256 bytes of the banks).
 // k rows past the end read as zeros; mn past the operand's last column reads
 // the next row or zeros and only reaches outputs that are never stored.
-template <int T>
+template <int R, int NW>
 struct McLoad {
-  static constexpr int NW = T / 32;
-  static constexpr int RB = 2 * T;            // bytes per stage row
+  static constexpr int J = R / (8 * NW);
+  static constexpr int RB = 2 * R;            // bytes per stage row
   static constexpr int RPK = 1024 / RB;       // rows per KiB
   static constexpr int LPR = 64 / RPK;        // lanes (chunks) per row
+  static __device__ __forceinline__ int sw(int k) {
+    return R == 64 ? (k >> 1) & 1 : k & 3;
+  }
   const char* base;   // k = 0, first mn of the tile
   int64_t ld;
   int64_t kdim;
   uint32_t skip;      // bytes of a row before the tile
-  uint32_t off[4];
+  uint32_t off[J];
   __device__ __forceinline__ void init(const char* p, int64_t ld_, int64_t mn0,
                                        int64_t K, int wave, int lane) {
     base = p + 2 * mn0;
@@ -119,9 +123,9 @@ struct McLoad {
     kdim = K;
     skip = (uint32_t)(2 * mn0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < J; ++j) {
       const int row = RPK * (NW * j + wave) + lane / LPR;
-      const int c = (lane & (LPR - 1)) ^ (4 * (row & 3));
+      const int c = (lane & (LPR - 1)) ^ (4 * sw(row));
       off[j] = (uint32_t)row * (uint32_t)ld + (uint32_t)(c * 16);
     }
   }
@@ -135,7 +139,7 @@ struct McLoad {
         (void*)(base + k0 * ld), (short)0, (int)(real ? rec : 0u),
         gg::kBufFlags);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < J; ++j) {
       MOE_LDS void* dst = (MOE_LDS void*)(lds + (NW * j + wave) * 1024);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, dst, 16, off[j], 0, 0, 0);
     }
@@ -156,10 +160,10 @@ struct McLoad {
                                                       uint32_t (&o)[NB]) {
     const int G = lane >> 4, s = lane & 15, j = s >> 2, q = s & 3;
     const int k0 = 8 * (G >> 1) + j;
-    const int x = 2 * (G & 1) + (q >> 1) + xb;   // chunk, bits 2-3 clear
+    const int x = 2 * (G & 1) + (q >> 1) + xb;   // xb % 4 == 0
 #pragma unroll
     for (int i = 0; i < NB; ++i)
-      o[i] = (uint32_t)(k0 * RB + (((x + 4 * i) ^ (4 * j)) * 16) +
+      o[i] = (uint32_t)(k0 * RB + (((x + 4 * i) ^ (4 * sw(j))) * 16) +
                         (q & 1) * 8);
   }
 };
@@ -201,77 +205,123 @@ __device__ __forceinline__ bool tile_of(const TileParams& p, int& tm, int& tn,
   return true;
 }
 
+// One output value (the skinny kernel's epilogue).
+__device__ __forceinline__ void finish1(const TileParams& p, int64_t row,
+                                        int col, float v) {
+  const int64_t at = row * p.ldc + col;
+  const float z = p.bias ? v + p.bias[col] : v;
+  if (p.z) p.z[at] = (uint16_t)f32_to_bf16(z);
+  float y = act_fwd1(p.act, z);
+  if (p.res) y += bf16_to_f32(p.res[at]);
+  p.c[at] = (uint16_t)f32_to_bf16(y);
+}
+
+// 16 bytes at 2-byte alignment (rows of an odd N): one access each, the
+// hardware takes unaligned global addresses
+typedef uint32_t u32x4_a2_t __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_a4_t __attribute__((ext_vector_type(4), aligned(4)));
+
 // One 8-value run of an output row: bias, activation, residual, rounding.
 // The activation is applied to the float32 value; the sum with the residual
 // is rounded to bf16 once.
-__device__ __forceinline__ void finish8(const TileParams& p, int64_t row,
-                                        int col, const float (&v)[8]) {
-  const int64_t at = row * p.ldc + col;
-  if (p.vec) {   // N % 8 == 0: the run is whole
-    if (col >= p.N) return;
-    float z[8], y[8];
-    float4 b0 = make_float4(0, 0, 0, 0), b1 = b0;
-    if (p.bias) {
-      b0 = *reinterpret_cast<const float4*>(p.bias + col);
-      b1 = *reinterpret_cast<const float4*>(p.bias + col + 4);
-    }
-    uint4 r = make_uint4(0, 0, 0, 0);
-    if (p.res) r = *reinterpret_cast<const uint4*>(p.res + at);
-    z[0] = v[0] + b0.x; z[1] = v[1] + b0.y;
-    z[2] = v[2] + b0.z; z[3] = v[3] + b0.w;
-    z[4] = v[4] + b1.x; z[5] = v[5] + b1.y;
-    z[6] = v[6] + b1.z; z[7] = v[7] + b1.w;
-    if (p.z)
-      *reinterpret_cast<uint4*>(p.z + at) =
-          make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]),
-                     pack_bf16x2(z[4], z[5]), pack_bf16x2(z[6], z[7]));
-    act_fwd8(p.act, z, y);
-    if (p.res) {
-      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+__device__ __forceinline__ void bias8(const TileParams& p, int col,
+                                      float (&b)[8]) {
+  f32x4_a4_t b0 = {0, 0, 0, 0}, b1 = b0;
+  if (p.bias) {
+    if (col + 8 <= p.N) {
+      b0 = *reinterpret_cast<const f32x4_a4_t*>(p.bias + col);
+      b1 = *reinterpret_cast<const f32x4_a4_t*>(p.bias + col + 4);
+    } else {   // (loads clamped: a branch around each would serialise them)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        y[2 * i] += bf16lo(w[i]);
-        y[2 * i + 1] += bf16hi(w[i]);
+        b0[i] = p.bias[min(col + i, p.N - 1)];
+        b1[i] = p.bias[min(col + 4 + i, p.N - 1)];
       }
     }
-    *reinterpret_cast<uint4*>(p.c + at) =
-        make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                   pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-  } else {
-    float z[8], y[8];
+  }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      z[i] = v[i] + (p.bias && col + i < p.N ? p.bias[col + i] : 0.0f);
+  for (int i = 0; i < 4; ++i) {
+    b[i] = b0[i];
+    b[4 + i] = b1[i];
+  }
+}
+
+// at: the run's first element in the output; b: its bias
+__device__ __forceinline__ void finish8(const TileParams& p, int64_t at,
+                                        int col, const float (&v)[8],
+                                        const float (&b)[8]) {
+  float z[8], y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) z[i] = v[i] + b[i];
+  if (col + 8 <= p.N) {
+    u32x4_a2_t r = {0, 0, 0, 0};
+    if (p.res) r = *reinterpret_cast<const u32x4_a2_t*>(p.res + at);
+    if (p.z) {
+      const u32x4_a2_t o = {pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]),
+                            pack_bf16x2(z[4], z[5]), pack_bf16x2(z[6], z[7])};
+      *reinterpret_cast<u32x4_a2_t*>(p.z + at) = o;
+    }
+    act_fwd8(p.act, z, y);
+    if (p.res) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[2 * i] += bf16lo(r[i]);
+        y[2 * i + 1] += bf16hi(r[i]);
+      }
+    }
+    const u32x4_a2_t o = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                          pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7])};
+    *reinterpret_cast<u32x4_a2_t*>(p.c + at) = o;
+  } else if (col < p.N) {   // the row's tail
+    const int n = p.N - col;
+    uint16_t r[8] = {};
+    if (p.res)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r[i] = p.res[at + min(i, n - 1)];
     act_fwd8(p.act, z, y);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (col + i >= p.N) break;
-      if (p.z) p.z[at + i] = (uint16_t)f32_to_bf16(z[i]);
-      const float r = p.res ? bf16_to_f32(p.res[at + i]) : 0.0f;
-      p.c[at + i] = (uint16_t)f32_to_bf16(y[i] + r);
+      if (p.res) y[i] += bf16_to_f32(r[i]);
+      if (i < n) {
+        if (p.z) p.z[at + i] = (uint16_t)f32_to_bf16(z[i]);
+        p.c[at + i] = (uint16_t)f32_to_bf16(y[i]);
+      }
     }
   }
 }
 
-template <int T, int LA, int LB>
-__global__ __launch_bounds__(2 * T, 2) void linear_tile_kernel(TileParams p) {
-  constexpr int MI = T / 64, NJ = 2;   // 32-row A / 32-column B blocks
-  constexpr int WN = T / 64;           // waves along N (two along M)
+// The wave grid of a tile: 256 x 256, 2 x 4 waves of 128 x 64; 128 x 128,
+// 2 x 2 of 64 x 64; 64 x 128, 1 x 4 of 64 x 32.
+template <int TM, int TN>
+struct TileShape {
+  static constexpr int WM = TM == 64 ? 1 : 2;
+  static constexpr int WN = TN == 256 || TM == 64 ? 4 : 2;
+  static constexpr int NW = WM * WN;
+  static constexpr int MI = TM / WM / 32;   // 32-row A blocks of a wave
+  static constexpr int NJ = TN / WN / 32;   // 32-column B blocks
+};
+
+template <int TM, int TN, int LA, int LB>
+__global__ __launch_bounds__((64 * TileShape<TM, TN>::NW), 2) void
+linear_tile_kernel(TileParams p) {
+#ifdef __HIP_DEVICE_COMPILE__   // (the host pass needs the launch stub only)
+  using S = TileShape<TM, TN>;
+  constexpr int MI = S::MI, NJ = S::NJ, WN = S::WN, NW = S::NW;
   constexpr int kSl = 4;               // 16-wide K slices per 64-wide step
-  constexpr int kStage = T * 128;
-  __shared__ __attribute__((aligned(1024))) char s0[kStage];
-  __shared__ __attribute__((aligned(1024))) char s1[kStage];
-  __shared__ __attribute__((aligned(1024))) char s2[kStage];
-  __shared__ __attribute__((aligned(1024))) char s3[kStage];
-  __shared__ __attribute__((aligned(1024))) char s4[kStage];
+  // B of three steps, A of two
+  __shared__ __attribute__((aligned(1024))) char b0[TN * 128];
+  __shared__ __attribute__((aligned(1024))) char b1[TN * 128];
+  __shared__ __attribute__((aligned(1024))) char b2[TN * 128];
+  __shared__ __attribute__((aligned(1024))) char a0[TM * 128];
+  __shared__ __attribute__((aligned(1024))) char a1[TM * 128];
   int tm, tn, split;
   if (!tile_of(p, tm, tn, split)) return;
   const int t = threadIdx.x;
   const int lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const int64_t m0 = (int64_t)tm * T;
-  const int n0 = tn * T;
+  const int64_t m0 = (int64_t)tm * TM;
+  const int n0 = tn * TN;
 
   // K steps [ks, ke) of this work-group
   const int nk_all = (int)((p.K + 63) / 64);
@@ -279,8 +329,10 @@ __global__ __launch_bounds__(2 * T, 2) void linear_tile_kernel(TileParams p) {
   const int ke = (int)((int64_t)(split + 1) * nk_all / p.splits);
   const int nk = ke - ks;
 
-  std::conditional_t<LA == KC, KcLoad<T>, McLoad<T>> da;
-  std::conditional_t<LB == KC, KcLoad<T>, McLoad<T>> db;
+  using LdA = std::conditional_t<LA == KC, KcLoad<TM, NW>, McLoad<TM, NW>>;
+  using LdB = std::conditional_t<LB == KC, KcLoad<TN, NW>, McLoad<TN, NW>>;
+  LdA da;
+  LdB db;
   if constexpr (LA == KC) da.init(p.a, p.lda, m0, p.M, p.K, wave, lane);
   else da.init(p.a, p.lda, m0, p.K, wave, lane);
   if constexpr (LB == KC) db.init(p.b, p.ldb, n0, p.N, p.K, wave, lane);
@@ -299,13 +351,15 @@ __global__ __launch_bounds__(2 * T, 2) void linear_tile_kernel(TileParams p) {
     for (int j = 0; j < NJ; ++j) acc[i][j] = f32x16_t{};
 
   using std::integral_constant;
-  auto buf = [&](auto nc) -> char* {
-    constexpr int n = decltype(nc)::value % 5;
-    if constexpr (n == 0) return s0;
-    else if constexpr (n == 1) return s1;
-    else if constexpr (n == 2) return s2;
-    else if constexpr (n == 3) return s3;
-    else return s4;
+  auto bufb = [&](auto nc) -> char* {
+    constexpr int n = decltype(nc)::value % 3;
+    if constexpr (n == 0) return b0;
+    else if constexpr (n == 1) return b1;
+    else return b2;
+  };
+  auto bufa = [&](auto nc) -> char* {
+    if constexpr (decltype(nc)::value % 2 == 0) return a0;
+    else return a1;
   };
   // Fragment offsets, passed through an empty asm at each use so that the
   // compiler forms addresses when they are needed instead of holding one
@@ -317,7 +371,7 @@ __global__ __launch_bounds__(2 * T, 2) void linear_tile_kernel(TileParams p) {
       fa[kk] = (uint32_t)(wm * (MI * 32 * 128) +
                           gg::frag_off(lane & 31, kk * 2 + (lane >> 5)));
   } else {
-    McLoad<T>::template frag_offsets<MI>(MI * 4 * wm, lane, ta);
+    LdA::template frag_offsets<MI>(MI * 4 * wm, lane, ta);
   }
   if constexpr (LB == KC) {
 #pragma unroll
@@ -325,7 +379,7 @@ __global__ __launch_bounds__(2 * T, 2) void linear_tile_kernel(TileParams p) {
       fb[kk] = (uint32_t)(wn * (NJ * 32 * 128) +
                           gg::frag_off(lane & 31, kk * 2 + (lane >> 5)));
   } else {
-    McLoad<T>::template frag_offsets<NJ>(NJ * 4 * wn, lane, tb);
+    LdB::template frag_offsets<NJ>(NJ * 4 * wn, lane, tb);
   }
   struct Frg { bf16x8_t a[MI], b[NJ]; };
   auto read = [&](Frg& f, const char* sa, const char* sb, int kk) {
@@ -340,7 +394,7 @@ __global__ __launch_bounds__(2 * T, 2) void linear_tile_kernel(TileParams p) {
       for (int i = 0; i < MI; ++i) {
         uint32_t o = ta[i];
         asm volatile("" : "+v"(o));
-        f.a[i] = McLoad<T>::tr8(sa + kk * 16 * McLoad<T>::RB + o);
+        f.a[i] = LdA::tr8(sa + kk * 16 * LdA::RB + o);
       }
     }
     if constexpr (LB == KC) {
@@ -354,7 +408,7 @@ __global__ __launch_bounds__(2 * T, 2) void linear_tile_kernel(TileParams p) {
       for (int j = 0; j < NJ; ++j) {
         uint32_t o = tb[j];
         asm volatile("" : "+v"(o));
-        f.b[j] = McLoad<T>::tr8(sb + kk * 16 * McLoad<T>::RB + o);
+        f.b[j] = LdB::tr8(sb + kk * 16 * LdB::RB + o);
       }
     }
   };
@@ -372,9 +426,10 @@ __global__ __launch_bounds__(2 * T, 2) void linear_tile_kernel(TileParams p) {
   using ZF = integral_constant<int, MI>;
   constexpr int kNR = (LA == KC ? MI : 2 * MI) + (LB == KC ? NJ : 2 * NJ);
   constexpr int kNM = MI * NJ;
-  // this wave's loads but the last four (B two steps ahead) have landed and
+  // this wave's loads but the last of B (two steps ahead) have landed and
   // its reads of the step's buffers are done, then every wave's
-  constexpr int kWait = (4 & 0xf) | (0x7 << 4);   // vmcnt(4) lgkmcnt(0)
+  static_assert(LdB::J < 16, "vmcnt field");
+  constexpr int kWait = LdB::J | (0x7 << 4);   // vmcnt(J) lgkmcnt(0)
   auto publish = [&]() {
     __builtin_amdgcn_s_waitcnt(kWait);
     asm volatile("" ::: "memory");
@@ -383,15 +438,16 @@ __global__ __launch_bounds__(2 * T, 2) void linear_tile_kernel(TileParams p) {
   };
   Frg cur, nxt;
   int k = 0;
-  // Step k: B_k in buffer 2 j, A_k in 2 j + 1 (j = k % 5); A_{k+1} goes to
-  // 2 j + 3 over the first slice, B_{k+2} to 2 j + 4 over the second.
+  // Step k (j = k mod 6): B_k in B buffer j % 3, A_k in A buffer j % 2;
+  // A_{k+1} lands in the other A buffer from the first slice on, B_{k+2} in
+  // the B buffer that step k - 1 has left from the second.
   auto rstep = [&](auto jc) {
     constexpr int j = decltype(jc)::value;
-    char* const b = buf(integral_constant<int, 2 * j>{});
-    char* const a = buf(integral_constant<int, 2 * j + 1>{});
-    char* const bn = buf(integral_constant<int, 2 * j + 2>{});
-    char* const an = buf(integral_constant<int, 2 * j + 3>{});
-    char* const bn2 = buf(integral_constant<int, 2 * j + 4>{});
+    char* const b = bufb(integral_constant<int, j>{});
+    char* const a = bufa(integral_constant<int, j>{});
+    char* const bn = bufb(integral_constant<int, j + 1>{});
+    char* const an = bufa(integral_constant<int, j + 1>{});
+    char* const bn2 = bufb(integral_constant<int, j + 2>{});
 #pragma unroll
     for (int kk = 0; kk < kSl - 1; ++kk) {
       if (kk == 0) issue_a(an, k + 1);
@@ -399,7 +455,8 @@ __global__ __launch_bounds__(2 * T, 2) void linear_tile_kernel(TileParams p) {
       read(nxt, a, b, kk + 1);
       mma(cur, Z0{}, ZF{});
       cur = nxt;
-      if (kk <= 1) sched_slice<4, kNR, kNM, 2>();
+      if (kk == 0) sched_slice<LdA::J, kNR, kNM, 2>();
+      else if (kk == 1) sched_slice<LdB::J, kNR, kNM, 2>();
       else sched_slice<0, kNR, kNM, 1>();
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -411,39 +468,35 @@ __global__ __launch_bounds__(2 * T, 2) void linear_tile_kernel(TileParams p) {
     read(nxt, an, bn, 0);
     mma(cur, ZH{}, ZF{});
     cur = nxt;
-    sched_slice<0, kNR, kNM / 2, 1>();
+    sched_slice<0, kNR, kNM - MI / 2 * NJ, 1>();
     __builtin_amdgcn_sched_barrier(0);
+    ++k;
   };
-  // prologue: B_0 into buffer 0, A_0 into buffer 1, then B_1 into buffer 2
-  // (left in flight)
-  issue_b(s0, 0);
-  issue_a(s1, 0);
-  issue_b(s2, 1);
+  // prologue: B_0 and A_0, then B_1 (left in flight)
+  issue_b(b0, 0);
+  issue_a(a0, 0);
+  issue_b(b1, 1);
   publish();
-  read(cur, s1, s0, 0);
-  const int trips = nk / 5, rem = nk - 5 * trips;
-  for (int tr = 0; tr < trips; ++tr) {
+  read(cur, a0, b0, 0);
+  for (int tr = nk / 6; tr > 0; --tr) {
     rstep(integral_constant<int, 0>{});
-    ++k;
     rstep(integral_constant<int, 1>{});
-    ++k;
     rstep(integral_constant<int, 2>{});
-    ++k;
     rstep(integral_constant<int, 3>{});
-    ++k;
     rstep(integral_constant<int, 4>{});
-    ++k;
+    rstep(integral_constant<int, 5>{});
   }
+  const int rem = nk % 6;
   if (rem > 0) {
     rstep(integral_constant<int, 0>{});
-    ++k;
     if (rem > 1) {
       rstep(integral_constant<int, 1>{});
-      ++k;
       if (rem > 2) {
         rstep(integral_constant<int, 2>{});
-        ++k;
-        if (rem > 3) rstep(integral_constant<int, 3>{});
+        if (rem > 3) {
+          rstep(integral_constant<int, 3>{});
+          if (rem > 4) rstep(integral_constant<int, 4>{});
+        }
       }
     }
   }
@@ -451,15 +504,17 @@ __global__ __launch_bounds__(2 * T, 2) void linear_tile_kernel(TileParams p) {
   // every wave is past its last read of the buffers (and every direct load
   // has landed) before they become epilogue staging
   __syncthreads();
-  // Two passes of 32 columns through the wave's own LDS: float32, 128-byte
+  // Passes of 32 columns through the wave's own LDS: float32, 128-byte
   // rows, 16-byte chunk c of row r at c ^ (r & 7); on readback lane l takes
   // columns 8 (l % 4) .. + 7 of row 16 q + l / 4.
   constexpr int kRows = 32 * MI;
   constexpr int kWaveBytes = kRows * 128;
-  constexpr int kPerBuf = kStage / kWaveBytes;
-  char* const wbuf =
-      (wave / kPerBuf == 0 ? s0 : wave / kPerBuf == 1 ? s1
-       : wave / kPerBuf == 2 ? s2 : s3) + (wave % kPerBuf) * kWaveBytes;
+  constexpr int kPerB = TN * 128 / kWaveBytes;   // waves per B buffer
+  static_assert(NW <= 3 * kPerB || (NW <= 4 * kPerB && TM == TN),
+                "staging fits the buffers");
+  char* wbuf = wave / kPerB == 0 ? b0 : wave / kPerB == 1 ? b1 : b2;
+  if constexpr (NW > 3 * kPerB) wbuf = wave / kPerB == 3 ? a0 : wbuf;
+  wbuf += (wave % kPerB) * kWaveBytes;
   const int colw = lane & 31, c4 = lane & 3;
   const int64_t rw = m0 + wm * kRows;
   float* const part = p.splits > 1 ? p.part + (int64_t)split * p.M * p.ldp
@@ -476,7 +531,10 @@ __global__ __launch_bounds__(2 * T, 2) void linear_tile_kernel(TileParams p) {
                                   (colw & 3) * 4) = acc[i][pass][r];
       }
     __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): staging written
-    const int col = n0 + wn * 64 + 32 * pass + 8 * c4;
+    const int col = n0 + wn * (32 * NJ) + 32 * pass + 8 * c4;
+    float bias[8];
+    bias8(p, col, bias);
+    int64_t at = (rw + (lane >> 2)) * p.ldc + col;
 #pragma unroll 2
     for (int q = 0; q < kRows / 16; ++q) {
       const int lr = 16 * q + (lane >> 2);
@@ -485,7 +543,7 @@ __global__ __launch_bounds__(2 * T, 2) void linear_tile_kernel(TileParams p) {
       const float4 v1 = *reinterpret_cast<const float4*>(
           wbuf + lr * 128 + (((2 * c4 + 1) ^ (lr & 7)) << 4));
       const int64_t row = rw + lr;
-      if (row >= p.M) continue;
+      if (row >= p.M) break;   // (and so are the lane's later rows)
       if (part) {
         if (col < p.ldp) {   // ldp % 8 == 0
           float* o = part + row * p.ldp + col;
@@ -494,11 +552,13 @@ __global__ __launch_bounds__(2 * T, 2) void linear_tile_kernel(TileParams p) {
         }
       } else {
         const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-        finish8(p, row, col, v);
+        finish8(p, at, col, v, bias);
+        at += 16 * p.ldc;
       }
     }
     __builtin_amdgcn_s_waitcnt(0xc07f);   // readback done before reuse
   }
+#endif
 }
 
 }  // namespace lin

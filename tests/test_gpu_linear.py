@@ -143,6 +143,17 @@ def test_larger(m, M, N, K):
     check_bwd(m, d, "gelu_tanh")
 
 
+@pytest.mark.parametrize("M,N,K", [
+    (1, 9000, 264), (16, 4100, 4104), (7, 5, 14336), (32, 16401, 72),
+    (17, 400, 4096), (33, 16500, 64), (64, 1000, 2056), (48, 20000, 520)])
+def test_few_rows(m, M, N, K):
+    """Every wave count and row-block form of the one-pass kernel, with
+    ragged weight rows and K tails inside and between its trips."""
+    d = make(M, N, K, 5)
+    check_fwd(m, d, "gelu", bias=True, res=True, save=True)
+    check_fwd(m, d, "none", bias=False, res=False, save=False)
+
+
 @pytest.mark.parametrize("want", [(1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 1, 0)])
 def test_partial_gradients(m, want):
     d = make(100, 90, 64, 4)
