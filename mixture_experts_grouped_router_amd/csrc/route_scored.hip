@@ -221,9 +221,12 @@ __device__ __forceinline__ double exp_neg(double a) {
   return __builtin_ldexp(p, a > 709.78 ? -4000 : (int)n);
 }
 
-// 1 / x for 1 <= x <= 2^11: the hardware estimate and two Newton steps
+// 1 / x for 1 <= x <= 2^11: the hardware estimate, two Newton steps to
+// within an ulp, and a third that rounds correctly (saturated scores differ
+// in their last bits only, and the order of those bits is the selection)
 __device__ __forceinline__ double recip(double x) {
   double y = __builtin_amdgcn_rcp(x);
+  y = fma(fma(-x, y, 1.0), y, y);
   y = fma(fma(-x, y, 1.0), y, y);
   return fma(fma(-x, y, 1.0), y, y);
 }

@@ -69,6 +69,9 @@ SHAPES = [
     (20, 256, 16, 2, 1), (6, 256, 17, 8, 8), (7, 20, 3, 10, 2),
     (11, 300, 9, 5, 3), (5, 1024, 32, 16, 4), (3, 1024, 8, 64, 8),
     (4, 100, 20, 4, 1), (2, 513, 5, 27, 5),
+    # lists of 2, 8 and 16 over 4, 8 and 16 experts per lane
+    (50, 100, 2, 1, 1), (50, 200, 1, 1, 1), (50, 256, 2, 16, 3),
+    (50, 128, 12, 8, 3), (50, 130, 16, 1, 1), (50, 64, 13, 1, 1),
 ]
 
 
@@ -121,6 +124,24 @@ def test_extreme_logits(m, score):
                   renormalize=ren)
     idx, w = run(m, lg, 4, score=score)
     assert bool(torch.isfinite(w).all())
+
+
+@pytest.mark.parametrize("E,k,G,tg", [(128, 8, 1, 1), (128, 8, 8, 4),
+                                      (40, 6, 1, 1), (60, 6, 3, 2),
+                                      (256, 16, 8, 4), (300, 9, 5, 3)])
+def test_scores_that_differ_in_their_last_bits(m, E, k, G, tg):
+    """Saturated sigmoids: keys that agree in their upper 42 bits and differ
+    (or do not) below, in every token and in one token of many."""
+    rng = np.random.default_rng(E)
+    lg = (24 + 13 * rng.random((48, E))).astype(np.float32)
+    mixed = rng.standard_normal((48, E)).astype(np.float32)
+    mixed[17] = lg[17]
+    for a in (lg, mixed):
+        for bias in (np.zeros(E, np.float32),
+                     (rng.integers(0, 2, E) * 2.0 ** -44).astype(np.float32)):
+            for gs in ("max", "top2") if G > 1 else ("max",):
+                check(m, a, k, bias=bias, score="sigmoid", n_group=G,
+                      topk_group=tg, group_score=gs)
 
 
 @pytest.mark.parametrize("E,G,tg", [(128, 1, 1), (64, 4, 2), (60, 3, 2),
