@@ -83,6 +83,7 @@ Plan plan_product(int64_t M, int64_t N, int64_t K) {
 
 // Sum of the split partials in split order, then the epilogue; a thread
 // takes 8 columns of a row.
+template <int ACT>
 __global__ __launch_bounds__(256) void linear_reduce_kernel(TileParams p) {
   const int64_t runs = p.ldp / 8;
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -100,10 +101,25 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(TileParams p) {
   }
   float b[8];
   bias8(p, col, b);
-  finish8(p, row * p.ldc + col, col, v, b);
+  finish8<ACT>(p, row * p.ldc + col, col, v, b);
 }
 
-template <int LA, int LB>
+template <int LA, int LB, int EPI>
+void launch_tiles(const TileParams& p, const Plan& pl, unsigned grid,
+                  hipStream_t stream) {
+  if (pl.tm == 256)
+    hipLaunchKernelGGL((linear_tile_kernel<256, 256, LA, LB, EPI>),
+                       dim3(grid), dim3(512), 0, stream, p);
+  else if (pl.tm == 128)
+    hipLaunchKernelGGL((linear_tile_kernel<128, 128, LA, LB, EPI>),
+                       dim3(grid), dim3(256), 0, stream, p);
+  else
+    hipLaunchKernelGGL((linear_tile_kernel<64, 128, LA, LB, EPI>),
+                       dim3(grid), dim3(256), 0, stream, p);
+}
+
+// ACT: the activation, or kEpiPlain for a gradient (a bf16 store alone).
+template <int LA, int LB, int ACT>
 hipError_t launch_product(const char* name, TileParams p, const Plan& pl,
                           void* part, hipStream_t stream) {
   p.tiles_m = (int)cdiv(p.M, pl.tm);
@@ -115,21 +131,14 @@ hipError_t launch_product(const char* name, TileParams p, const Plan& pl,
   const unsigned grid = (unsigned)(cdiv(total, gg::kXcds) * gg::kXcds);
   {
     KernelScope ks(name, stream);
-    if (pl.tm == 256)
-      hipLaunchKernelGGL((linear_tile_kernel<256, 256, LA, LB>), dim3(grid),
-                         dim3(512), 0, stream, p);
-    else if (pl.tm == 128)
-      hipLaunchKernelGGL((linear_tile_kernel<128, 128, LA, LB>), dim3(grid),
-                         dim3(256), 0, stream, p);
-    else
-      hipLaunchKernelGGL((linear_tile_kernel<64, 128, LA, LB>), dim3(grid),
-                         dim3(256), 0, stream, p);
+    if (pl.S > 1) launch_tiles<LA, LB, kEpiPlain>(p, pl, grid, stream);
+    else launch_tiles<LA, LB, ACT>(p, pl, grid, stream);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || pl.S == 1) return e;
   KernelScope ks("linear_split_reduce", stream);
   const int64_t threads = p.M * (p.ldp / 8);
-  hipLaunchKernelGGL(linear_reduce_kernel,
+  hipLaunchKernelGGL((linear_reduce_kernel<(ACT < 0 ? ACT_NONE : ACT)>),
                      dim3((unsigned)cdiv(threads, 256)), dim3(256), 0, stream,
                      p);
   return hipGetLastError();
@@ -318,8 +327,20 @@ hipError_t launch_linear_fwd(int64_t M, int N, int K, int act, const void* x,
   p.z = static_cast<uint16_t*>(z_save);
   p.act = act;
   if (is_skinny(M, N, K)) return launch_skinny(p, stream);
-  return launch_product<KC, KC>("linear_fwd", p, plan_product(M, N, K), ws,
-                                stream);
+  const Plan pl = plan_product(M, N, K);
+  switch (act) {
+    case ACT_RELU:
+      return launch_product<KC, KC, ACT_RELU>("linear_fwd", p, pl, ws, stream);
+    case ACT_GELU:
+      return launch_product<KC, KC, ACT_GELU>("linear_fwd", p, pl, ws, stream);
+    case ACT_GELU_TANH:
+      return launch_product<KC, KC, ACT_GELU_TANH>("linear_fwd", p, pl, ws,
+                                                   stream);
+    case ACT_SILU:
+      return launch_product<KC, KC, ACT_SILU>("linear_fwd", p, pl, ws, stream);
+    default:
+      return launch_product<KC, KC, ACT_NONE>("linear_fwd", p, pl, ws, stream);
+  }
 }
 
 // The dz buffer is skipped where dy can be the products' operand itself.
@@ -408,7 +429,7 @@ hipError_t launch_linear_bwd(int64_t M, int N, int K, int act, const void* dy,
     p.K = N;
     p.c = static_cast<uint16_t*>(dx);
     p.ldc = K;
-    e = launch_product<KC, MC>("linear_dgrad", p, plan_product(M, K, N), wp,
+    e = launch_product<KC, MC, kEpiPlain>("linear_dgrad", p, plan_product(M, K, N), wp,
                                stream);
     if (e != hipSuccess) return e;
   }
@@ -423,7 +444,7 @@ hipError_t launch_linear_bwd(int64_t M, int N, int K, int act, const void* dy,
     p.K = M;
     p.c = static_cast<uint16_t*>(dw);
     p.ldc = K;
-    e = launch_product<MC, MC>("linear_wgrad", p, plan_product(N, K, M), wp,
+    e = launch_product<MC, MC, kEpiPlain>("linear_wgrad", p, plan_product(N, K, M), wp,
                                stream);
   }
   return e;

@@ -75,26 +75,7 @@ __device__ __forceinline__ float act_grad(float z) {
   }
 }
 
-// y = act(z) for 8 values; act is uniform
-__device__ __forceinline__ void act_fwd8(int act, const float (&z)[8],
-                                         float (&y)[8]) {
-#define MOE_ACT_CASE(A)                                 \
-  case A:                                               \
-    _Pragma("unroll") for (int i = 0; i < 8; ++i)       \
-        y[i] = act_fwd<A>(z[i]);                        \
-    break;
-  switch (act) {
-    MOE_ACT_CASE(ACT_RELU)
-    MOE_ACT_CASE(ACT_GELU)
-    MOE_ACT_CASE(ACT_GELU_TANH)
-    MOE_ACT_CASE(ACT_SILU)
-    default:
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = z[i];
-  }
-#undef MOE_ACT_CASE
-}
-
+// act is uniform
 __device__ __forceinline__ float act_fwd1(int act, float z) {
   switch (act) {
     case ACT_RELU: return act_fwd<ACT_RELU>(z);
@@ -103,26 +84,6 @@ __device__ __forceinline__ float act_fwd1(int act, float z) {
     case ACT_SILU: return act_fwd<ACT_SILU>(z);
     default: return z;
   }
-}
-
-// d = act'(z) for 8 values
-__device__ __forceinline__ void act_grad8(int act, const float (&z)[8],
-                                          float (&d)[8]) {
-#define MOE_ACT_CASE(A)                                 \
-  case A:                                               \
-    _Pragma("unroll") for (int i = 0; i < 8; ++i)       \
-        d[i] = act_grad<A>(z[i]);                       \
-    break;
-  switch (act) {
-    MOE_ACT_CASE(ACT_RELU)
-    MOE_ACT_CASE(ACT_GELU)
-    MOE_ACT_CASE(ACT_GELU_TANH)
-    MOE_ACT_CASE(ACT_SILU)
-    default:
-#pragma unroll
-      for (int i = 0; i < 8; ++i) d[i] = 1.0f;
-  }
-#undef MOE_ACT_CASE
 }
 
 }  // namespace lin

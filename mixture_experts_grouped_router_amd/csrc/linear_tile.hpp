@@ -221,9 +221,9 @@ __device__ __forceinline__ void finish1(const TileParams& p, int64_t row,
 typedef uint32_t u32x4_a2_t __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x4_a4_t __attribute__((ext_vector_type(4), aligned(4)));
 
-// One 8-value run of an output row: bias, activation, residual, rounding.
+// Runs of 8 values of an output row: bias, activation, residual, rounding.
 // The activation is applied to the float32 value; the sum with the residual
-// is rounded to bf16 once.
+// is rounded to bf16 once.  Bias of a run:
 __device__ __forceinline__ void bias8(const TileParams& p, int col,
                                       float (&b)[8]) {
   f32x4_a4_t b0 = {0, 0, 0, 0}, b1 = b0;
@@ -246,45 +246,57 @@ __device__ __forceinline__ void bias8(const TileParams& p, int col,
   }
 }
 
-// at: the run's first element in the output; b: its bias
-__device__ __forceinline__ void finish8(const TileParams& p, int64_t at,
-                                        int col, const float (&v)[8],
-                                        const float (&b)[8]) {
+__device__ __forceinline__ u32x4_a2_t pack8(const float (&v)[8]) {
+  return u32x4_a2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                    pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+}
+
+// A whole run at element `at` of the output, b its bias, r its residual
+// (read only where there is one).
+template <int ACT>
+__device__ __forceinline__ void finish_run(const TileParams& p, int64_t at,
+                                           const float (&v)[8],
+                                           const float (&b)[8],
+                                           const u32x4_a2_t& r) {
   float z[8], y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) z[i] = v[i] + b[i];
+  if (p.z) *reinterpret_cast<u32x4_a2_t*>(p.z + at) = pack8(z);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = act_fwd<ACT>(z[i]);
+  if (p.res) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[2 * i] += bf16lo(r[i]);
+      y[2 * i + 1] += bf16hi(r[i]);
+    }
+  }
+  *reinterpret_cast<u32x4_a2_t*>(p.c + at) = pack8(y);
+}
+
+// A run that may cross the row's end (or lie behind it).
+template <int ACT>
+__device__ __forceinline__ void finish8(const TileParams& p, int64_t at,
+                                        int col, const float (&v)[8],
+                                        const float (&b)[8]) {
   if (col + 8 <= p.N) {
     u32x4_a2_t r = {0, 0, 0, 0};
     if (p.res) r = *reinterpret_cast<const u32x4_a2_t*>(p.res + at);
-    if (p.z) {
-      const u32x4_a2_t o = {pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]),
-                            pack_bf16x2(z[4], z[5]), pack_bf16x2(z[6], z[7])};
-      *reinterpret_cast<u32x4_a2_t*>(p.z + at) = o;
-    }
-    act_fwd8(p.act, z, y);
-    if (p.res) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        y[2 * i] += bf16lo(r[i]);
-        y[2 * i + 1] += bf16hi(r[i]);
-      }
-    }
-    const u32x4_a2_t o = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                          pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7])};
-    *reinterpret_cast<u32x4_a2_t*>(p.c + at) = o;
-  } else if (col < p.N) {   // the row's tail
+    finish_run<ACT>(p, at, v, b, r);
+  } else if (col < p.N) {
     const int n = p.N - col;
     uint16_t r[8] = {};
-    if (p.res)
+    if (p.res)   // (loads clamped: a branch around each would serialise them)
 #pragma unroll
       for (int i = 0; i < 8; ++i) r[i] = p.res[at + min(i, n - 1)];
-    act_fwd8(p.act, z, y);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (p.res) y[i] += bf16_to_f32(r[i]);
+      const float z = v[i] + b[i];
+      float y = act_fwd<ACT>(z);
+      if (p.res) y += bf16_to_f32(r[i]);
       if (i < n) {
-        if (p.z) p.z[at + i] = (uint16_t)f32_to_bf16(z[i]);
-        p.c[at + i] = (uint16_t)f32_to_bf16(y[i]);
+        if (p.z) p.z[at + i] = (uint16_t)f32_to_bf16(z);
+        p.c[at + i] = (uint16_t)f32_to_bf16(y);
       }
     }
   }
@@ -301,7 +313,11 @@ struct TileShape {
   static constexpr int NJ = TN / WN / 32;   // 32-column B blocks
 };
 
-template <int TM, int TN, int LA, int LB>
+// EPI: the activation of a forward product, or kEpiPlain: float32 partials
+// where p.splits > 1, else a bf16 store alone (no bias, residual, save).
+constexpr int kEpiPlain = -1;
+
+template <int TM, int TN, int LA, int LB, int EPI>
 __global__ __launch_bounds__((64 * TileShape<TM, TN>::NW), 2) void
 linear_tile_kernel(TileParams p) {
 #ifdef __HIP_DEVICE_COMPILE__   // (the host pass needs the launch stub only)
@@ -517,10 +533,31 @@ linear_tile_kernel(TileParams p) {
   wbuf += (wave % kPerB) * kWaveBytes;
   const int colw = lane & 31, c4 = lane & 3;
   const int64_t rw = m0 + wm * kRows;
-  float* const part = p.splits > 1 ? p.part + (int64_t)split * p.M * p.ldp
-                                   : nullptr;
+  constexpr int kQ = kRows / 16;
+  const int lrow = lane >> 2;               // row 16 q + lrow
+  float* const part = EPI == kEpiPlain && p.splits > 1
+                          ? p.part + (int64_t)split * p.M * p.ldp
+                          : nullptr;
+  // (uniform) no run of the tile crosses the row's end
+  const bool whole = n0 + TN <= p.N;
 #pragma unroll
   for (int pass = 0; pass < NJ; ++pass) {
+    const int col = n0 + wn * (32 * NJ) + 32 * pass + 8 * c4;
+    const int64_t at0 = (rw + lrow) * p.ldc + col;
+    // the residual's loads go out ahead of the staging
+    [[maybe_unused]] u32x4_a2_t res[kQ];
+    [[maybe_unused]] float bias[8];
+    if constexpr (EPI != kEpiPlain) {
+      bias8(p, col, bias);
+      if (whole && p.res) {
+#pragma unroll
+        for (int q = 0; q < kQ; ++q) {
+          const int64_t r = min((int64_t)(16 * q), p.M - 1 - rw - lrow);
+          res[q] = *reinterpret_cast<const u32x4_a2_t*>(
+              p.res + (r < 0 ? col : at0 + r * p.ldc));
+        }
+      }
+    }
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -531,29 +568,54 @@ linear_tile_kernel(TileParams p) {
                                   (colw & 3) * 4) = acc[i][pass][r];
       }
     __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): staging written
-    const int col = n0 + wn * (32 * NJ) + 32 * pass + 8 * c4;
-    float bias[8];
-    bias8(p, col, bias);
-    int64_t at = (rw + (lane >> 2)) * p.ldc + col;
-#pragma unroll 2
-    for (int q = 0; q < kRows / 16; ++q) {
-      const int lr = 16 * q + (lane >> 2);
+    auto staged = [&](int q, float (&v)[8]) {
+      const int lr = 16 * q + lrow;
       const float4 v0 = *reinterpret_cast<const float4*>(
           wbuf + lr * 128 + (((2 * c4) ^ (lr & 7)) << 4));
       const float4 v1 = *reinterpret_cast<const float4*>(
           wbuf + lr * 128 + (((2 * c4 + 1) ^ (lr & 7)) << 4));
-      const int64_t row = rw + lr;
-      if (row >= p.M) break;   // (and so are the lane's later rows)
-      if (part) {
-        if (col < p.ldp) {   // ldp % 8 == 0
+      v[0] = v0.x; v[1] = v0.y; v[2] = v0.z; v[3] = v0.w;
+      v[4] = v1.x; v[5] = v1.y; v[6] = v1.z; v[7] = v1.w;
+    };
+    if (part) {
+      if (col < p.ldp) {   // ldp % 8 == 0
+#pragma unroll
+        for (int q = 0; q < kQ; ++q) {
+          const int64_t row = rw + 16 * q + lrow;
+          if (row >= p.M) break;
+          float v[8];
+          staged(q, v);
           float* o = part + row * p.ldp + col;
-          *reinterpret_cast<float4*>(o) = v0;
-          *reinterpret_cast<float4*>(o + 4) = v1;
+          *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<float4*>(o + 4) =
+              make_float4(v[4], v[5], v[6], v[7]);
         }
-      } else {
-        const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-        finish8(p, at, col, v, bias);
-        at += 16 * p.ldc;
+      }
+    } else if (whole) {
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) {
+        const int64_t at = at0 + (int64_t)(16 * q) * p.ldc;
+        float v[8];
+        staged(q, v);
+        if (rw + 16 * q + lrow >= p.M) break;
+        if constexpr (EPI == kEpiPlain) {
+          *reinterpret_cast<u32x4_a2_t*>(p.c + at) = pack8(v);
+        } else {
+          finish_run<EPI>(p, at, v, bias, res[q]);
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (int q = 0; q < kQ; ++q) {
+        if (rw + 16 * q + lrow >= p.M) break;
+        float v[8];
+        staged(q, v);
+        if constexpr (EPI == kEpiPlain) {
+          float none[8] = {};
+          finish8<ACT_NONE>(p, at0 + (int64_t)(16 * q) * p.ldc, col, v, none);
+        } else {
+          finish8<EPI>(p, at0 + (int64_t)(16 * q) * p.ldc, col, v, bias);
+        }
       }
     }
     __builtin_amdgcn_s_waitcnt(0xc07f);   // readback done before reuse
