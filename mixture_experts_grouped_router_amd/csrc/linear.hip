@@ -41,18 +41,19 @@ struct Plan {
 // of work-groups that puts c of them on a CU takes
 //   steps * max(lat, thr c) + fix c
 // microseconds (lat: one K step with a CU to itself, thr: its share of a
-// busy CU, fix: prologue and epilogue); a split adds a launch and the
-// float32 partials' round trip at 8 TB/s (they mostly stay in the caches).
-// The constants are a least-squares fit to 900 timed (shape, tile, split)
-// combinations of the three products; the choice is then 2.4% slower than the
-// best combination on average, 24% at worst (a 14 us call).
+// busy CU, fix: prologue and epilogue; the 64 x 64 tile takes four steps at a
+// time); a split adds a launch and the float32 partials' round trip at 6
+// TB/s (they mostly stay in the caches).  The constants come from 1200 timed
+// (shape, tile, split) combinations of the three products; the choice is 2%
+// slower than the best combination on average.
 Plan plan_product(int64_t M, int64_t N, int64_t K) {
   static const struct {
-    int tm, tn, per_cu;
+    int tm, tn, per_cu, groups;
     double lat, thr, fix;
-  } kTiles[] = {{256, 256, 1, 1.17, 0.0, 9.0},
-                {128, 128, 2, 0.51, 0.43, 2.8},
-                {64, 128, 2, 0.42, 0.31, 1.9}};
+  } kTiles[] = {{256, 256, 1, 1, 1.2, 0.0, 11.0},
+                {128, 128, 2, 1, 0.53, 0.46, 2.6},
+                {64, 128, 2, 1, 0.45, 0.33, 1.8},
+                {64, 64, 1, 4, 1.05, 0.0, 2.0}};
   const int64_t steps = cdiv(K, 64);
   Plan best{128, 128, 1};
   double best_us = 1e30;
@@ -63,7 +64,7 @@ Plan plan_product(int64_t M, int64_t N, int64_t K) {
       if (S > 1 && (S * 2 > steps ||
                     (int64_t)S * M * pad8(N) * 4 > kMaxPartBytes))
         break;
-      const double st = (double)cdiv(steps, S);
+      const double st = (double)cdiv(cdiv(steps, S), c.groups);
       auto round_us = [&](int64_t groups) {
         const double occ = (double)cdiv(groups, kCus);
         return st * std::max(c.lat, c.thr * occ) + c.fix * occ;
@@ -71,7 +72,7 @@ Plan plan_product(int64_t M, int64_t N, int64_t K) {
       const int64_t last = tiles * S % slots;
       double us = (double)(tiles * S / slots) * round_us(slots);
       if (last) us += round_us(last);
-      if (S > 1) us += 3.2 + (double)S * M * N * 1e-6;
+      if (S > 1) us += 4.5 + (double)S * M * N * 8.0 / 6e6;
       if (us < best_us) {
         best_us = us;
         best = Plan{c.tm, c.tn, S};
@@ -113,9 +114,12 @@ void launch_tiles(const TileParams& p, const Plan& pl, unsigned grid,
   else if (pl.tm == 128)
     hipLaunchKernelGGL((linear_tile_kernel<128, 128, LA, LB, EPI>),
                        dim3(grid), dim3(256), 0, stream, p);
-  else
+  else if (pl.tn == 128)
     hipLaunchKernelGGL((linear_tile_kernel<64, 128, LA, LB, EPI>),
                        dim3(grid), dim3(256), 0, stream, p);
+  else
+    hipLaunchKernelGGL((linear_tile_kernel<64, 64, LA, LB, EPI>), dim3(grid),
+                       dim3(1024), 0, stream, p);
 }
 
 // ACT: the activation, or kEpiPlain for a gradient (a bf16 store alone).

@@ -9,8 +9,8 @@
 //
 // Tiles: 256 x 256 (eight waves, one work-group per CU) where the product
 // fills the chip with them, else 128 x 128 or 64 x 128 (four waves, two
-// work-groups per CU); each may split K over S work-groups that write
-// float32 partial tiles.
+// work-groups per CU), or 64 x 64 with K dealt to four groups of four waves;
+// each may split K over S work-groups that write float32 partial tiles.
 //
 // Any M and N; K in multiples of 8 (16-byte chunks).  Rows past the end and
 // the K tail of the last step read as zeros: their byte offsets lie past the
@@ -302,13 +302,20 @@ __device__ __forceinline__ void finish8(const TileParams& p, int64_t at,
   }
 }
 
-// The wave grid of a tile: 256 x 256, 2 x 4 waves of 128 x 64; 128 x 128,
-// 2 x 2 of 64 x 64; 64 x 128, 1 x 4 of 64 x 32.
+// The waves of a tile: 256 x 256, 2 x 4 waves of 128 x 64; 128 x 128, 2 x 2
+// of 64 x 64; 64 x 128, 1 x 4 of 64 x 32; 64 x 64, 2 x 2 of 32 x 32, and four
+// such groups, each with a quarter of the K steps and its own LDS stages,
+// that add up through LDS: for products with few tiles, whose time is the
+// latency of their K steps.
 template <int TM, int TN>
 struct TileShape {
-  static constexpr int WM = TM == 64 ? 1 : 2;
-  static constexpr int WN = TN == 256 || TM == 64 ? 4 : 2;
-  static constexpr int NW = WM * WN;
+  static constexpr bool kWide = TM == 64 && TN == 128;
+  static constexpr int WM = kWide ? 1 : 2;
+  static constexpr int WN = TN == 256 || kWide ? 4 : 2;
+  static constexpr int NW = WM * WN;        // waves per group
+  static constexpr int G = TM == 64 && TN == 64 ? 4 : 1;   // K groups
+  static constexpr int kThreads = 64 * NW * G;
+  static constexpr int kWavesPerSimd = G > 1 ? 4 : 2;
   static constexpr int MI = TM / WM / 32;   // 32-row A blocks of a wave
   static constexpr int NJ = TN / WN / 32;   // 32-column B blocks
 };
@@ -318,32 +325,42 @@ struct TileShape {
 constexpr int kEpiPlain = -1;
 
 template <int TM, int TN, int LA, int LB, int EPI>
-__global__ __launch_bounds__((64 * TileShape<TM, TN>::NW), 2) void
+__global__ __launch_bounds__((TileShape<TM, TN>::kThreads),
+                             (TileShape<TM, TN>::kWavesPerSimd)) void
 linear_tile_kernel(TileParams p) {
 #ifdef __HIP_DEVICE_COMPILE__   // (the host pass needs the launch stub only)
   using S = TileShape<TM, TN>;
-  constexpr int MI = S::MI, NJ = S::NJ, WN = S::WN, NW = S::NW;
+  constexpr int MI = S::MI, NJ = S::NJ, WN = S::WN, NW = S::NW, G = S::G;
   constexpr int kSl = 4;               // 16-wide K slices per 64-wide step
   // B of three steps, A of two
-  __shared__ __attribute__((aligned(1024))) char b0[TN * 128];
-  __shared__ __attribute__((aligned(1024))) char b1[TN * 128];
-  __shared__ __attribute__((aligned(1024))) char b2[TN * 128];
-  __shared__ __attribute__((aligned(1024))) char a0[TM * 128];
-  __shared__ __attribute__((aligned(1024))) char a1[TM * 128];
+  __shared__ __attribute__((aligned(1024))) char b0[G * TN * 128];
+  __shared__ __attribute__((aligned(1024))) char b1[G * TN * 128];
+  __shared__ __attribute__((aligned(1024))) char b2[G * TN * 128];
+  __shared__ __attribute__((aligned(1024))) char a0[G * TM * 128];
+  __shared__ __attribute__((aligned(1024))) char a1[G * TM * 128];
   int tm, tn, split;
   if (!tile_of(p, tm, tn, split)) return;
   const int t = threadIdx.x;
   const int lane = t & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wave_id = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wave = G == 1 ? wave_id : wave_id % NW;   // in its group
+  const int grp = G == 1 ? 0 : wave_id / NW;
   const int wm = wave / WN, wn = wave % WN;
   const int64_t m0 = (int64_t)tm * TM;
   const int n0 = tn * TN;
 
-  // K steps [ks, ke) of this work-group
+  // K steps [ks, ke) of this work-group (group); nk: those of the longest
+  // group, steps past ke read zeros
   const int nk_all = (int)((p.K + 63) / 64);
-  const int ks = (int)((int64_t)split * nk_all / p.splits);
-  const int ke = (int)((int64_t)(split + 1) * nk_all / p.splits);
-  const int nk = ke - ks;
+  int ks = (int)((int64_t)split * nk_all / p.splits);
+  int ke = (int)((int64_t)(split + 1) * nk_all / p.splits);
+  int nk = ke - ks;
+  if constexpr (G > 1) {
+    nk = (nk + G - 1) / G;
+    ks += grp * nk;
+    ke = max(ks, min(ke, ks + nk));
+  }
+  const int own = ke - ks;
 
   using LdA = std::conditional_t<LA == KC, KcLoad<TM, NW>, McLoad<TM, NW>>;
   using LdB = std::conditional_t<LB == KC, KcLoad<TN, NW>, McLoad<TN, NW>>;
@@ -354,10 +371,10 @@ linear_tile_kernel(TileParams p) {
   if constexpr (LB == KC) db.init(p.b, p.ldb, n0, p.N, p.K, wave, lane);
   else db.init(p.b, p.ldb, n0, p.K, wave, lane);
   auto issue_a = [&](char* dst, int kt) {
-    da.issue(dst, ks + kt, kt < nk, wave);
+    da.issue(dst, ks + kt, kt < own, wave);
   };
   auto issue_b = [&](char* dst, int kt) {
-    db.issue(dst, ks + kt, kt < nk, wave);
+    db.issue(dst, ks + kt, kt < own, wave);
   };
 
   f32x16_t acc[MI][NJ];
@@ -369,14 +386,16 @@ linear_tile_kernel(TileParams p) {
   using std::integral_constant;
   auto bufb = [&](auto nc) -> char* {
     constexpr int n = decltype(nc)::value % 3;
-    if constexpr (n == 0) return b0;
-    else if constexpr (n == 1) return b1;
-    else return b2;
+    if constexpr (n == 0) return b0 + grp * (TN * 128);
+    else if constexpr (n == 1) return b1 + grp * (TN * 128);
+    else return b2 + grp * (TN * 128);
   };
   auto bufa = [&](auto nc) -> char* {
-    if constexpr (decltype(nc)::value % 2 == 0) return a0;
-    else return a1;
+    if constexpr (decltype(nc)::value % 2 == 0) return a0 + grp * (TM * 128);
+    else return a1 + grp * (TM * 128);
   };
+  using I0 = integral_constant<int, 0>;
+  using I1 = integral_constant<int, 1>;
   // Fragment offsets, passed through an empty asm at each use so that the
   // compiler forms addresses when they are needed instead of holding one
   // per buffer, slice and operand.
@@ -489,11 +508,11 @@ linear_tile_kernel(TileParams p) {
     ++k;
   };
   // prologue: B_0 and A_0, then B_1 (left in flight)
-  issue_b(b0, 0);
-  issue_a(a0, 0);
-  issue_b(b1, 1);
+  issue_b(bufb(I0{}), 0);
+  issue_a(bufa(I0{}), 0);
+  issue_b(bufb(I1{}), 1);
   publish();
-  read(cur, a0, b0, 0);
+  read(cur, bufa(I0{}), bufb(I0{}), 0);
   for (int tr = nk / 6; tr > 0; --tr) {
     rstep(integral_constant<int, 0>{});
     rstep(integral_constant<int, 1>{});
@@ -520,6 +539,58 @@ linear_tile_kernel(TileParams p) {
   // every wave is past its last read of the buffers (and every direct load
   // has landed) before they become epilogue staging
   __syncthreads();
+  float* const part = EPI == kEpiPlain && p.splits > 1
+                          ? p.part + (int64_t)split * p.M * p.ldp
+                          : nullptr;
+  // one run of 8 columns of an output row, whichever the epilogue
+  auto run_out = [&](int64_t row, int col, const float (&v)[8]) {
+    if (row >= p.M) return;
+    const int64_t at = row * p.ldc + col;
+    if constexpr (EPI == kEpiPlain) {
+      if (part) {
+        if (col < p.ldp) {   // ldp % 8 == 0
+          float* o = part + row * p.ldp + col;
+          *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<float4*>(o + 4) =
+              make_float4(v[4], v[5], v[6], v[7]);
+        }
+      } else {
+        float none[8] = {};
+        finish8<ACT_NONE>(p, at, col, v, none);
+      }
+    } else {
+      float bias[8];
+      bias8(p, col, bias);
+      finish8<EPI>(p, at, col, v, bias);
+    }
+  };
+  if constexpr (G > 1) {
+    // the groups' float32 tiles side by side (256-byte rows, 16 KiB each in
+    // b0 and b1), then one run of 8 columns per thread, groups in order
+    static_assert(MI == 1 && NJ == 1 && TM == 64 && TN == 64 && G == 4,
+                  "group sums");
+    char* const mine = (grp < 2 ? b0 : b1) + (grp & 1) * (64 * 256);
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      *reinterpret_cast<float*>(
+          mine + (32 * wm + gg::acc_row(0, r, lane)) * 256 +
+          (32 * wn + (lane & 31)) * 4) = acc[0][0][r];
+    __syncthreads();
+    if (t < 512) {
+      const int row = t >> 3, c8 = t & 7;
+      float v[8] = {};
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const char* src =
+            (g < 2 ? b0 : b1) + (g & 1) * (64 * 256) + row * 256 + c8 * 32;
+        const float4 x = *reinterpret_cast<const float4*>(src);
+        const float4 y = *reinterpret_cast<const float4*>(src + 16);
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+      }
+      run_out(m0 + row, n0 + 8 * c8, v);
+    }
+  } else {
   // Passes of 32 columns through the wave's own LDS: float32, 128-byte
   // rows, 16-byte chunk c of row r at c ^ (r & 7); on readback lane l takes
   // columns 8 (l % 4) .. + 7 of row 16 q + l / 4.
@@ -535,9 +606,6 @@ linear_tile_kernel(TileParams p) {
   const int64_t rw = m0 + wm * kRows;
   constexpr int kQ = kRows / 16;
   const int lrow = lane >> 2;               // row 16 q + lrow
-  float* const part = EPI == kEpiPlain && p.splits > 1
-                          ? p.part + (int64_t)split * p.M * p.ldp
-                          : nullptr;
   // (uniform) no run of the tile crosses the row's end
   const bool whole = n0 + TN <= p.N;
 #pragma unroll
@@ -577,21 +645,7 @@ linear_tile_kernel(TileParams p) {
       v[0] = v0.x; v[1] = v0.y; v[2] = v0.z; v[3] = v0.w;
       v[4] = v1.x; v[5] = v1.y; v[6] = v1.z; v[7] = v1.w;
     };
-    if (part) {
-      if (col < p.ldp) {   // ldp % 8 == 0
-#pragma unroll
-        for (int q = 0; q < kQ; ++q) {
-          const int64_t row = rw + 16 * q + lrow;
-          if (row >= p.M) break;
-          float v[8];
-          staged(q, v);
-          float* o = part + row * p.ldp + col;
-          *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
-          *reinterpret_cast<float4*>(o + 4) =
-              make_float4(v[4], v[5], v[6], v[7]);
-        }
-      }
-    } else if (whole) {
+    if (whole && !part) {
 #pragma unroll
       for (int q = 0; q < kQ; ++q) {
         const int64_t at = at0 + (int64_t)(16 * q) * p.ldc;
@@ -605,20 +659,15 @@ linear_tile_kernel(TileParams p) {
         }
       }
     } else {
-#pragma unroll 1
+#pragma unroll 2
       for (int q = 0; q < kQ; ++q) {
-        if (rw + 16 * q + lrow >= p.M) break;
         float v[8];
         staged(q, v);
-        if constexpr (EPI == kEpiPlain) {
-          float none[8] = {};
-          finish8<ACT_NONE>(p, at0 + (int64_t)(16 * q) * p.ldc, col, v, none);
-        } else {
-          finish8<EPI>(p, at0 + (int64_t)(16 * q) * p.ldc, col, v, bias);
-        }
+        run_out(rw + 16 * q + lrow, col, v);
       }
     }
     __builtin_amdgcn_s_waitcnt(0xc07f);   // readback done before reuse
+  }
   }
 #endif
 }
