@@ -37,57 +37,139 @@ struct Plan {
   }
 };
 
-// Tile and split of an M x N x K product: the least estimated time.  A round
-// of work-groups that puts c of them on a CU takes
+// Estimated times, in microseconds.  A round of work-groups that puts c of
+// them on a CU takes
 //   steps * max(lat, thr c) + fix c
-// microseconds (lat: one K step with a CU to itself, thr: its share of a
-// busy CU, fix: prologue and epilogue; the 64 x 64 tile takes four steps at a
-// time); a split adds a launch and the float32 partials' round trip at 6
-// TB/s (they mostly stay in the caches).  The constants come from 1200 timed
-// (shape, tile, split) combinations of the three products; the choice is 2%
-// slower than the best combination on average.
-Plan plan_product(int64_t M, int64_t N, int64_t K) {
-  static const struct {
-    int tm, tn, per_cu, groups;
-    double lat, thr, fix;
-  } kTiles[] = {{256, 256, 1, 1, 1.2, 0.0, 11.0},
-                {128, 128, 2, 1, 0.53, 0.46, 2.6},
-                {64, 128, 2, 1, 0.45, 0.33, 1.8},
-                {64, 64, 1, 4, 1.05, 0.0, 2.0}};
-  const int64_t steps = cdiv(K, 64);
+// (lat: one K step with a CU to itself, thr: its share of a busy CU, fix:
+// prologue and epilogue; the 64 x 64 tile takes four steps at a time); a
+// split adds a launch and the float32 partials' round trip at 6 TB/s (they
+// mostly stay in the caches).  The constants come from 1200 timed (shape,
+// tile, split) combinations of the three products; the choice is 2% slower
+// than the best combination on average.
+struct TileCost {
+  int tm, tn, per_cu, groups;
+  double lat, thr, fix;
+};
+constexpr TileCost kTiles[] = {{256, 256, 1, 1, 1.2, 0.0, 11.0},
+                               {128, 128, 2, 1, 0.53, 0.46, 2.6},
+                               {64, 128, 2, 1, 0.45, 0.33, 1.8},
+                               {64, 64, 1, 4, 1.05, 0.0, 2.0}};
+constexpr double kLaunchUs = 4.5;
+
+struct Product {
+  int64_t M, N, K;
+  int64_t groups(const TileCost& c, int S) const {
+    return cdiv(M, c.tm) * cdiv(N, c.tn) * S;
+  }
+  double steps(const TileCost& c, int S) const {
+    return (double)cdiv(cdiv(cdiv(K, 64), S), c.groups);
+  }
+  bool can_split(int S) const {
+    return S == 1 || (S * 2 <= cdiv(K, 64) &&
+                      (int64_t)S * M * pad8(N) * 4 <= kMaxPartBytes);
+  }
+  double partial_us(int S) const {
+    return S > 1 ? (double)S * M * N * 8.0 / 6e6 : 0.0;
+  }
+};
+
+// Tile and split of one product: the least estimated time, also in *us.
+Plan plan_product(int64_t M, int64_t N, int64_t K, double* us = nullptr) {
+  const Product p{M, N, K};
   Plan best{128, 128, 1};
   double best_us = 1e30;
   for (const auto& c : kTiles) {
-    const int64_t tiles = cdiv(M, c.tm) * cdiv(N, c.tn);
     const int64_t slots = (int64_t)kCus * c.per_cu;
-    for (int S = 1; S <= kMaxSplits; ++S) {
-      if (S > 1 && (S * 2 > steps ||
-                    (int64_t)S * M * pad8(N) * 4 > kMaxPartBytes))
-        break;
-      const double st = (double)cdiv(cdiv(steps, S), c.groups);
+    for (int S = 1; S <= kMaxSplits && p.can_split(S); ++S) {
+      const double st = p.steps(c, S);
       auto round_us = [&](int64_t groups) {
         const double occ = (double)cdiv(groups, kCus);
         return st * std::max(c.lat, c.thr * occ) + c.fix * occ;
       };
-      const int64_t last = tiles * S % slots;
-      double us = (double)(tiles * S / slots) * round_us(slots);
-      if (last) us += round_us(last);
-      if (S > 1) us += 4.5 + (double)S * M * N * 8.0 / 6e6;
-      if (us < best_us) {
-        best_us = us;
+      const int64_t n = p.groups(c, S), last = n % slots;
+      double t = (double)(n / slots) * round_us(slots);
+      if (last) t += round_us(last);
+      if (S > 1) t += kLaunchUs + p.partial_us(S);
+      if (t < best_us) {
+        best_us = t;
         best = Plan{c.tm, c.tn, S};
       }
     }
   }
+  if (us) *us = best_us;
   return best;
+}
+
+// Both gradient products of a linear layer: one launch of one tile shape for
+// both where that is estimated to be faster than two (small products leave
+// CUs idle, large ones their last round), else each by itself.
+struct GradPlan {
+  bool joint;
+  bool x_first;
+  Plan x, w;
+};
+GradPlan plan_grads(int64_t M, int N, int K) {
+  const Product px{M, K, N}, pw{N, K, M};
+  double ux, uw;
+  GradPlan best{false, true, plan_product(M, K, N, &ux),
+                plan_product(N, K, M, &uw)};
+  double best_us = ux + uw + kLaunchUs;
+  for (const auto& c : kTiles) {
+    const int64_t slots = (int64_t)kCus * c.per_cu;
+    // a work-group's share of its slot when the chip is full
+    auto full_us = [&](const Product& p, int S) {
+      return p.steps(c, S) * std::max(c.lat, c.thr * c.per_cu) +
+             c.fix * c.per_cu;
+    };
+    for (int sx = 1; sx <= kMaxSplits && px.can_split(sx); ++sx)
+      for (int sw = 1; sw <= kMaxSplits && pw.can_split(sw); ++sw) {
+        const double fx = full_us(px, sx), fw = full_us(pw, sw);
+        const double work = ((double)px.groups(c, sx) * fx +
+                             (double)pw.groups(c, sw) * fw) / slots;
+        const int64_t n = px.groups(c, sx) + pw.groups(c, sw);
+        // the shorter product's groups fill the tail of the longer one
+        double t = std::max(std::max(fx, fw), work + 0.5 * std::min(fx, fw));
+        if (n <= slots) t = std::max(fx, fw);   // one round
+        if (n <= kCus)
+          t = std::max(px.steps(c, sx), pw.steps(c, sw)) * c.lat + c.fix;
+        if (sx > 1 || sw > 1)
+          t += kLaunchUs + px.partial_us(sx) + pw.partial_us(sw);
+        if (t < best_us) {
+          best_us = t;
+          best = GradPlan{true, fx >= fw, Plan{c.tm, c.tn, sx},
+                          Plan{c.tm, c.tn, sw}};
+        }
+      }
+  }
+  return best;
+}
+
+// The plan of the last sizes asked for, per thread: a call asks for the
+// workspace size and then launches, and a layer keeps its sizes.
+template <class P, class F>
+P remembered(int64_t M, int64_t N, int64_t K, F make) {
+  constexpr int kSlots = 16;
+  struct Entry {
+    int64_t M = -1, N, K;
+    P plan;
+  };
+  static thread_local Entry table[kSlots];
+  Entry& e = table[(uint64_t)(M * 31 + N * 7 + K) % kSlots];
+  if (e.M != M || e.N != N || e.K != K) e = Entry{M, N, K, make()};
+  return e.plan;
+}
+Plan product_plan(int64_t M, int64_t N, int64_t K) {
+  return remembered<Plan>(M, N, K, [&] { return plan_product(M, N, K); });
+}
+GradPlan grad_plan(int64_t M, int N, int K) {
+  return remembered<GradPlan>(M, N, K, [&] { return plan_grads(M, N, K); });
 }
 
 // Sum of the split partials in split order, then the epilogue; a thread
 // takes 8 columns of a row.
 template <int ACT>
-__global__ __launch_bounds__(256) void linear_reduce_kernel(TileParams p) {
+__device__ __forceinline__ void reduce_run(const TileParams& p, int64_t id) {
   const int64_t runs = p.ldp / 8;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t row = id / runs;
   if (row >= p.M) return;
   const int col = (int)(id - row * runs) * 8;
@@ -103,6 +185,53 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(TileParams p) {
   float b[8];
   bias8(p, col, b);
   finish8<ACT>(p, row * p.ldc + col, col, v, b);
+}
+
+template <int ACT>
+__global__ __launch_bounds__(256) void linear_reduce_kernel(TileParams p) {
+  reduce_run<ACT>(p, (int64_t)blockIdx.x * 256 + threadIdx.x);
+}
+
+// db[c] = sum over the row chunks: 16 columns per block, 16 strided partial
+// sums each (a thread loads eight chunks before it adds them), then a tree
+__device__ __forceinline__ void db_columns(const float* __restrict__ part,
+                                           int chunks, int N, int block,
+                                           float* __restrict__ db) {
+  __shared__ float red[16][17];
+  const int lane = threadIdx.x & 15, ct = threadIdx.x >> 4;
+  const int c = block * 16 + lane;
+  const float* src = part + min(c, N - 1);
+  float s = 0.0f;
+  for (int i0 = ct; i0 < chunks; i0 += 128) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      v[u] = src[(int64_t)min(i0 + 16 * u, chunks - 1) * N];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s += i0 + 16 * u < chunks ? v[u] : 0.0f;
+  }
+  red[ct][lane] = s;
+  __syncthreads();
+#pragma unroll
+  for (int h = 8; h >= 1; h >>= 1) {
+    if (ct < h) red[ct][lane] += red[ct + h][lane];
+    __syncthreads();
+  }
+  if (ct == 0 && c < N) db[c] = red[0][lane];
+}
+
+// What is left of a backward after its products, in one launch: db from its
+// partial sums (bd work-groups), then the split partials of dx (bx) and dW.
+__global__ __launch_bounds__(256) void linear_finish_kernel(
+    const float* __restrict__ db_part, int chunks, int N, float* db, int bd,
+    TileParams px, int bx, TileParams pw) {
+  const int b = blockIdx.x;
+  if (b < bd)
+    db_columns(db_part, chunks, N, b, db);
+  else if (b < bd + bx)
+    reduce_run<ACT_NONE>(px, (int64_t)(b - bd) * 256 + threadIdx.x);
+  else
+    reduce_run<ACT_NONE>(pw, (int64_t)(b - bd - bx) * 256 + threadIdx.x);
 }
 
 template <int LA, int LB, int EPI>
@@ -122,28 +251,33 @@ void launch_tiles(const TileParams& p, const Plan& pl, unsigned grid,
                        dim3(1024), 0, stream, p);
 }
 
-// ACT: the activation, or kEpiPlain for a gradient (a bf16 store alone).
-template <int LA, int LB, int ACT>
-hipError_t launch_product(const char* name, TileParams p, const Plan& pl,
-                          void* part, hipStream_t stream) {
+unsigned tile_grid(TileParams& p, const Plan& pl, void* part) {
   p.tiles_m = (int)cdiv(p.M, pl.tm);
   p.tiles_n = (int)cdiv(p.N, pl.tn);
   p.splits = pl.S;
   p.part = static_cast<float*>(part);
   p.ldp = pad8(p.N);
   const int64_t total = (int64_t)p.tiles_m * p.tiles_n * pl.S;
-  const unsigned grid = (unsigned)(cdiv(total, gg::kXcds) * gg::kXcds);
+  return (unsigned)(cdiv(total, gg::kXcds) * gg::kXcds);
+}
+int64_t reduce_blocks(const TileParams& p) {
+  return p.splits > 1 ? cdiv(p.M * (p.ldp / 8), 256) : 0;
+}
+
+template <int ACT>
+hipError_t launch_forward(TileParams p, const Plan& pl, void* part,
+                          hipStream_t stream) {
+  const unsigned grid = tile_grid(p, pl, part);
   {
-    KernelScope ks(name, stream);
-    if (pl.S > 1) launch_tiles<LA, LB, kEpiPlain>(p, pl, grid, stream);
-    else launch_tiles<LA, LB, ACT>(p, pl, grid, stream);
+    KernelScope ks("linear_fwd", stream);
+    if (pl.S > 1) launch_tiles<KC, KC, kEpiPlain>(p, pl, grid, stream);
+    else launch_tiles<KC, KC, ACT>(p, pl, grid, stream);
   }
-  hipError_t e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || pl.S == 1) return e;
   KernelScope ks("linear_split_reduce", stream);
-  const int64_t threads = p.M * (p.ldp / 8);
-  hipLaunchKernelGGL((linear_reduce_kernel<(ACT < 0 ? ACT_NONE : ACT)>),
-                     dim3((unsigned)cdiv(threads, 256)), dim3(256), 0, stream,
+  hipLaunchKernelGGL((linear_reduce_kernel<ACT>),
+                     dim3((unsigned)reduce_blocks(p)), dim3(256), 0, stream,
                      p);
   return hipGetLastError();
 }
@@ -270,34 +404,6 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(
   }
 }
 
-// db[c] = sum over the row chunks: 16 columns per block, 64 strided partial
-// sums each (a thread loads four chunks before it adds them), then a tree
-__global__ __launch_bounds__(1024) void linear_db_kernel(
-    const float* __restrict__ part, int chunks, int N,
-    float* __restrict__ db) {
-  __shared__ float red[64][17];
-  const int lane = threadIdx.x & 15, ct = threadIdx.x >> 4;
-  const int c = blockIdx.x * 16 + lane;
-  float s = 0.0f;
-  for (int i0 = ct; i0 < chunks; i0 += 256) {
-    float v[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int i = i0 + 64 * u;
-      v[u] = i < chunks && c < N ? part[(int64_t)i * N + c] : 0.0f;
-    }
-    s += (v[0] + v[1]) + (v[2] + v[3]);
-  }
-  red[ct][lane] = s;
-  __syncthreads();
-#pragma unroll
-  for (int h = 32; h >= 1; h >>= 1) {
-    if (ct < h) red[ct][lane] += red[ct + h][lane];
-    __syncthreads();
-  }
-  if (ct == 0 && c < N) db[c] = red[0][lane];
-}
-
 // row chunks of the dz pass: about four blocks per CU, 32 rows at least
 int64_t dz_chunks(int64_t M, int N) {
   const int64_t cb = cdiv(pad8(N), 256);
@@ -308,7 +414,7 @@ int64_t dz_chunks(int64_t M, int N) {
 }  // namespace
 
 size_t linear_fwd_ws_bytes(int64_t M, int N, int K) {
-  return M == 0 || is_skinny(M, N, K) ? 0 : plan_product(M, N, K).part_bytes(M, N);
+  return M == 0 || is_skinny(M, N, K) ? 0 : product_plan(M, N, K).part_bytes(M, N);
 }
 
 hipError_t launch_linear_fwd(int64_t M, int N, int K, int act, const void* x,
@@ -331,24 +437,27 @@ hipError_t launch_linear_fwd(int64_t M, int N, int K, int act, const void* x,
   p.z = static_cast<uint16_t*>(z_save);
   p.act = act;
   if (is_skinny(M, N, K)) return launch_skinny(p, stream);
-  const Plan pl = plan_product(M, N, K);
+  const Plan pl = product_plan(M, N, K);
   switch (act) {
-    case ACT_RELU:
-      return launch_product<KC, KC, ACT_RELU>("linear_fwd", p, pl, ws, stream);
-    case ACT_GELU:
-      return launch_product<KC, KC, ACT_GELU>("linear_fwd", p, pl, ws, stream);
+    case ACT_RELU: return launch_forward<ACT_RELU>(p, pl, ws, stream);
+    case ACT_GELU: return launch_forward<ACT_GELU>(p, pl, ws, stream);
     case ACT_GELU_TANH:
-      return launch_product<KC, KC, ACT_GELU_TANH>("linear_fwd", p, pl, ws,
-                                                   stream);
-    case ACT_SILU:
-      return launch_product<KC, KC, ACT_SILU>("linear_fwd", p, pl, ws, stream);
-    default:
-      return launch_product<KC, KC, ACT_NONE>("linear_fwd", p, pl, ws, stream);
+      return launch_forward<ACT_GELU_TANH>(p, pl, ws, stream);
+    case ACT_SILU: return launch_forward<ACT_SILU>(p, pl, ws, stream);
+    default: return launch_forward<ACT_NONE>(p, pl, ws, stream);
   }
 }
 
 // The dz buffer is skipped where dy can be the products' operand itself.
 static bool needs_dz(int N, int act) { return act != ACT_NONE || N % 8 != 0; }
+
+// Tiles and splits are those of both gradients whichever is asked for, so
+// that a gradient's bits do not depend on the other.
+static GradPlan wanted_plan(int64_t M, int N, int K, bool dx, bool dw) {
+  GradPlan g = grad_plan(M, N, K);
+  g.joint = g.joint && dx && dw;
+  return g;
+}
 
 size_t linear_bwd_ws_bytes(int64_t M, int N, int K, int act, bool want_dx,
                            bool want_dw, bool want_db) {
@@ -356,10 +465,10 @@ size_t linear_bwd_ws_bytes(int64_t M, int N, int K, int act, bool want_dx,
   size_t b = 0;
   if (needs_dz(N, act)) b += align256((size_t)M * pad8(N) * 2);
   if (want_db) b += align256((size_t)dz_chunks(M, N) * N * sizeof(float));
-  size_t part = 0;
-  if (want_dx) part = plan_product(M, K, N).part_bytes(M, K);
-  if (want_dw) part = std::max(part, plan_product(N, K, M).part_bytes(N, K));
-  return b + part;
+  const GradPlan g = wanted_plan(M, N, K, want_dx, want_dw);
+  if (want_dx) b += g.x.part_bytes(M, K);
+  if (want_dw) b += g.w.part_bytes(N, K);
+  return b;
 }
 
 hipError_t launch_linear_bwd(int64_t M, int N, int K, int act, const void* dy,
@@ -367,8 +476,7 @@ hipError_t launch_linear_bwd(int64_t M, int N, int K, int act, const void* dy,
                              void* dx, void* dw, float* db, void* ws,
                              hipStream_t stream) {
   hipError_t e = hipSuccess;
-  if (M == 0) {   // empty sums
-    // (N * K bf16 values are whole dwords: K % 8 == 0)
+  if (M == 0) {   // empty sums (N * K bf16 values are whole dwords)
     if (dw)
       e = launch_zero_u32(static_cast<uint32_t*>(dw), (int64_t)N * K / 2,
                           stream, "linear_zero");
@@ -378,19 +486,21 @@ hipError_t launch_linear_bwd(int64_t M, int N, int K, int act, const void* dy,
     return e;
   }
   char* wp = static_cast<char*>(ws);
+  auto take = [&](size_t bytes) {
+    char* q = wp;
+    wp += bytes;
+    return q;
+  };
   const bool own_dz = needs_dz(N, act);
   const int64_t ldz = own_dz ? pad8(N) : N;
   uint16_t* dz = nullptr;
-  if (own_dz) {
-    dz = reinterpret_cast<uint16_t*>(wp);
-    wp += align256((size_t)M * ldz * 2);
-  }
+  if (own_dz)
+    dz = reinterpret_cast<uint16_t*>(take(align256((size_t)M * ldz * 2)));
   const int64_t chunks = dz_chunks(M, N);
   float* db_part = nullptr;
-  if (db) {
-    db_part = reinterpret_cast<float*>(wp);
-    wp += align256((size_t)chunks * N * sizeof(float));
-  }
+  if (db)
+    db_part = reinterpret_cast<float*>(
+        take(align256((size_t)chunks * N * sizeof(float))));
   const bool products = dx || dw;
   if ((own_dz && products) || db) {
     KernelScope ks("linear_dz", stream);
@@ -413,45 +523,75 @@ hipError_t launch_linear_bwd(int64_t M, int N, int K, int act, const void* dy,
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (db) {
-    KernelScope ks("linear_db", stream);
-    hipLaunchKernelGGL(linear_db_kernel, dim3((unsigned)cdiv(N, 16)),
-                       dim3(1024), 0, stream, db_part, (int)chunks, N, db);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
   const char* g = own_dz ? reinterpret_cast<const char*>(dz)
                          : static_cast<const char*>(dy);
+  const GradPlan gp = wanted_plan(M, N, K, dx != nullptr, dw != nullptr);
+  TileParams px{}, pw{};   // splits = 0: not asked for
+  unsigned gx = 0, gw = 0;
   if (dx) {
-    TileParams p{};
-    p.a = g;
-    p.lda = 2 * ldz;
-    p.b = static_cast<const char*>(w);
-    p.ldb = 2 * (int64_t)K;
-    p.M = M;
-    p.N = K;
-    p.K = N;
-    p.c = static_cast<uint16_t*>(dx);
-    p.ldc = K;
-    e = launch_product<KC, MC, kEpiPlain>("linear_dgrad", p, plan_product(M, K, N), wp,
-                               stream);
-    if (e != hipSuccess) return e;
+    px.a = g;
+    px.lda = 2 * ldz;
+    px.b = static_cast<const char*>(w);
+    px.ldb = 2 * (int64_t)K;
+    px.M = M;
+    px.N = K;
+    px.K = N;
+    px.c = static_cast<uint16_t*>(dx);
+    px.ldc = K;
+    gx = tile_grid(px, gp.x, take(gp.x.part_bytes(M, K)));
   }
   if (dw) {
-    TileParams p{};
-    p.a = g;
-    p.lda = 2 * ldz;
-    p.b = static_cast<const char*>(x);
-    p.ldb = 2 * (int64_t)K;
-    p.M = N;
-    p.N = K;
-    p.K = M;
-    p.c = static_cast<uint16_t*>(dw);
-    p.ldc = K;
-    e = launch_product<MC, MC, kEpiPlain>("linear_wgrad", p, plan_product(N, K, M), wp,
-                               stream);
+    pw.a = g;
+    pw.lda = 2 * ldz;
+    pw.b = static_cast<const char*>(x);
+    pw.ldb = 2 * (int64_t)K;
+    pw.M = N;
+    pw.N = K;
+    pw.K = M;
+    pw.c = static_cast<uint16_t*>(dw);
+    pw.ldc = K;
+    gw = tile_grid(pw, gp.w, take(gp.w.part_bytes(N, K)));
   }
-  return e;
+  if (gp.joint) {
+    KernelScope ks("linear_grads", stream);
+    const unsigned grid = gx + gw;
+    const int first = (int)(gp.x_first ? gx : gw), xf = gp.x_first ? 1 : 0;
+    if (gp.x.tm == 256)
+      hipLaunchKernelGGL((linear_grads_kernel<256, 256>), dim3(grid),
+                         dim3(512), 0, stream, px, pw, first, xf);
+    else if (gp.x.tm == 128)
+      hipLaunchKernelGGL((linear_grads_kernel<128, 128>), dim3(grid),
+                         dim3(256), 0, stream, px, pw, first, xf);
+    else if (gp.x.tn == 128)
+      hipLaunchKernelGGL((linear_grads_kernel<64, 128>), dim3(grid),
+                         dim3(256), 0, stream, px, pw, first, xf);
+    else
+      hipLaunchKernelGGL((linear_grads_kernel<64, 64>), dim3(grid),
+                         dim3(1024), 0, stream, px, pw, first, xf);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  } else {
+    if (dx) {
+      KernelScope ks("linear_dgrad", stream);
+      launch_tiles<KC, MC, kEpiPlain>(px, gp.x, gx, stream);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    if (dw) {
+      KernelScope ks("linear_wgrad", stream);
+      launch_tiles<MC, MC, kEpiPlain>(pw, gp.w, gw, stream);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+  }
+  const int64_t bd = db ? cdiv(N, 16) : 0, bx = reduce_blocks(px),
+                bw = reduce_blocks(pw);
+  if (bd + bx + bw == 0) return e;
+  KernelScope ks("linear_finish", stream);
+  hipLaunchKernelGGL(linear_finish_kernel, dim3((unsigned)(bd + bx + bw)),
+                     dim3(256), 0, stream, db_part, (int)chunks, N, db,
+                     (int)bd, px, (int)bx, pw);
+  return hipGetLastError();
 }
 
 }  // namespace moe

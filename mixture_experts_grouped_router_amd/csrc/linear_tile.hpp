@@ -185,23 +185,27 @@ __device__ __forceinline__ void sched_slice() {
 }
 
 // Work-groups b = x mod 8 run on XCD x; each XCD takes one contiguous run of
-// the tile list, in bands of 8 M tiles with M fastest: the 32 tiles in
-// flight on an XCD are 8 x 4 and share their panels in its L2.
-__device__ __forceinline__ bool tile_of(const TileParams& p, int& tm, int& tn,
-                                        int& split) {
+// the tile list, in bands of kBand M tiles with M fastest: the 32 tiles in
+// flight on an XCD are 4 x 8 and share their panels in its L2.  (8 x 4 wrote
+// its outputs to fewer memory channels at a time: 16384 x 8192 x 512 202 us
+// against 188, 8192 x 14336 x 4096 the same.)
+constexpr int kBand = 4;
+
+__device__ __forceinline__ bool tile_of(const TileParams& p, int block,
+                                        int& tm, int& tn, int& split) {
   const int tiles = p.tiles_m * p.tiles_n;
   const int total = tiles * p.splits;
   const int per = (total + gg::kXcds - 1) / gg::kXcds;
-  const int idx = blockIdx.x / gg::kXcds;
-  const int L = (blockIdx.x % gg::kXcds) * per + idx;
+  const int idx = block / gg::kXcds;
+  const int L = (block % gg::kXcds) * per + idx;
   if (idx >= per || L >= total) return false;
   split = L / tiles;
   const int l = L - split * tiles;
-  const int band = l / (8 * p.tiles_n);
-  const int in = l - band * 8 * p.tiles_n;
-  const int gm = min(8, p.tiles_m - 8 * band);
+  const int band = l / (kBand * p.tiles_n);
+  const int in = l - band * kBand * p.tiles_n;
+  const int gm = min(kBand, p.tiles_m - kBand * band);
   tn = in / gm;
-  tm = 8 * band + in - tn * gm;
+  tm = kBand * band + in - tn * gm;
   return true;
 }
 
@@ -324,22 +328,20 @@ struct TileShape {
 // where p.splits > 1, else a bf16 store alone (no bias, residual, save).
 constexpr int kEpiPlain = -1;
 
+// The tile that work-group `block` of a launch owns.  b0 - b2, a0, a1: the
+// operand stages in LDS, B of three steps, A of two (G TN 128 and G TM 128
+// bytes each; distinct LDS objects, so that the compiler does not make a read
+// of one wait for the loads into another).
 template <int TM, int TN, int LA, int LB, int EPI>
-__global__ __launch_bounds__((TileShape<TM, TN>::kThreads),
-                             (TileShape<TM, TN>::kWavesPerSimd)) void
-linear_tile_kernel(TileParams p) {
-#ifdef __HIP_DEVICE_COMPILE__   // (the host pass needs the launch stub only)
+__device__ __forceinline__ void tile_body(const TileParams& p, int block,
+                                          char* const b0, char* const b1,
+                                          char* const b2, char* const a0,
+                                          char* const a1) {
   using S = TileShape<TM, TN>;
   constexpr int MI = S::MI, NJ = S::NJ, WN = S::WN, NW = S::NW, G = S::G;
   constexpr int kSl = 4;               // 16-wide K slices per 64-wide step
-  // B of three steps, A of two
-  __shared__ __attribute__((aligned(1024))) char b0[G * TN * 128];
-  __shared__ __attribute__((aligned(1024))) char b1[G * TN * 128];
-  __shared__ __attribute__((aligned(1024))) char b2[G * TN * 128];
-  __shared__ __attribute__((aligned(1024))) char a0[G * TM * 128];
-  __shared__ __attribute__((aligned(1024))) char a1[G * TM * 128];
   int tm, tn, split;
-  if (!tile_of(p, tm, tn, split)) return;
+  if (!tile_of(p, block, tm, tn, split)) return;   // the whole work-group
   const int t = threadIdx.x;
   const int lane = t & 63;
   const int wave_id = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -669,6 +671,42 @@ linear_tile_kernel(TileParams p) {
     __builtin_amdgcn_s_waitcnt(0xc07f);   // readback done before reuse
   }
   }
+}
+
+#define MOE_LIN_STAGES(TM, TN)                                               \
+  constexpr int kG = TileShape<TM, TN>::G;                                   \
+  __shared__ __attribute__((aligned(1024))) char b0[kG * TN * 128];          \
+  __shared__ __attribute__((aligned(1024))) char b1[kG * TN * 128];          \
+  __shared__ __attribute__((aligned(1024))) char b2[kG * TN * 128];          \
+  __shared__ __attribute__((aligned(1024))) char a0[kG * TM * 128];          \
+  __shared__ __attribute__((aligned(1024))) char a1[kG * TM * 128];
+
+template <int TM, int TN, int LA, int LB, int EPI>
+__global__ __launch_bounds__((TileShape<TM, TN>::kThreads),
+                             (TileShape<TM, TN>::kWavesPerSimd)) void
+linear_tile_kernel(TileParams p) {
+#ifdef __HIP_DEVICE_COMPILE__   // (the host pass needs the launch stub only)
+  MOE_LIN_STAGES(TM, TN)
+  tile_body<TM, TN, LA, LB, EPI>(p, blockIdx.x, b0, b1, b2, a0, a1);
+#endif
+}
+
+// dx = dz W and dW = dz^T x in one launch: `first` work-groups for the one
+// whose tiles take longer, the others behind them, so that the second fills
+// the CUs that the first leaves idle.
+template <int TM, int TN>
+__global__ __launch_bounds__((TileShape<TM, TN>::kThreads),
+                             (TileShape<TM, TN>::kWavesPerSimd)) void
+linear_grads_kernel(TileParams px, TileParams pw, int first, int x_first) {
+#ifdef __HIP_DEVICE_COMPILE__
+  MOE_LIN_STAGES(TM, TN)
+  const int b = blockIdx.x;
+  if ((b < first) == (x_first != 0))
+    tile_body<TM, TN, KC, MC, kEpiPlain>(px, x_first ? b : b - first, b0, b1,
+                                         b2, a0, a1);
+  else
+    tile_body<TM, TN, MC, MC, kEpiPlain>(pw, x_first ? b - first : b, b0, b1,
+                                         b2, a0, a1);
 #endif
 }
 
