@@ -49,11 +49,17 @@ struct Plan {
 struct TileCost {
   int tm, tn, per_cu, groups;
   double lat, thr, fix;
+  int threads;
 };
-constexpr TileCost kTiles[] = {{256, 256, 1, 1, 1.2, 0.0, 11.0},
-                               {128, 128, 2, 1, 0.53, 0.46, 2.6},
-                               {64, 128, 2, 1, 0.45, 0.33, 1.8},
-                               {64, 64, 1, 4, 1.05, 0.0, 2.0}};
+constexpr TileCost kTiles[] = {{256, 256, 1, 1, 1.2, 0.0, 11.0, 512},
+                               {128, 128, 2, 1, 0.53, 0.46, 2.6, 256},
+                               {64, 128, 2, 1, 0.45, 0.33, 1.8, 256},
+                               {64, 64, 1, 4, 1.05, 0.0, 2.0, 1024}};
+// a launch holds fewer than 2^32 threads (the size limits of the entry
+// points leave room for the 128 x 128 tile)
+bool fits_launch(const TileCost& c, int64_t groups) {
+  return groups * c.threads < ((int64_t)1 << 32) - 65536;
+}
 constexpr double kLaunchUs = 4.5;
 
 struct Product {
@@ -87,6 +93,7 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, double* us = nullptr) {
         return st * std::max(c.lat, c.thr * occ) + c.fix * occ;
       };
       const int64_t n = p.groups(c, S), last = n % slots;
+      if (!fits_launch(c, n)) continue;
       double t = (double)(n / slots) * round_us(slots);
       if (last) t += round_us(last);
       if (S > 1) t += kLaunchUs + p.partial_us(S);
@@ -127,6 +134,7 @@ GradPlan plan_grads(int64_t M, int N, int K) {
         const double work = ((double)px.groups(c, sx) * fx +
                              (double)pw.groups(c, sw) * fw) / slots;
         const int64_t n = px.groups(c, sx) + pw.groups(c, sw);
+        if (!fits_launch(c, n)) continue;
         // the shorter product's groups fill the tail of the longer one
         double t = std::max(std::max(fx, fw), work + 0.5 * std::min(fx, fw));
         if (n <= slots) t = std::max(fx, fw);   // one round
@@ -404,11 +412,16 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(
   }
 }
 
-// row chunks of the dz pass: about four blocks per CU, 32 rows at least
+// Row chunks of the dz pass.  Few rows are bound by a thread's chain of
+// derivatives: 8 rows per chunk (one per thread) while that takes no more than
+// two blocks per CU; more chunks cost the finishing launch more than they save
+// (1001 x 2047: 36.8 us for the backward with 8 rows, 32.8 with 16, 33.8 with
+// 32; 658 x 35: 15.2, 18.6 and 24.1).  Many rows: about four blocks per CU.
 int64_t dz_chunks(int64_t M, int N) {
   const int64_t cb = cdiv(pad8(N), 256);
   return std::max<int64_t>(
-      1, std::min<int64_t>(cdiv(M, 32), cdiv(4 * kCus, cb)));
+      {1, std::min<int64_t>(cdiv(M, 8), 2 * kCus / cb),
+       std::min<int64_t>(cdiv(M, 32), cdiv(4 * kCus, cb))});
 }
 
 }  // namespace
