@@ -414,8 +414,9 @@ moe_status_t check_route(int64_t T, int32_t E, int32_t k,
   MOE_REQUIRE(std::isfinite(o->scale), MOE_ERR_INVALID_ARG,
               "scale must be finite");
   out->score = o->score == MOE_SCORE_SIGMOID;
-  out->n_group = o->n_group;
-  out->topk_group = o->topk_group;
+  // all groups stay: no groups
+  out->n_group = o->topk_group < o->n_group ? o->n_group : 1;
+  out->topk_group = o->topk_group < o->n_group ? o->topk_group : 1;
   out->group_score = o->group_score == MOE_GROUP_TOP2;
   out->renormalize = o->renormalize != 0;
   out->scale = (double)o->scale;
