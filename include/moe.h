@@ -438,7 +438,8 @@ moe_status_t moe_unpermute_probs_grad(moe_ctx_t ctx, const float* dw_perm,
  *  residual bf16 [T, H] or NULL (0); y may be the residual itself
  *  y, dy    bf16 [T, H];  dz_perm bf16 [T*k, H]
  *  dtopk_w  float32 [T, k] or NULL; needs z_perm (else nullable)
- *  T >= 0, H % 8 == 0, k <= 32, 0 <= p <= 1; rows 16-byte aligned.
+ *  T >= 0, H % 8 == 0, k <= 32, 0 <= p <= 1; rows 16-byte aligned.  No
+ *  other output may overlap an input.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_HIP.
  * ---------------------------------------------------------------------- */
 moe_status_t moe_unpermute_dropout(moe_ctx_t ctx, const void* z_perm,
@@ -464,7 +465,8 @@ moe_status_t moe_unpermute_dropout_bwd(moe_ctx_t ctx, const void* dy,
  *  layers beside the MoE ones (projections, shared branches).]
  *   z = x W^T + bias,  y = act(z) + residual
  *   dz = dy act'(z),  dx = dz W,  dW = dz^T x,  db = sum over rows of dz
- * (dresidual = dy).  act: none, relu (0 at 0, like its gradient), gelu
+ * (dresidual = dy).  act: none, relu (0 at 0, like its gradient; NaN stays
+ * NaN, as in the others), gelu
  * z Phi(z), gelu_tanh 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))), silu
  * z / (1 + e^-z).  Products are accumulated in float32; bias, activation
  * and residual are applied to the float32 value and y is rounded to bf16

@@ -39,7 +39,7 @@ __device__ __forceinline__ float ndtr(float z, float* e) {
 template <int ACT>
 __device__ __forceinline__ float act_fwd(float z) {
   if constexpr (ACT == ACT_RELU) {
-    return fmaxf(z, 0.0f);
+    return z <= 0.0f ? 0.0f : z;   // NaN stays NaN
   } else if constexpr (ACT == ACT_GELU) {
     float e;
     return z * ndtr(z, &e);
@@ -57,14 +57,16 @@ __device__ __forceinline__ float act_fwd(float z) {
 template <int ACT>
 __device__ __forceinline__ float act_grad(float z) {
   if constexpr (ACT == ACT_RELU) {
-    return z > 0.0f ? 1.0f : 0.0f;
+    return z <= 0.0f ? 0.0f : z == z ? 1.0f : z;
   } else if constexpr (ACT == ACT_GELU) {
     float e;
     const float c = ndtr(z, &e);
     return c + z * 0.3989422804014327f * e;
   } else if constexpr (ACT == ACT_GELU_TANH) {
     const float u2 = 1.5957691216057308f * (z + 0.044715f * z * z * z);
-    const float du2 = 1.5957691216057308f * (1.0f + 0.134145f * z * z);
+    // (z^2 may overflow where s or 1 - s is 0 already)
+    const float z2 = fminf(z * z, 1e30f);
+    const float du2 = 1.5957691216057308f * (1.0f + 0.134145f * z2);
     const float s = sigm(u2);
     return s + z * s * (1.0f - s) * du2;
   } else if constexpr (ACT == ACT_SILU) {

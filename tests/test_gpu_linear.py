@@ -204,6 +204,31 @@ def test_activation_range(m, act):
         assert abs(float(g[0]) - ref) <= 2.0 ** -18 * (1 + abs(z[i])), z[i]
 
 
+@pytest.mark.parametrize("act", ACTS[1:])
+def test_activation_extremes(m, act):
+    """Derivatives of the largest magnitudes (0 or 1 exactly: the other terms
+    vanish) and NaN, which stays NaN in both directions."""
+    v = np.array([1e10, 1e19, 3e19, 1e25, 3e38], np.float32)
+    zb = bf16_bits(np.concatenate([v, -v, [np.nan]]).astype(np.float32))
+    n = zb.size
+    one = bf16_bits(np.ones((1, n), np.float32))
+    g = m.moe_linear_bwd(dev(one), None, None, act=ACTS.index(act),
+                         z=dev(zb.reshape(1, n)), want_dx=False,
+                         want_dw=False, want_db=True)["db"].cpu().numpy()
+    ref = B.act_grad(act, bf16_to_f64(zb[:-1]))
+    assert np.all(ref == np.repeat([1.0, 0.0], 5))
+    assert np.all(g[:-1] == ref) and np.isnan(g[-1])
+    for M in (1, 5, 70):
+        x = torch.full((M, 8), float("nan"), dtype=torch.bfloat16,
+                       device="cuda")
+        w = torch.ones((9, 8), dtype=torch.bfloat16, device="cuda")
+        y = m.moe_linear_fwd(x, w, act=ACTS.index(act))["y"]
+        assert bool(torch.isnan(y).all())
+        dx = m.moe_linear_bwd(torch.ones_like(y), x, w, act=ACTS.index(act),
+                              z=y, want_dw=False)["dx"]
+        assert bool(torch.isnan(dx).all())
+
+
 def test_rows_are_isolated(m):
     """A NaN row of x or W reaches its own output row or column only, also
     through K tails (the bytes behind a row's end are the next row's)."""
