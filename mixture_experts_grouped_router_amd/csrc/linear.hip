@@ -156,13 +156,16 @@ GradPlan plan_grads(int64_t M, int N, int K) {
 // workspace size and then launches, and a layer keeps its sizes.
 template <class P, class F>
 P remembered(int64_t M, int64_t N, int64_t K, F make) {
-  constexpr int kSlots = 16;
+  constexpr int kSlots = 64;
   struct Entry {
     int64_t M = -1, N, K;
     P plan;
   };
   static thread_local Entry table[kSlots];
-  Entry& e = table[(uint64_t)(M * 31 + N * 7 + K) % kSlots];
+  // (the top bits of an odd multiple: sizes are often multiples of 64)
+  const uint64_t h = ((uint64_t)M * 0x10001 + (uint64_t)N * 0x101 +
+                      (uint64_t)K) * 0x9E3779B97F4A7C15ull;
+  Entry& e = table[h >> 58];
   if (e.M != M || e.N != N || e.K != K) e = Entry{M, N, K, make()};
   return e.plan;
 }
