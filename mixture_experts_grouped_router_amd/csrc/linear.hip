@@ -41,26 +41,26 @@ struct Plan {
 // them on a CU takes
 //   steps * max(lat, thr c) + fix c
 // (lat: one K step with a CU to itself, thr: its share of a busy CU, fix:
-// prologue and epilogue; the 64 x 64 tile takes four steps at a time); a
-// split adds a launch and the float32 partials' round trip at 6 TB/s (they
-// mostly stay in the caches).  The constants come from 1200 timed (shape,
-// tile, split) combinations of the three products; the choice is 2% slower
-// than the best combination on average.
+// prologue and epilogue; the 64 x 64 tile takes two steps at a time); a
+// split adds a launch, the float32 partials' round trip at 6 TB/s (they mostly
+// stay in the caches) and their sum's chain.  The constants come from 2000
+// timed (shape, tile, split) combinations of the three products; the choice is
+// 1% slower than the best combination on average, 22% at worst.
 struct TileCost {
   int tm, tn, per_cu, groups;
   double lat, thr, fix;
   int threads;
 };
-constexpr TileCost kTiles[] = {{256, 256, 1, 1, 1.2, 0.0, 11.0, 512},
-                               {128, 128, 2, 1, 0.53, 0.46, 2.6, 256},
-                               {64, 128, 2, 1, 0.45, 0.33, 1.8, 256},
-                               {64, 64, 1, 4, 1.05, 0.0, 2.0, 1024}};
+constexpr TileCost kTiles[] = {{256, 256, 1, 1, 1.15, 0.0, 11.5, 512},
+                               {128, 128, 2, 1, 0.5, 0.4, 2.1, 256},
+                               {64, 128, 2, 1, 0.3, 0.32, 1.4, 256},
+                               {64, 64, 1, 2, 0.4, 0.0, 1.5, 512}};
 // a launch holds fewer than 2^32 threads (the size limits of the entry
 // points leave room for the 128 x 128 tile)
 bool fits_launch(const TileCost& c, int64_t groups) {
   return groups * c.threads < ((int64_t)1 << 32) - 65536;
 }
-constexpr double kLaunchUs = 4.5;
+constexpr double kLaunchUs = 3.2;
 
 struct Product {
   int64_t M, N, K;
@@ -75,7 +75,7 @@ struct Product {
                       (int64_t)S * M * pad8(N) * 4 <= kMaxPartBytes);
   }
   double partial_us(int S) const {
-    return S > 1 ? (double)S * M * N * 8.0 / 6e6 : 0.0;
+    return S > 1 ? S * (0.25 + (double)M * N * 8.0 / 6e6) : 0.0;
   }
 };
 
@@ -140,8 +140,10 @@ GradPlan plan_grads(int64_t M, int N, int K) {
         if (n <= slots) t = std::max(fx, fw);   // one round
         if (n <= kCus)
           t = std::max(px.steps(c, sx), pw.steps(c, sw)) * c.lat + c.fix;
+        // (db needs the finishing launch anyway, but the plan must not depend
+        // on whether it is asked for)
         if (sx > 1 || sw > 1)
-          t += kLaunchUs + px.partial_us(sx) + pw.partial_us(sw);
+          t += kLaunchUs / 2 + px.partial_us(sx) + pw.partial_us(sw);
         if (t < best_us) {
           best_us = t;
           best = GradPlan{true, fx >= fw, Plan{c.tm, c.tn, sx},
@@ -259,7 +261,7 @@ void launch_tiles(const TileParams& p, const Plan& pl, unsigned grid,
                        dim3(grid), dim3(256), 0, stream, p);
   else
     hipLaunchKernelGGL((linear_tile_kernel<64, 64, LA, LB, EPI>), dim3(grid),
-                       dim3(1024), 0, stream, p);
+                       dim3(512), 0, stream, p);
 }
 
 unsigned tile_grid(TileParams& p, const Plan& pl, void* part) {
@@ -294,11 +296,13 @@ hipError_t launch_forward(TileParams p, const Plan& pl, void* part,
 }
 
 // Few rows: one pass over the weights.  Up to 16 rows the MFMA form saves
-// the tile kernel's second launch (4 x 768 x 2048: 5.0 against 8.5 us; 16 x
-// 4096 x 4096: 11.6 against 14.1), but reads large weights more slowly (16 x
-// 14336 x 4096: 40.9 against 28.1).
+// the tile kernel's second launch (4 x 768 x 2048: 4.7 against 7.6 us; 16 x
+// 4096 x 4096: 10.2 against 11.9), but it reads large weights more slowly (16 x
+// 14336 x 4096: 40.9 against 28.1) and does not split a long K over
+// work-groups (16 x 100 x 8192: 16.1 against 10.1).
 bool is_skinny(int64_t M, int64_t N, int64_t K) {
-  return M <= 2 || (M <= kSkinnyMaxM && N * K <= (int64_t)1 << 24);
+  return M <= 2 || (M <= kSkinnyMaxM && K <= 4096 &&
+                    N * K <= (int64_t)1 << 24);
 }
 hipError_t launch_skinny(const TileParams& p, hipStream_t stream) {
   KernelScope ks("linear_skinny", stream);
@@ -583,7 +587,7 @@ hipError_t launch_linear_bwd(int64_t M, int N, int K, int act, const void* dy,
                          dim3(256), 0, stream, px, pw, first, xf);
     else
       hipLaunchKernelGGL((linear_grads_kernel<64, 64>), dim3(grid),
-                         dim3(1024), 0, stream, px, pw, first, xf);
+                         dim3(512), 0, stream, px, pw, first, xf);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   } else {

@@ -3,14 +3,22 @@
 //
 // C[m, n] = sum_k A(m, k) B(n, k), float32 accumulation, 32x32x16 bf16
 // MFMAs.  Operands are K-contiguous (KC: [mn][k]) or MN-contiguous (MC:
-// [k][mn]); both go global -> LDS directly and, like in the grouped GEMMs
-// (grouped_gemm_w8b.hpp), B is loaded two K steps ahead (three buffers) and
-// A one (two buffers), with one barrier per step.
+// [k][mn]); both go global -> LDS directly, one barrier per step of 64 k.
 //
-// Tiles: 256 x 256 (eight waves, one work-group per CU) where the product
-// fills the chip with them, else 128 x 128 or 64 x 128 (four waves, two
-// work-groups per CU), or 64 x 64 with K dealt to four groups of four waves;
-// each may split K over S work-groups that write float32 partial tiles.
+// Tiles, and how far ahead their operands are loaded:
+//  * 256 x 256 (eight waves, one work-group per CU) where the product fills
+//    the chip with them, 128 x 128 (four waves, two work-groups per CU): like
+//    in the grouped GEMMs (grouped_gemm_w8b.hpp) B two steps ahead (three
+//    buffers) and A one (two buffers), which fills the LDS.
+//  * 64 x 128 (four waves, two work-groups per CU): both two steps ahead.
+//    With A one step ahead a step took 0.36 us on a CU of its own instead of
+//    0.27 (1024 x 1024 x 4096: 29 -> 22.8 us).
+//  * 64 x 64, K steps dealt to two groups of four waves (one work-group per
+//    CU): four steps ahead, 128 KiB in flight per CU, so that a step takes
+//    what the CU's load path needs for it (16 KiB at 95 GB/s; rows that do
+//    not start on a 128-byte line touch two lines per segment and get 65).
+//    Four groups with shorter queues: 333 x 1000 x 2048 11.7 us, now 9.2.
+// Each may split K over S work-groups that write float32 partial tiles.
 //
 // Any M and N; K in multiples of 8 (16-byte chunks).  Rows past the end and
 // the K tail of the last step read as zeros: their byte offsets lie past the
@@ -307,19 +315,19 @@ __device__ __forceinline__ void finish8(const TileParams& p, int64_t at,
 }
 
 // The waves of a tile: 256 x 256, 2 x 4 waves of 128 x 64; 128 x 128, 2 x 2
-// of 64 x 64; 64 x 128, 1 x 4 of 64 x 32; 64 x 64, 2 x 2 of 32 x 32, and four
-// such groups, each with a quarter of the K steps and its own LDS stages,
-// that add up through LDS: for products with few tiles, whose time is the
-// latency of their K steps.
+// of 64 x 64; 64 x 128, 1 x 4 of 64 x 32; 64 x 64, 2 x 2 of 32 x 32, and two
+// such groups, each with every second K step and its own LDS stages, that add
+// up through LDS: for products with few tiles.
 template <int TM, int TN>
 struct TileShape {
   static constexpr bool kWide = TM == 64 && TN == 128;
   static constexpr int WM = kWide ? 1 : 2;
   static constexpr int WN = TN == 256 || kWide ? 4 : 2;
   static constexpr int NW = WM * WN;        // waves per group
-  static constexpr int G = TM == 64 && TN == 64 ? 4 : 1;   // K groups
+  static constexpr int G = TM == 64 && TN == 64 ? 2 : 1;   // K groups
   static constexpr int kThreads = 64 * NW * G;
-  static constexpr int kWavesPerSimd = G > 1 ? 4 : 2;
+  // LDS stages that hold A and B of a step together (0: B three, A two)
+  static constexpr int kStages = G > 1 ? 5 : kWide ? 3 : 0;
   static constexpr int MI = TM / WM / 32;   // 32-row A blocks of a wave
   static constexpr int NJ = TN / WN / 32;   // 32-column B blocks
 };
@@ -329,9 +337,10 @@ struct TileShape {
 constexpr int kEpiPlain = -1;
 
 // The tile that work-group `block` of a launch owns.  b0 - b2, a0, a1: the
-// operand stages in LDS, B of three steps, A of two (G TN 128 and G TM 128
-// bytes each; distinct LDS objects, so that the compiler does not make a read
-// of one wait for the loads into another).
+// operand stages in LDS, B of three steps and A of two (TN 128 and TM 128
+// bytes each), or kStages of both (G (TM + TN) 128 bytes each, b0 first).
+// Distinct LDS objects, so that the compiler does not make a read of one wait
+// for the loads into another.
 template <int TM, int TN, int LA, int LB, int EPI>
 __device__ __forceinline__ void tile_body(const TileParams& p, int block,
                                           char* const b0, char* const b1,
@@ -351,18 +360,14 @@ __device__ __forceinline__ void tile_body(const TileParams& p, int block,
   const int64_t m0 = (int64_t)tm * TM;
   const int n0 = tn * TN;
 
-  // K steps [ks, ke) of this work-group (group); nk: those of the longest
-  // group, steps past ke read zeros
+  // K steps [ks, ke) of this work-group, dealt to its groups in turn (rows
+  // that do not start on a 128-byte line share lines between neighbouring
+  // steps, which are then in flight together); nk: those of the first group,
+  // steps past ke read zeros
   const int nk_all = (int)((p.K + 63) / 64);
-  int ks = (int)((int64_t)split * nk_all / p.splits);
-  int ke = (int)((int64_t)(split + 1) * nk_all / p.splits);
-  int nk = ke - ks;
-  if constexpr (G > 1) {
-    nk = (nk + G - 1) / G;
-    ks += grp * nk;
-    ke = max(ks, min(ke, ks + nk));
-  }
-  const int own = ke - ks;
+  const int ks = (int)((int64_t)split * nk_all / p.splits);
+  const int ke = (int)((int64_t)(split + 1) * nk_all / p.splits);
+  const int nk = (ke - ks + G - 1) / G;
 
   using LdA = std::conditional_t<LA == KC, KcLoad<TM, NW>, McLoad<TM, NW>>;
   using LdB = std::conditional_t<LB == KC, KcLoad<TN, NW>, McLoad<TN, NW>>;
@@ -373,10 +378,12 @@ __device__ __forceinline__ void tile_body(const TileParams& p, int block,
   if constexpr (LB == KC) db.init(p.b, p.ldb, n0, p.N, p.K, wave, lane);
   else db.init(p.b, p.ldb, n0, p.K, wave, lane);
   auto issue_a = [&](char* dst, int kt) {
-    da.issue(dst, ks + kt, kt < own, wave);
+    const int st = ks + G * kt + grp;
+    da.issue(dst, st, st < ke, wave);
   };
   auto issue_b = [&](char* dst, int kt) {
-    db.issue(dst, ks + kt, kt < own, wave);
+    const int st = ks + G * kt + grp;
+    db.issue(dst, st, st < ke, wave);
   };
 
   f32x16_t acc[MI][NJ];
@@ -386,18 +393,30 @@ __device__ __forceinline__ void tile_body(const TileParams& p, int block,
     for (int j = 0; j < NJ; ++j) acc[i][j] = f32x16_t{};
 
   using std::integral_constant;
-  auto bufb = [&](auto nc) -> char* {
-    constexpr int n = decltype(nc)::value % 3;
-    if constexpr (n == 0) return b0 + grp * (TN * 128);
-    else if constexpr (n == 1) return b1 + grp * (TN * 128);
-    else return b2 + grp * (TN * 128);
-  };
+  constexpr int kStage = (TM + TN) * 128;      // a group's part of a stage
+  constexpr int R = S::kStages;
+  constexpr int kAhead = R ? R - 1 : 1;        // steps that A is loaded ahead
+  constexpr int kAheadB = R ? R - 1 : 2;
+  constexpr int kRing = R ? R : 6;             // steps until buffers repeat
   auto bufa = [&](auto nc) -> char* {
-    if constexpr (decltype(nc)::value % 2 == 0) return a0 + grp * (TM * 128);
-    else return a1 + grp * (TM * 128);
+    constexpr int n = decltype(nc)::value;
+    if constexpr (R > 0) {
+      char* const s[5] = {b0, b1, b2, a0, a1};
+      return s[n % R] + grp * kStage;
+    } else {
+      return n % 2 == 0 ? a0 : a1;
+    }
+  };
+  auto bufb = [&](auto nc) -> char* {
+    constexpr int n = decltype(nc)::value;
+    if constexpr (R > 0) return bufa(nc) + TM * 128;
+    else return n % 3 == 0 ? b0 : n % 3 == 1 ? b1 : b2;
   };
   using I0 = integral_constant<int, 0>;
   using I1 = integral_constant<int, 1>;
+  using I2 = integral_constant<int, 2>;
+  using I3 = integral_constant<int, 3>;
+  using I4 = integral_constant<int, 4>;
   // Fragment offsets, passed through an empty asm at each use so that the
   // compiler forms addresses when they are needed instead of holding one
   // per buffer, slice and operand.
@@ -463,32 +482,34 @@ __device__ __forceinline__ void tile_body(const TileParams& p, int block,
   using ZF = integral_constant<int, MI>;
   constexpr int kNR = (LA == KC ? MI : 2 * MI) + (LB == KC ? NJ : 2 * NJ);
   constexpr int kNM = MI * NJ;
-  // this wave's loads but the last of B (two steps ahead) have landed and
-  // its reads of the step's buffers are done, then every wave's
-  static_assert(LdB::J < 16, "vmcnt field");
-  constexpr int kWait = LdB::J | (0x7 << 4);   // vmcnt(J) lgkmcnt(0)
+  // this wave's loads of the next step have landed (in order; those of the
+  // steps behind it are in flight) and its reads of the step's buffers are
+  // done, then every wave's
+  constexpr int kInFlight = (kAhead - 1) * LdA::J + (kAheadB - 1) * LdB::J;
+  static_assert(kInFlight < 16, "vmcnt field");
   auto publish = [&]() {
-    __builtin_amdgcn_s_waitcnt(kWait);
+    __builtin_amdgcn_s_waitcnt(kInFlight | (0x7 << 4));   // and lgkmcnt(0)
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-  Frg cur, nxt;
   int k = 0;
-  // Step k (j = k mod 6): B_k in B buffer j % 3, A_k in A buffer j % 2;
-  // A_{k+1} lands in the other A buffer from the first slice on, B_{k+2} in
-  // the B buffer that step k - 1 has left from the second.
+  Frg cur, nxt;
+  // Step k (j = k mod kRing): the loads of A for step k + kAhead go out in
+  // the first slice, those of B for step k + kAheadB in the second, into the
+  // buffers that step k - 1 has left.
   auto rstep = [&](auto jc) {
     constexpr int j = decltype(jc)::value;
     char* const b = bufb(integral_constant<int, j>{});
     char* const a = bufa(integral_constant<int, j>{});
     char* const bn = bufb(integral_constant<int, j + 1>{});
     char* const an = bufa(integral_constant<int, j + 1>{});
-    char* const bn2 = bufb(integral_constant<int, j + 2>{});
+    char* const aw = bufa(integral_constant<int, j + kAhead>{});
+    char* const bw = bufb(integral_constant<int, j + kAheadB>{});
 #pragma unroll
     for (int kk = 0; kk < kSl - 1; ++kk) {
-      if (kk == 0) issue_a(an, k + 1);
-      if (kk == 1) issue_b(bn2, k + 2);
+      if (kk == 0) issue_a(aw, k + kAhead);
+      if (kk == 1) issue_b(bw, k + kAheadB);
       read(nxt, a, b, kk + 1);
       mma(cur, Z0{}, ZF{});
       cur = nxt;
@@ -509,37 +530,42 @@ __device__ __forceinline__ void tile_body(const TileParams& p, int block,
     __builtin_amdgcn_sched_barrier(0);
     ++k;
   };
-  // prologue: B_0 and A_0, then B_1 (left in flight)
+  // prologue: step 0, then what the first steps find in flight
   issue_b(bufb(I0{}), 0);
   issue_a(bufa(I0{}), 0);
   issue_b(bufb(I1{}), 1);
+  if constexpr (R > 0) issue_a(bufa(I1{}), 1);
+  if constexpr (R > 3) {
+    issue_b(bufb(I2{}), 2);
+    issue_a(bufa(I2{}), 2);
+    issue_b(bufb(I3{}), 3);
+    issue_a(bufa(I3{}), 3);
+  }
   publish();
   read(cur, bufa(I0{}), bufb(I0{}), 0);
-  for (int tr = nk / 6; tr > 0; --tr) {
-    rstep(integral_constant<int, 0>{});
-    rstep(integral_constant<int, 1>{});
-    rstep(integral_constant<int, 2>{});
-    rstep(integral_constant<int, 3>{});
-    rstep(integral_constant<int, 4>{});
-    rstep(integral_constant<int, 5>{});
-  }
-  const int rem = nk % 6;
-  if (rem > 0) {
-    rstep(integral_constant<int, 0>{});
-    if (rem > 1) {
-      rstep(integral_constant<int, 1>{});
-      if (rem > 2) {
-        rstep(integral_constant<int, 2>{});
-        if (rem > 3) {
-          rstep(integral_constant<int, 3>{});
-          if (rem > 4) rstep(integral_constant<int, 4>{});
-        }
-      }
+  for (int tr = nk / kRing; tr > 0; --tr) {
+    rstep(I0{});
+    rstep(I1{});
+    rstep(I2{});
+    if constexpr (kRing > 3) {
+      rstep(I3{});
+      rstep(I4{});
     }
+    if constexpr (kRing > 5) rstep(integral_constant<int, 5>{});
+  }
+  const int rem = nk % kRing;
+  if (rem > 0) rstep(I0{});
+  if (rem > 1) rstep(I1{});
+  if constexpr (kRing > 3) {
+    if (rem > 2) rstep(I2{});
+    if (rem > 3) rstep(I3{});
+    if constexpr (kRing > 5)
+      if (rem > 4) rstep(I4{});
   }
 
-  // every wave is past its last read of the buffers (and every direct load
-  // has landed) before they become epilogue staging
+  // every wave is past its last read of the buffers and every direct load
+  // has landed before they become epilogue staging
+  __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0)
   __syncthreads();
   float* const part = EPI == kEpiPlain && p.splits > 1
                           ? p.part + (int64_t)split * p.M * p.ldp
@@ -567,31 +593,28 @@ __device__ __forceinline__ void tile_body(const TileParams& p, int block,
     }
   };
   if constexpr (G > 1) {
-    // the groups' float32 tiles side by side (256-byte rows, 16 KiB each in
-    // b0 and b1), then one run of 8 columns per thread, groups in order
-    static_assert(MI == 1 && NJ == 1 && TM == 64 && TN == 64 && G == 4,
+    // the groups' float32 tiles (256-byte rows, 16 KiB each), then one run of
+    // 8 columns per thread, groups in order
+    static_assert(MI == 1 && NJ == 1 && TM == 64 && TN == 64 && G == 2,
                   "group sums");
-    char* const mine = (grp < 2 ? b0 : b1) + (grp & 1) * (64 * 256);
+    char* const mine = grp == 0 ? b0 : b1;
 #pragma unroll
     for (int r = 0; r < 16; ++r)
       *reinterpret_cast<float*>(
           mine + (32 * wm + gg::acc_row(0, r, lane)) * 256 +
           (32 * wn + (lane & 31)) * 4) = acc[0][0][r];
     __syncthreads();
-    if (t < 512) {
-      const int row = t >> 3, c8 = t & 7;
-      float v[8] = {};
+    const int row = t >> 3, c8 = t & 7;
+    float v[8] = {};
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const char* src =
-            (g < 2 ? b0 : b1) + (g & 1) * (64 * 256) + row * 256 + c8 * 32;
-        const float4 x = *reinterpret_cast<const float4*>(src);
-        const float4 y = *reinterpret_cast<const float4*>(src + 16);
-        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
-      }
-      run_out(m0 + row, n0 + 8 * c8, v);
+    for (int g = 0; g < G; ++g) {
+      const char* src = (g == 0 ? b0 : b1) + row * 256 + c8 * 32;
+      const float4 x = *reinterpret_cast<const float4*>(src);
+      const float4 y = *reinterpret_cast<const float4*>(src + 16);
+      v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+      v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
     }
+    run_out(m0 + row, n0 + 8 * c8, v);
   } else {
   // Passes of 32 columns through the wave's own LDS: float32, 128-byte
   // rows, 16-byte chunk c of row r at c ^ (r & 7); on readback lane l takes
@@ -673,17 +696,19 @@ __device__ __forceinline__ void tile_body(const TileParams& p, int block,
   }
 }
 
-#define MOE_LIN_STAGES(TM, TN)                                               \
-  constexpr int kG = TileShape<TM, TN>::G;                                   \
-  __shared__ __attribute__((aligned(1024))) char b0[kG * TN * 128];          \
-  __shared__ __attribute__((aligned(1024))) char b1[kG * TN * 128];          \
-  __shared__ __attribute__((aligned(1024))) char b2[kG * TN * 128];          \
-  __shared__ __attribute__((aligned(1024))) char a0[kG * TM * 128];          \
-  __shared__ __attribute__((aligned(1024))) char a1[kG * TM * 128];
+#define MOE_LIN_STAGES(TM, TN)                                              \
+  constexpr int kG = TileShape<TM, TN>::G;                                  \
+  constexpr int kStg = TileShape<TM, TN>::kStages;                          \
+  constexpr int kB = kStg ? kG * (TM + TN) * 128 : TN * 128;                \
+  constexpr int kA = kStg == 5 ? kB : kStg ? 16 : TM * 128;                 \
+  __shared__ __attribute__((aligned(1024))) char b0[kB];                    \
+  __shared__ __attribute__((aligned(1024))) char b1[kB];                    \
+  __shared__ __attribute__((aligned(1024))) char b2[kB];                    \
+  __shared__ __attribute__((aligned(1024))) char a0[kA];                    \
+  __shared__ __attribute__((aligned(1024))) char a1[kA];
 
 template <int TM, int TN, int LA, int LB, int EPI>
-__global__ __launch_bounds__((TileShape<TM, TN>::kThreads),
-                             (TileShape<TM, TN>::kWavesPerSimd)) void
+__global__ __launch_bounds__((TileShape<TM, TN>::kThreads), 2) void
 linear_tile_kernel(TileParams p) {
 #ifdef __HIP_DEVICE_COMPILE__   // (the host pass needs the launch stub only)
   MOE_LIN_STAGES(TM, TN)
@@ -695,8 +720,7 @@ linear_tile_kernel(TileParams p) {
 // whose tiles take longer, the others behind them, so that the second fills
 // the CUs that the first leaves idle.
 template <int TM, int TN>
-__global__ __launch_bounds__((TileShape<TM, TN>::kThreads),
-                             (TileShape<TM, TN>::kWavesPerSimd)) void
+__global__ __launch_bounds__((TileShape<TM, TN>::kThreads), 2) void
 linear_grads_kernel(TileParams px, TileParams pw, int first, int x_first) {
 #ifdef __HIP_DEVICE_COMPILE__
   MOE_LIN_STAGES(TM, TN)
