@@ -110,40 +110,50 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, double* us = nullptr) {
 // Both gradient products of a linear layer: one launch of one tile shape for
 // both where that is estimated to be faster than two (small products leave
 // CUs idle, large ones their last round), else each by itself.
+//
+// The joint launch has its own constants (75 layers, 5000 timed combinations
+// of tile and splits; the choice is 1% slower than the best one on average, 8%
+// at worst).  It takes
+//   all work-groups resident, each on its own CU: the longer product's
+//     steps * lat + fix
+//   else the work divided by the slots and part of a work-group's time on a
+//     full CU for the uneven end, and at least the former.
 struct GradPlan {
   bool joint;
   bool x_first;
   Plan x, w;
 };
+constexpr TileCost kGradTiles[] = {{256, 256, 1, 1, 1.1, 0.0, 9.5, 512},
+                                   {128, 128, 2, 1, 0.6, 0.36, 2.4, 256},
+                                   {64, 128, 2, 1, 0.45, 0.25, 1.3, 256},
+                                   {64, 64, 1, 2, 0.5, 0.0, 1.7, 512}};
 GradPlan plan_grads(int64_t M, int N, int K) {
   const Product px{M, K, N}, pw{N, K, M};
   double ux, uw;
   GradPlan best{false, true, plan_product(M, K, N, &ux),
                 plan_product(N, K, M, &uw)};
-  double best_us = ux + uw + kLaunchUs;
-  for (const auto& c : kTiles) {
+  double best_us = ux + uw + 4.5;
+  for (const auto& c : kGradTiles) {
     const int64_t slots = (int64_t)kCus * c.per_cu;
-    // a work-group's share of its slot when the chip is full
-    auto full_us = [&](const Product& p, int S) {
-      return p.steps(c, S) * std::max(c.lat, c.thr * c.per_cu) +
-             c.fix * c.per_cu;
-    };
     for (int sx = 1; sx <= kMaxSplits && px.can_split(sx); ++sx)
       for (int sw = 1; sw <= kMaxSplits && pw.can_split(sw); ++sw) {
-        const double fx = full_us(px, sx), fw = full_us(pw, sw);
-        const double work = ((double)px.groups(c, sx) * fx +
-                             (double)pw.groups(c, sw) * fw) / slots;
-        const int64_t n = px.groups(c, sx) + pw.groups(c, sw);
-        if (!fits_launch(c, n)) continue;
-        // the shorter product's groups fill the tail of the longer one
-        double t = std::max(std::max(fx, fw), work + 0.5 * std::min(fx, fw));
-        if (n <= slots) t = std::max(fx, fw);   // one round
-        if (n <= kCus)
-          t = std::max(px.steps(c, sx), pw.steps(c, sw)) * c.lat + c.fix;
+        const double stx = px.steps(c, sx), stw = pw.steps(c, sw);
+        const double step = std::max(c.lat, c.thr * c.per_cu);
+        const double fx = stx * step + c.fix * c.per_cu;   // on a full CU
+        const double fw = stw * step + c.fix * c.per_cu;
+        const double longer = std::max(fx, fw);
+        const int64_t nx = px.groups(c, sx), nw = pw.groups(c, sw);
+        if (!fits_launch(c, nx + nw)) continue;
+        const double work = ((double)nx * fx + (double)nw * fw) / slots;
+        double t = std::max(stx, stw) * c.lat + c.fix;     // each on a CU
+        if (nx + nw > slots)
+          t = std::max(t, work + 0.2 * std::min(fx, fw) + 0.3 * longer);
+        else if (nx + nw > kCus)
+          t = std::max(t, std::min(longer, work + 0.45 * longer));
         // (db needs the finishing launch anyway, but the plan must not depend
         // on whether it is asked for)
         if (sx > 1 || sw > 1)
-          t += kLaunchUs / 2 + px.partial_us(sx) + pw.partial_us(sw);
+          t += 1.1 + px.partial_us(sx) + pw.partial_us(sw);
         if (t < best_us) {
           best_us = t;
           best = GradPlan{true, fx >= fw, Plan{c.tm, c.tn, sx},
