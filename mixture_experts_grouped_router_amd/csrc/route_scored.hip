@@ -33,7 +33,8 @@
 //
 // Bound by VALU work (one float64 exponential per logit with a bias or
 // group sums, the networks, one exponential and division per weight); the
-// row is read once.
+// row is read once.  16384 tokens, E 128, k 8: 7.5 us without a bias, 13.3
+// with sigmoid scores, bias and groups; one token 6.0 (one wave's chain).
 #include <type_traits>
 
 #include "common.hpp"
@@ -625,8 +626,8 @@ __global__ __launch_bounds__(256) void route_scored_kernel(
 //     softmax   dl_e = s_e (G_e - sum_i s_i g_i), G the scattered g
 // in float64.  Bound by writing dlogits: lane j computes slot j, the values
 // are scattered into the token's row in LDS and the row leaves in 16-byte
-// streaming stores.  An id outside [0, E) contributes nothing; one named
-// twice adds both contributions.
+// streaming stores (32767 tokens, E 256, sigmoid: 7.6 us, 4.8 TB/s).  An id
+// outside [0, E) contributes nothing; one named twice adds both contributions.
 template <int LPT, int VPL>
 __global__ __launch_bounds__(256) void route_scored_bwd_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
