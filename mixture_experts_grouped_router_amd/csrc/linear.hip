@@ -143,17 +143,15 @@ GradPlan plan_grads(int64_t M, int N, int K) {
         const double fw = stw * step + c.fix * c.per_cu;
         const double longer = std::max(fx, fw);
         const int64_t nx = px.groups(c, sx), nw = pw.groups(c, sw);
-        if (!fits_launch(c, nx + nw)) continue;
+        if (!fits_launch(c, nx + nw + cdiv(N, 16))) continue;   // and db's
         const double work = ((double)nx * fx + (double)nw * fw) / slots;
         double t = std::max(stx, stw) * c.lat + c.fix;     // each on a CU
         if (nx + nw > slots)
           t = std::max(t, work + 0.2 * std::min(fx, fw) + 0.3 * longer);
         else if (nx + nw > kCus)
           t = std::max(t, std::min(longer, work + 0.45 * longer));
-        // (db needs the finishing launch anyway, but the plan must not depend
-        // on whether it is asked for)
         if (sx > 1 || sw > 1)
-          t += 1.1 + px.partial_us(sx) + pw.partial_us(sw);
+          t += 2.5 + px.partial_us(sx) + pw.partial_us(sw);
         if (t < best_us) {
           best_us = t;
           best = GradPlan{true, fx >= fw, Plan{c.tm, c.tn, sx},
@@ -216,44 +214,16 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(TileParams p) {
   reduce_run<ACT>(p, (int64_t)blockIdx.x * 256 + threadIdx.x);
 }
 
-// db[c] = sum over the row chunks: 16 columns per block, 16 strided partial
-// sums each (a thread loads eight chunks before it adds them), then a tree
-__device__ __forceinline__ void db_columns(const float* __restrict__ part,
-                                           int chunks, int N, int block,
-                                           float* __restrict__ db) {
-  __shared__ float red[16][17];
-  const int lane = threadIdx.x & 15, ct = threadIdx.x >> 4;
-  const int c = block * 16 + lane;
-  const float* src = part + min(c, N - 1);
-  float s = 0.0f;
-  for (int i0 = ct; i0 < chunks; i0 += 128) {
-    float v[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      v[u] = src[(int64_t)min(i0 + 16 * u, chunks - 1) * N];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) s += i0 + 16 * u < chunks ? v[u] : 0.0f;
-  }
-  red[ct][lane] = s;
-  __syncthreads();
-#pragma unroll
-  for (int h = 8; h >= 1; h >>= 1) {
-    if (ct < h) red[ct][lane] += red[ct + h][lane];
-    __syncthreads();
-  }
-  if (ct == 0 && c < N) db[c] = red[0][lane];
-}
-
 // What is left of a backward after its products, in one launch: db from its
-// partial sums (bd work-groups), then the split partials of dx (bx) and dW.
-// Bound by reading the partials (from the caches, mostly): 7 us with five
-// partials of 768 x 2048, 3.9 us for db of 2047 columns alone.
+// partial sums (bd work-groups; none after a joint launch), then the split
+// partials of dx (bx) and dW.  Bound by reading the partials (from the caches,
+// mostly): 7 us with five partials of 768 x 2048.
 __global__ __launch_bounds__(256) void linear_finish_kernel(
-    const float* __restrict__ db_part, int chunks, int N, float* db, int bd,
-    TileParams px, int bx, TileParams pw) {
+    DbSum d, int N, int bd, TileParams px, int bx, TileParams pw) {
+  __shared__ float red[272];
   const int b = blockIdx.x;
   if (b < bd)
-    db_columns(db_part, chunks, N, b, db);
+    db_columns(d, N, b, red);
   else if (b < bd + bx)
     reduce_run<ACT_NONE>(px, (int64_t)(b - bd) * 256 + threadIdx.x);
   else
@@ -586,22 +556,21 @@ hipError_t launch_linear_bwd(int64_t M, int N, int K, int act, const void* dy,
     pw.ldc = K;
     gw = tile_grid(pw, gp.w, take(gp.w.part_bytes(N, K)));
   }
+  const DbSum sums{db_part, (int)chunks, db_shift(chunks), db};
+  const int64_t db_groups = db ? cdiv(N, (int64_t)1 << sums.cs) : 0;
   if (gp.joint) {
     KernelScope ks("linear_grads", stream);
-    const unsigned grid = gx + gw;
-    const int first = (int)(gp.x_first ? gx : gw), xf = gp.x_first ? 1 : 0;
-    if (gp.x.tm == 256)
-      hipLaunchKernelGGL((linear_grads_kernel<256, 256>), dim3(grid),
-                         dim3(512), 0, stream, px, pw, first, xf);
-    else if (gp.x.tm == 128)
-      hipLaunchKernelGGL((linear_grads_kernel<128, 128>), dim3(grid),
-                         dim3(256), 0, stream, px, pw, first, xf);
-    else if (gp.x.tn == 128)
-      hipLaunchKernelGGL((linear_grads_kernel<64, 128>), dim3(grid),
-                         dim3(256), 0, stream, px, pw, first, xf);
-    else
-      hipLaunchKernelGGL((linear_grads_kernel<64, 64>), dim3(grid),
-                         dim3(512), 0, stream, px, pw, first, xf);
+    const unsigned grid = gx + gw + (unsigned)db_groups;
+    const int first = (int)(gp.x_first ? gx : gw);
+    const int second = (int)(gx + gw) - first, xf = gp.x_first ? 1 : 0;
+    auto go = [&](auto kern, int threads) {
+      hipLaunchKernelGGL(kern, dim3(grid), dim3(threads), 0, stream, px, pw,
+                         first, second, xf, sums);
+    };
+    if (gp.x.tm == 256) go(linear_grads_kernel<256, 256>, 512);
+    else if (gp.x.tm == 128) go(linear_grads_kernel<128, 128>, 256);
+    else if (gp.x.tn == 128) go(linear_grads_kernel<64, 128>, 256);
+    else go(linear_grads_kernel<64, 64>, 512);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   } else {
@@ -618,13 +587,12 @@ hipError_t launch_linear_bwd(int64_t M, int N, int K, int act, const void* dy,
       if (e != hipSuccess) return e;
     }
   }
-  const int64_t bd = db ? cdiv(N, 16) : 0, bx = reduce_blocks(px),
+  const int64_t bd = gp.joint ? 0 : db_groups, bx = reduce_blocks(px),
                 bw = reduce_blocks(pw);
   if (bd + bx + bw == 0) return e;
   KernelScope ks("linear_finish", stream);
   hipLaunchKernelGGL(linear_finish_kernel, dim3((unsigned)(bd + bx + bw)),
-                     dim3(256), 0, stream, db_part, (int)chunks, N, db,
-                     (int)bd, px, (int)bx, pw);
+                     dim3(256), 0, stream, sums, N, (int)bd, px, (int)bx, pw);
   return hipGetLastError();
 }
 

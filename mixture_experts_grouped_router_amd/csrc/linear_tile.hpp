@@ -716,17 +716,61 @@ linear_tile_kernel(TileParams p) {
 #endif
 }
 
+// db[c] = sum over the row chunks of the dz pass: 2^cs columns per work-group,
+// its first 256 threads take 256 / 2^cs strided partial sums each (a thread
+// loads eight chunks before it adds them), then a tree.  red: 272 floats of
+// LDS.  Few chunks take many columns: next to tiles a work-group occupies a
+// tile's LDS, and 749 of them (42 x 11984) took 2.5 us longer than 47.
+struct DbSum {
+  const float* part;   // [chunks][N]
+  int chunks, cs;
+  float* db;           // null: not asked for
+};
+__host__ __device__ inline int db_shift(int64_t chunks) {
+  return chunks <= 8 ? 8 : chunks <= 32 ? 6 : 4;
+}
+__device__ __forceinline__ void db_columns(const DbSum& d, int N, int block,
+                                           float* red) {
+  const int C = 1 << d.cs, P = 256 >> d.cs;
+  const int t = threadIdx.x, lane = t & (C - 1), ct = t >> d.cs;
+  const int c = (block << d.cs) + lane;
+  const float* src = d.part + min(c, N - 1);
+  if (t < 256) {
+    float s = 0.0f;
+    for (int i0 = ct; i0 < d.chunks; i0 += 8 * P) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        v[u] = src[(int64_t)min(i0 + P * u, d.chunks - 1) * N];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += i0 + P * u < d.chunks ? v[u] : 0.0f;
+    }
+    red[ct * (C + 1) + lane] = s;
+  }
+  __syncthreads();
+  for (int h = P >> 1; h >= 1; h >>= 1) {
+    if (ct < h) red[ct * (C + 1) + lane] += red[(ct + h) * (C + 1) + lane];
+    __syncthreads();
+  }
+  if (ct == 0 && c < N) d.db[c] = red[lane];
+}
+
 // dx = dz W and dW = dz^T x in one launch: `first` work-groups for the one
-// whose tiles take longer, the others behind them, so that the second fills
-// the CUs that the first leaves idle (16384 x 768 x 2048: 97 us, 1063 TFLOP/s;
-// 1001 x 2047 x 1032: 21.8 us).
+// whose tiles take longer, then `second` for the other, so that the second
+// fills the CUs that the first leaves idle (16384 x 768 x 2048: 97 us, 1063
+// TFLOP/s; 1001 x 2047 x 1032: 21.8 us).  Work-groups behind them sum db from
+// the partial sums that the dz pass left.
 template <int TM, int TN>
 __global__ __launch_bounds__((TileShape<TM, TN>::kThreads), 2) void
-linear_grads_kernel(TileParams px, TileParams pw, int first, int x_first) {
+linear_grads_kernel(TileParams px, TileParams pw, int first, int second,
+                    int x_first, DbSum d) {
 #ifdef __HIP_DEVICE_COMPILE__
   MOE_LIN_STAGES(TM, TN)
   const int b = blockIdx.x;
-  if ((b < first) == (x_first != 0))
+  if (b >= first + second)
+    db_columns(d, (int)pw.M, b - first - second,
+               reinterpret_cast<float*>(b0));
+  else if ((b < first) == (x_first != 0))
     tile_body<TM, TN, KC, MC, kEpiPlain>(px, x_first ? b : b - first, b0, b1,
                                          b2, a0, a1);
   else

@@ -168,6 +168,22 @@ def test_partial_gradients(m, want):
         assert torch.equal(g[n], full[n])
 
 
+@pytest.mark.parametrize("M,N,K", [(5, 700, 64), (40, 513, 136),
+                                   (250, 90, 64), (700, 260, 72)])
+def test_bias_gradient_with_either_product(m, M, N, K):
+    """db is summed next to both products, or after one, or alone: the same
+    bits, for every way its partial sums are dealt (1, 5, 32 and 88 chunks of
+    rows)."""
+    d = make(M, N, K, 8)
+    full = check_bwd(m, d, "gelu")
+    for dx, dw in ((1, 0), (0, 1), (0, 0)):
+        g = m.moe_linear_bwd(dev(d["dy"]), dev(d["x"]), dev(d["w"]), act=2,
+                             z=dev(d["z"]), want_dx=bool(dx),
+                             want_dw=bool(dw), want_db=True)
+        for n in g:
+            assert torch.equal(g[n], full[n]), (n, dx, dw)
+
+
 @pytest.mark.parametrize("act", ACTS[1:])
 def test_activation_range(m, act):
     """Every magnitude of z through the activation and its derivative: K = 8
