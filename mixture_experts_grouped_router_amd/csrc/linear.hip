@@ -313,6 +313,21 @@ hipError_t launch_skinny(const TileParams& p, hipStream_t stream) {
 // blocks, row chunks).
 constexpr int kDzU = 4;
 
+// v's 16-bit values moved down by sh (0 to 7) places, zeros behind them
+__device__ __forceinline__ u32x4_a2_t shift_down(const u32x4_a2_t& v,
+                                                 int sh) {
+  uint64_t lo = v[0] | (uint64_t)v[1] << 32, hi = v[2] | (uint64_t)v[3] << 32;
+  if (sh & 4) {
+    lo = hi;
+    hi = 0;
+  }
+  const int b = 16 * (sh & 3);
+  lo = lo >> b | (b ? hi << (64 - b) : 0ull);
+  hi >>= b;
+  return u32x4_a2_t{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi,
+                    (uint32_t)(hi >> 32)};
+}
+
 template <int ACT>
 __global__ __launch_bounds__(256) void linear_dz_kernel(
     const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z,
@@ -336,12 +351,14 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(
           make_uint4(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]),
                      pack_bf16x2(g[4], g[5]), pack_bf16x2(g[6], g[7]));
   };
-  if (col + 8 <= N) {
+  if (N >= 8 && col < N) {
+    // a run that crosses the row's end: the row's last 8 values, moved down
+    const int cl = min(col, N - 8), sh = col - cl;
     for (int64_t rb = r0 + rt; rb < r1; rb += 8 * kDzU) {
       u32x4_a2_t a[kDzU], b[kDzU];
 #pragma unroll
       for (int u = 0; u < kDzU; ++u) {
-        const int64_t at = min(rb + 8 * u, r1 - 1) * N + col;
+        const int64_t at = min(rb + 8 * u, r1 - 1) * N + cl;
         a[u] = *reinterpret_cast<const u32x4_a2_t*>(dy + at);
         if constexpr (ACT != ACT_NONE)
           b[u] = *reinterpret_cast<const u32x4_a2_t*>(z + at);
@@ -349,6 +366,10 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(
 #pragma unroll
       for (int u = 0; u < kDzU; ++u) {
         if (rb + 8 * u >= r1) break;
+        if (sh) {
+          a[u] = shift_down(a[u], sh);
+          if constexpr (ACT != ACT_NONE) b[u] = shift_down(b[u], sh);
+        }
         float g[8], zz[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -362,7 +383,7 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(
         row(rb + 8 * u, g, zz);
       }
     }
-  } else if (col < ldz) {   // the row's tail (loads clamped, then masked)
+  } else if (col < N) {   // rows of less than 8 (loads clamped, then masked)
     for (int64_t rb = r0 + rt; rb < r1; rb += 8 * kDzU) {
       uint16_t a[kDzU][8], b[kDzU][8];
 #pragma unroll
