@@ -117,25 +117,29 @@ __device__ __forceinline__ void lds_groups(const double (&gv)[VPL],
     sg[g] = top2 ? a1 + a2 : a1;
   }
   lds_wave_fence();
+  // a lane ranks group g0 + s; bit g of kept: the token keeps group g
+  const int lane = threadIdx.x & 63;
+  uint64_t kept = 0;
+  for (int g0 = 0; g0 < o.n_group; g0 += LPT) {   // uniform; n_group <= 64
+    const int g = g0 + s;
+    bool keep = false;
+    if (g < o.n_group) {
+      const double mine = sg[g];
+      int ahead = 0;
+      for (int h = 0; h < o.n_group; ++h)
+        ahead += beats(sg[h], h, mine, g) ? 1 : 0;
+      keep = ahead < o.topk_group;
+    }
+    const uint64_t b = __ballot(keep);
+    kept |= (LPT == 64 ? b : b >> (lane & 48) & 0xffff) << g0;
+  }
   int g = e0 / gsz, left = gsz - (e0 - g * gsz);
-  bool out = false, fresh = true;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    if (i < C && e0 + i < E) {
-      if (fresh) {
-        const double mine = sg[g];
-        int ahead = 0;
-        for (int h = 0; h < o.n_group; ++h)
-          ahead += beats(sg[h], h, mine, g) ? 1 : 0;
-        out = ahead >= o.topk_group;
-        fresh = false;
-      }
-      if (out) drop(i);
-      if (--left == 0) {
-        ++g;
-        left = gsz;
-        fresh = true;
-      }
+    if (i < C && e0 + i < E && !(kept >> g & 1)) drop(i);
+    if (--left == 0) {
+      ++g;
+      left = gsz;
     }
   }
 }
