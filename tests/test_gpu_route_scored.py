@@ -144,6 +144,19 @@ def test_scores_that_differ_in_their_last_bits(m, E, k, G, tg):
                       topk_group=tg, group_score=gs)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,G,tg", [
+    (50, 192, 8, 8, 4), (50, 192, 16, 4, 2), (50, 160, 2, 5, 3),
+    (50, 145, 7, 1, 1), (50, 130, 8, 2, 1), (50, 176, 12, 16, 5),
+    (50, 189, 6, 63, 20), (50, 240, 8, 60, 31), (50, 190, 1, 38, 17)])
+def test_twelve_experts_per_lane_and_many_groups(m, T, E, k, G, tg, score):
+    """Lists of 2, 8 and 16 over 12 experts per lane; groups in whole lanes,
+    through LDS, and more groups than lanes."""
+    test_route_scored(m, T, E, k, G, tg, score)
+    test_ties_and_signed_zeros(m, score, E, k, G, tg)
+    test_scores_that_differ_in_their_last_bits(m, E, k, G, tg)
+
+
 @pytest.mark.parametrize("E,G,tg", [(128, 1, 1), (64, 4, 2), (60, 3, 2),
                                     (512, 8, 2)])
 def test_masked_experts(m, E, G, tg):
