@@ -185,17 +185,19 @@ __device__ __forceinline__ bool load_inputs(const float* __restrict__ row,
 #pragma unroll
     for (int i = 0; i < VPL; ++i) bv[i] = 0.0f;
   }
+  none = ~0u << max(0, min(C, E - e0));
+  // (what is no expert holds some logit and bias of the row: a bad one is bad
+  // for its own lane too)
   bool bad = false;
-  none = 0;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const bool no = (i >= C) | (e0 + i >= E);
-    const bool nf = !no & !__builtin_isfinite(v[i]);
-    const bool nb = !no & !(bv[i] < INFINITY);   // -inf: a masked expert
-    bad |= nf | nb;
-    none |= no ? 1u << i : 0u;
-    if (no | nf) v[i] = 0.0f;
-    if (no | nb) bv[i] = 0.0f;
+  for (int i = 0; i < VPL; ++i)   // -inf: a masked expert
+    bad |= !__builtin_isfinite(v[i]) | !(bv[i] < INFINITY);
+  if (__any(bad)) {   // uniform
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      if (!__builtin_isfinite(v[i])) v[i] = 0.0f;
+      if (!(bv[i] < INFINITY)) bv[i] = 0.0f;
+    }
   }
   return bad;
 }
@@ -225,6 +227,10 @@ __device__ __forceinline__ double exp_neg(double a) {
   p = fma(p, r, 1.0);
   return __builtin_ldexp(p, a > 709.78 ? -4000 : (int)n);
 }
+
+// exp_neg of it is 0: for what is no expert (a select of the argument; one of
+// the result becomes a branch around every exponential)
+constexpr double kFarBelow = 2000.0;
 
 // 1 / x for 1 <= x <= 2^11: the hardware estimate, two Newton steps to
 // within an ulp, and a third that rounds correctly (saturated scores differ
@@ -285,19 +291,13 @@ __device__ __forceinline__ void sort_desc(double* c) {
             order2(c[i + j], c[i + j + h]);
 }
 
-// a <- the L largest of the descending lists a and b, descending; rej <- the
-// largest value left out so far
-template <int L, bool REJ>
-__device__ __forceinline__ void merge_top(double* a, const double* b,
-                                          double& rej) {
+// a <- the L largest of the descending lists a and b, descending
+template <int L>
+__device__ __forceinline__ void merge_top(double* a, const double* b) {
 #pragma unroll
   for (int i = 0; i < L / 2; ++i) {
     // (pairs i and L - 1 - i together: a[L - 1 - i] is still needed)
     const double x = a[i], y = a[L - 1 - i];
-    if constexpr (REJ) {
-      rej = __builtin_fmax(rej, __builtin_fmin(x, b[L - 1 - i]));
-      rej = __builtin_fmax(rej, __builtin_fmin(y, b[i]));
-    }
     a[i] = __builtin_fmax(x, b[L - 1 - i]);
     a[L - 1 - i] = __builtin_fmax(y, b[i]);
   }
@@ -308,13 +308,12 @@ __device__ __forceinline__ void merge_top(double* a, const double* b,
       if ((i & h) == 0) order2(a[i], a[i + h]);
 }
 
-template <int CTRL, int L, bool REJ>
-__device__ __forceinline__ void merge_lanes(double* a, double& rej) {
+template <int CTRL, int L>
+__device__ __forceinline__ void merge_lanes(double* a) {
   double b[L];
 #pragma unroll
   for (int i = 0; i < L; ++i) b[i] = dpp_d<CTRL>(a[i]);
-  if constexpr (REJ) rej = __builtin_fmax(rej, dpp_d<CTRL>(rej));
-  merge_top<L, REJ>(a, b, rej);
+  merge_top<L>(a, b);
 }
 
 // Selection of one token by the whole wave, full float64 comparisons: lane
@@ -339,7 +338,7 @@ __device__ __forceinline__ int select_wave(
       double part = 0.0;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        gv[i] = (taken >> i & 1u) ? 0.0 : exp_neg(m - (double)v[i]);
+        gv[i] = exp_neg((taken >> i & 1u) ? kFarBelow : m - (double)v[i]);
         part += gv[i];
       }
       const double rz = recip(lanes_sum<64>(part));
@@ -422,7 +421,7 @@ __device__ __forceinline__ void write_slots(
     double part = 0.0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (i < C) part += (none >> i & 1u) ? 0.0 : exp_neg(m - (double)v[i]);
+      part += exp_neg((none >> i & 1u) ? kFarBelow : m - (double)v[i]);
     den = lanes_sum<LPT>(part);
     num = exp(l - m);
   }
@@ -473,7 +472,7 @@ __global__ __launch_bounds__(256) void route_scored16_kernel(
       double part = 0.0;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        gv[i] = (none >> i & 1u) ? 0.0 : exp_neg(m - (double)v[i]);
+        gv[i] = exp_neg((none >> i & 1u) ? kFarBelow : m - (double)v[i]);
         part += gv[i];
       }
       const double rz = recip(lanes_sum<16>(part));
@@ -531,7 +530,6 @@ __global__ __launch_bounds__(256) void route_scored16_kernel(
   }
 
   // the lane's L largest, then the token's
-  double rej = no_key();
   double top[L];
 #pragma unroll
   for (int i = 0; i < L; ++i) top[i] = i < VPL ? c[i] : no_key();
@@ -544,26 +542,35 @@ __global__ __launch_bounds__(256) void route_scored16_kernel(
       for (int i = 0; i < L; ++i)
         more[i] = q + i < VPL ? c[q + i < VPL ? q + i : 0] : no_key();
       sort_desc<L>(more);
-      merge_top<L, BIAS>(top, more, rej);
+      merge_top<L>(top, more);
     }
   }
-  merge_lanes<kDppXor1, L, BIAS>(top, rej);
-  merge_lanes<kDppXor2, L, BIAS>(top, rej);
-  merge_lanes<kDppHalfMirror, L, BIAS>(top, rej);
-  merge_lanes<kDppMirror, L, BIAS>(top, rej);
+  merge_lanes<kDppXor1, L>(top);
+  merge_lanes<kDppXor2, L>(top);
+  merge_lanes<kDppHalfMirror, L>(top);
+  merge_lanes<kDppMirror, L>(top);
 
-  // lane s: slot s and the key behind it
-  double mine = top[0], next = L > 1 ? top[L > 1 ? 1 : 0] : rej;
+  // lane s: slot s
+  double mine = top[0];
 #pragma unroll
-  for (int i = 1; i < L; ++i) {
-    mine = s == i ? top[i] : mine;
-    next = s == i ? (i + 1 < L ? top[i + 1 < L ? i + 1 : i] : rej) : next;
-  }
+  for (int i = 1; i < L; ++i) mine = s == i ? top[i] : mine;
   int my_e = min(packed_expert(mine), E - 1);
   if constexpr (BIAS) {
     // Equal upper bits: fine where every expert with these bits has the very
     // same key (the ids then decide); else the wave selects again.
-    const bool twin = s < k && packed_bits(mine) == packed_bits(next);
+    // Slot s is compared with the key behind it, lane s + 1's; what is behind
+    // a full list is looked for among all keys.
+    const double next = dpp_d<kDppRor0 + 15>(mine);
+    bool twin = s < min(k, L - 1) && packed_bits(mine) == packed_bits(next);
+    if (k == L) {   // uniform
+      bool behind = false;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        behind |= packed_bits(c[i]) == packed_bits(top[L - 1]) &&
+                  c[i] != top[L - 1];
+      const uint64_t rows = __ballot(behind);
+      twin |= s == L - 1 && (rows >> (lane & 48) & 0xffff) != 0;
+    }
     if (__any(twin)) {   // uniform
       bool again = false;
       for (int j = 0; j < k; ++j) {
