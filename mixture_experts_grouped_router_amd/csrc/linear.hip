@@ -426,9 +426,9 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(
 
 // Row chunks of the dz pass.  Few rows are bound by a thread's chain of
 // derivatives: 8 rows per chunk (one per thread) while that takes no more than
-// two blocks per CU; more chunks cost the finishing launch more than they save
-// (1001 x 2047: 36.8 us for the backward with 8 rows, 32.8 with 16, 33.8 with
-// 32; 658 x 35: 15.2, 18.6 and 24.1).  Many rows: about four blocks per CU.
+// two blocks per CU; more chunks cost db's sum more than they save (backward of
+// 1001 x 2047: 27.5 us with 8 rows, 26.3 with 16 or 32; 658 x 35: 9.0 with 8,
+// 10.5 with 32).  Many rows: about four blocks per CU.
 int64_t dz_chunks(int64_t M, int N) {
   const int64_t cb = cdiv(pad8(N), 256);
   return std::max<int64_t>(

@@ -758,7 +758,7 @@ __device__ __forceinline__ void db_columns(const DbSum& d, int N, int block,
 // dx = dz W and dW = dz^T x in one launch: `first` work-groups for the one
 // whose tiles take longer, then `second` for the other, so that the second
 // fills the CUs that the first leaves idle (16384 x 768 x 2048: 97 us, 1063
-// TFLOP/s; 1001 x 2047 x 1032: 21.8 us).  Work-groups behind them sum db from
+// TFLOP/s; 1001 x 2047 x 1032: 20 us).  Work-groups behind them sum db from
 // the partial sums that the dz pass left.
 template <int TM, int TN>
 __global__ __launch_bounds__((TileShape<TM, TN>::kThreads), 2) void
