@@ -43,7 +43,7 @@ struct Plan {
 // (lat: one K step with a CU to itself, thr: its share of a busy CU, fix:
 // prologue and epilogue; the 64 x 64 tile takes two steps at a time); a
 // split adds a launch, the float32 partials' round trip at 6 TB/s (they mostly
-// stay in the caches) and their sum's chain.  The constants come from 2000
+// stay in the caches) and their sum's chain.  The constants come from 4000
 // timed (shape, tile, split) combinations of the three products; the choice is
 // 1% slower than the best combination on average, 22% at worst.
 struct TileCost {
