@@ -203,9 +203,10 @@ __device__ __forceinline__ bool load_inputs(const float* __restrict__ row,
 }
 
 // e^-a for a >= 0: Cody-Waite reduction a = -(n ln 2 + r) with |r| <= ln 2 /
-// 2 and ln 2 in two parts, the Taylor polynomial of degree 13 (remainder
-// below 2^-57), scaling by 2^n.  0 above 709.78, where 1 + e^a overflows: the
-// sigmoid of such a logit is 0.
+// 2 and ln 2 in two parts (its 32 bits behind the point, so that n times them
+// is exact, and the rest), the Taylor polynomial of degree 13 (remainder
+// below 2^-57), scaling by 2^n, which rounds once more where the result is
+// subnormal (a > 708.4) and gives 0 from a = 745.2 on.
 __device__ __forceinline__ double exp_neg(double a) {
   a = fmin(a, 1000.0);   // keeps the reduction exact
   const double n = __builtin_rint(a * -1.4426950408889634);
@@ -225,7 +226,7 @@ __device__ __forceinline__ double exp_neg(double a) {
   p = fma(p, r, 0.5);
   p = fma(p, r, 1.0);
   p = fma(p, r, 1.0);
-  return __builtin_ldexp(p, a > 709.78 ? -4000 : (int)n);
+  return __builtin_ldexp(p, (int)n);
 }
 
 // exp_neg of it is 0: for what is no expert (a select of the argument; one of
@@ -242,9 +243,11 @@ __device__ __forceinline__ double recip(double x) {
   return fma(fma(-x, y, 1.0), y, y);
 }
 
-// sigmoid(l): 1 / (1 + e^-l) or e^l / (1 + e^l), within a few ulp
+// sigmoid(l): 1 / (1 + e^-l) or e^l / (1 + e^l), within a few ulp; 0 where
+// e^-l is beyond the largest float64 (l < -709.783), as in sigmoid64
 __device__ __forceinline__ double sigmoid_key(double l) {
-  const double e = exp_neg(__builtin_fabs(l));
+  const double a = __builtin_fabs(l);
+  const double e = exp_neg(a > 709.782712893384 ? kFarBelow : a);
   const double y = recip(1.0 + e);
   return l < 0.0 ? e * y : y;
 }
