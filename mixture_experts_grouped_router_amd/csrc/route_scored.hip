@@ -670,6 +670,7 @@ __global__ __launch_bounds__(256) void route_scored_bwd_kernel(
       report_error(status, kDevErrExpertId);
       have = false;
       e = 0;
+      gw = 0.0f;   // it may be NaN, and takes part in the token's sums
     }
   }
   const float lf = have ? lrow[e] : 0.0f;
