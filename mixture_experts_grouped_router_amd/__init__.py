@@ -280,6 +280,15 @@ def _out_or_new(out: Optional[torch.Tensor], shape, dtype,
     return out
 
 
+def _need_i32(a: int, b: int, c: int = 0, d: int = 0) -> None:
+    """Sizes and choices that the C interface takes as 32-bit integers (ctypes
+    would pass on the low 32 bits of a larger one)."""
+    if (a | b | c | d) >> 31:   # (not for 0 to 2^31 - 1)
+        for v in (a, b, c, d):
+            if not -0x80000000 <= v <= 0x7fffffff:
+                raise ValueError(f"{v} does not fit 32 bits")
+
+
 def _u64(v: int, name: str) -> int:
     v = int(v)
     if not 0 <= v < 1 << 64:
@@ -429,6 +438,7 @@ def moe_router_bwd(logits: torch.Tensor, topk_idx: torch.Tensor,
 
 def _route_opts(score: int, n_group: int, topk_group: int, group_score: int,
                 renormalize: bool, scale: float) -> _RouteOpts:
+    _need_i32(score, n_group, topk_group, group_score)
     return _RouteOpts(int(score), int(n_group), int(topk_group),
                       int(group_score), int(bool(renormalize)), float(scale))
 
@@ -444,6 +454,9 @@ def moe_route_scored(logits: torch.Tensor, k: int,
     expert groups: logits float32 [T, E] -> (topk_idx int32 [T, k], topk_w
     float32 [T, k])."""
     T, E = logits.shape
+    _need_i32(E, k)
+    o = _route_opts(score, n_group, topk_group, group_score, renormalize,
+                    scale)
     dev = logits.device
     _need(logits, torch.float32, (T, E), "logits")
     _need_on(dev, bias, torch.float32, (E,), "bias")
@@ -451,8 +464,6 @@ def moe_route_scored(logits: torch.Tensor, k: int,
         raise ValueError("k must be positive")
     idx = torch.empty((T, k), dtype=torch.int32, device=dev)
     w = torch.empty((T, k), dtype=torch.float32, device=dev)
-    o = _route_opts(score, n_group, topk_group, group_score, renormalize,
-                    scale)
     _check(load_library().moe_route_scored(
         _context(dev), _ptr(logits), _ptr(bias), T, E, k, ctypes.byref(o),
         _ptr(idx), _ptr(w), _stream()))
@@ -467,12 +478,13 @@ def moe_route_scored_bwd(logits: torch.Tensor, topk_idx: torch.Tensor,
     moe_route_scored's weights (float32 [T, k])."""
     T, E = logits.shape
     k = topk_idx.shape[1]
+    _need_i32(E, k)
+    o = _route_opts(score, 1, 1, GROUP_MAX, renormalize, scale)
     dev = logits.device
     _need(logits, torch.float32, (T, E), "logits")
     _need_on(dev, topk_idx, torch.int32, (T, k), "topk_idx")
     _need_on(dev, dtopk_w, torch.float32, (T, k), "dtopk_w")
     dl = torch.empty((T, E), dtype=torch.float32, device=dev)
-    o = _route_opts(score, 1, 1, GROUP_MAX, renormalize, scale)
     _check(load_library().moe_route_scored_bwd(
         _context(dev), _ptr(logits), _ptr(topk_idx), _ptr(dtopk_w), T, E, k,
         ctypes.byref(o), _ptr(dl), _stream()))
@@ -486,6 +498,7 @@ def moe_router_proj_bwd(dlogits: torch.Tensor, x: torch.Tensor,
     "dw_r" [E, H] and "dx" [T, H], float32."""
     T, E = dlogits.shape
     H = x.shape[1]
+    _need_i32(E, H)
     dev = dlogits.device
     _need(dlogits, torch.float32, (T, E), "dlogits")
     _need_on(dev, x, torch.bfloat16, (T, H), "x")
@@ -636,6 +649,7 @@ def moe_unpermute_dropout(z_perm: torch.Tensor,
     rows, H = z_perm.shape
     if rows % k:
         raise ValueError("z_perm must hold k rows per token")
+    _need_i32(H, k)
     T = rows // k
     dev = z_perm.device
     _need(z_perm, torch.bfloat16, (rows, H), "z_perm")
@@ -665,6 +679,7 @@ def moe_unpermute_dropout_bwd(dy: torch.Tensor,
     if k < 1:
         raise ValueError("k must be positive")
     T, H = dy.shape
+    _need_i32(H, k)
     dev = dy.device
     _need(dy, torch.bfloat16, (T, H), "dy")
     _need_on(dev, row_map, torch.int32, (T * k,), "row_map")
@@ -696,6 +711,7 @@ def moe_linear_fwd(x: torch.Tensor, w: torch.Tensor,
     residual."""
     M, K = x.shape
     N = w.shape[0]
+    _need_i32(N, K, act)
     dev = x.device
     _need(x, torch.bfloat16, (M, K), "x")
     _need_on(dev, w, torch.bfloat16, (N, K), "w")
@@ -736,6 +752,7 @@ def moe_linear_bwd(dy: torch.Tensor, x: Optional[torch.Tensor],
     if ref is None and not want_db:
         raise ValueError("no gradient asked for")
     K = ref.shape[1] if ref is not None else 8
+    _need_i32(N, K, act)
     _need(dy, torch.bfloat16, (M, N), "dy")
     _need_on(dev, x, torch.bfloat16, (M, K), "x")
     _need_on(dev, w, torch.bfloat16, (N, K), "w")
