@@ -5,12 +5,12 @@
 // MoE training for biological foundation models (NVIDIA)", section "Why
 // dense and MoE models differ").
 //
-// The products run on linear_tile.hpp.  dz is one HBM-bound pass that also
+// The products run on linear_tile.hpp (linear_plan.hpp chooses the tile and the
+// split) or, with few rows, on linear_skinny.hpp.  dz is one HBM-bound pass that also
 // sums db; it is rounded to bf16, the operand type of the two products (the
 // saved z is bf16 as well), while db sums the float32 values.
-#include <algorithm>
-
 #include "kernels.hpp"
+#include "linear_plan.hpp"
 #include "linear_skinny.hpp"
 #include "linear_tile.hpp"
 #include "timer.hpp"
@@ -20,171 +20,6 @@ namespace moe {
 using namespace lin;
 
 namespace {
-
-constexpr int kCus = 256;   // MI355X compute units
-constexpr int kMaxSplits = 16;
-constexpr int64_t kMaxPartBytes = (int64_t)256 << 20;
-
-size_t align256(size_t b) { return (b + 255) / 256 * 256; }
-int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-struct Plan {
-  int tm, tn;   // tile
-  int S;        // K splits
-  size_t part_bytes(int64_t M, int64_t N) const {
-    return S > 1 ? align256((size_t)S * M * pad8(N) * sizeof(float)) : 0;
-  }
-};
-
-// Estimated times, in microseconds.  A round of work-groups that puts c of
-// them on a CU takes
-//   steps * max(lat, thr c) + fix c
-// (lat: one K step with a CU to itself, thr: its share of a busy CU, fix:
-// prologue and epilogue; the 64 x 64 tile takes two steps at a time); a
-// split adds a launch, the float32 partials' round trip at 6 TB/s (they mostly
-// stay in the caches) and their sum's chain.  The constants come from 4000
-// timed (shape, tile, split) combinations of the three products; the choice is
-// 1% slower than the best combination on average, 22% at worst.
-struct TileCost {
-  int tm, tn, per_cu, groups;
-  double lat, thr, fix;
-  int threads;
-};
-constexpr TileCost kTiles[] = {{256, 256, 1, 1, 1.15, 0.0, 11.5, 512},
-                               {128, 128, 2, 1, 0.5, 0.4, 2.1, 256},
-                               {64, 128, 2, 1, 0.3, 0.32, 1.4, 256},
-                               {64, 64, 1, 2, 0.4, 0.0, 1.5, 512}};
-// a launch holds fewer than 2^32 threads (the size limits of the entry
-// points leave room for the 128 x 128 tile)
-bool fits_launch(const TileCost& c, int64_t groups) {
-  return groups * c.threads < ((int64_t)1 << 32) - 65536;
-}
-constexpr double kLaunchUs = 3.2;
-
-struct Product {
-  int64_t M, N, K;
-  int64_t groups(const TileCost& c, int S) const {
-    return cdiv(M, c.tm) * cdiv(N, c.tn) * S;
-  }
-  double steps(const TileCost& c, int S) const {
-    return (double)cdiv(cdiv(cdiv(K, 64), S), c.groups);
-  }
-  bool can_split(int S) const {
-    return S == 1 || (S * 2 <= cdiv(K, 64) &&
-                      (int64_t)S * M * pad8(N) * 4 <= kMaxPartBytes);
-  }
-  double partial_us(int S) const {
-    return S > 1 ? S * (0.25 + (double)M * N * 8.0 / 6e6) : 0.0;
-  }
-};
-
-// Tile and split of one product: the least estimated time, also in *us.
-Plan plan_product(int64_t M, int64_t N, int64_t K, double* us = nullptr) {
-  const Product p{M, N, K};
-  Plan best{128, 128, 1};
-  double best_us = 1e30;
-  for (const auto& c : kTiles) {
-    const int64_t slots = (int64_t)kCus * c.per_cu;
-    for (int S = 1; S <= kMaxSplits && p.can_split(S); ++S) {
-      const double st = p.steps(c, S);
-      auto round_us = [&](int64_t groups) {
-        const double occ = (double)cdiv(groups, kCus);
-        return st * std::max(c.lat, c.thr * occ) + c.fix * occ;
-      };
-      const int64_t n = p.groups(c, S), last = n % slots;
-      if (!fits_launch(c, n)) continue;
-      double t = (double)(n / slots) * round_us(slots);
-      if (last) t += round_us(last);
-      if (S > 1) t += kLaunchUs + p.partial_us(S);
-      if (t < best_us) {
-        best_us = t;
-        best = Plan{c.tm, c.tn, S};
-      }
-    }
-  }
-  if (us) *us = best_us;
-  return best;
-}
-
-// Both gradient products of a linear layer: one launch of one tile shape for
-// both where that is estimated to be faster than two (small products leave
-// CUs idle, large ones their last round), else each by itself.
-//
-// The joint launch has its own constants (75 layers, 5000 timed combinations
-// of tile and splits; the choice is 1% slower than the best one on average, 8%
-// at worst).  It takes
-//   all work-groups resident, each on its own CU: the longer product's
-//     steps * lat + fix
-//   else the work divided by the slots and part of a work-group's time on a
-//     full CU for the uneven end, and at least the former.
-struct GradPlan {
-  bool joint;
-  bool x_first;
-  Plan x, w;
-};
-constexpr TileCost kGradTiles[] = {{256, 256, 1, 1, 1.1, 0.0, 9.5, 512},
-                                   {128, 128, 2, 1, 0.6, 0.36, 2.4, 256},
-                                   {64, 128, 2, 1, 0.45, 0.25, 1.3, 256},
-                                   {64, 64, 1, 2, 0.5, 0.0, 1.7, 512}};
-GradPlan plan_grads(int64_t M, int N, int K) {
-  const Product px{M, K, N}, pw{N, K, M};
-  double ux, uw;
-  GradPlan best{false, true, plan_product(M, K, N, &ux),
-                plan_product(N, K, M, &uw)};
-  double best_us = ux + uw + 4.5;
-  for (const auto& c : kGradTiles) {
-    const int64_t slots = (int64_t)kCus * c.per_cu;
-    for (int sx = 1; sx <= kMaxSplits && px.can_split(sx); ++sx)
-      for (int sw = 1; sw <= kMaxSplits && pw.can_split(sw); ++sw) {
-        const double stx = px.steps(c, sx), stw = pw.steps(c, sw);
-        const double step = std::max(c.lat, c.thr * c.per_cu);
-        const double fx = stx * step + c.fix * c.per_cu;   // on a full CU
-        const double fw = stw * step + c.fix * c.per_cu;
-        const double longer = std::max(fx, fw);
-        const int64_t nx = px.groups(c, sx), nw = pw.groups(c, sw);
-        if (!fits_launch(c, nx + nw + cdiv(N, 16))) continue;   // and db's
-        const double work = ((double)nx * fx + (double)nw * fw) / slots;
-        double t = std::max(stx, stw) * c.lat + c.fix;     // each on a CU
-        if (nx + nw > slots)
-          t = std::max(t, work + 0.2 * std::min(fx, fw) + 0.3 * longer);
-        else if (nx + nw > kCus)
-          t = std::max(t, std::min(longer, work + 0.45 * longer));
-        if (sx > 1 || sw > 1)
-          t += 2.5 + px.partial_us(sx) + pw.partial_us(sw);
-        if (t < best_us) {
-          best_us = t;
-          best = GradPlan{true, fx >= fw, Plan{c.tm, c.tn, sx},
-                          Plan{c.tm, c.tn, sw}};
-        }
-      }
-  }
-  return best;
-}
-
-// The plan of the last sizes asked for, per thread: a call asks for the
-// workspace size and then launches, and a layer keeps its sizes.
-template <class P, class F>
-P remembered(int64_t M, int64_t N, int64_t K, F make) {
-  constexpr int kSlots = 64;
-  struct Entry {
-    int64_t M = -1, N, K;
-    P plan;
-  };
-  static thread_local Entry table[kSlots];
-  // (the top bits of an odd multiple: sizes are often multiples of 64)
-  const uint64_t h = ((uint64_t)M * 0x10001 + (uint64_t)N * 0x101 +
-                      (uint64_t)K) * 0x9E3779B97F4A7C15ull;
-  Entry& e = table[h >> 58];
-  if (e.M != M || e.N != N || e.K != K) e = Entry{M, N, K, make()};
-  return e.plan;
-}
-Plan product_plan(int64_t M, int64_t N, int64_t K) {
-  return remembered<Plan>(M, N, K, [&] { return plan_product(M, N, K); });
-}
-GradPlan grad_plan(int64_t M, int N, int K) {
-  return remembered<GradPlan>(M, N, K, [&] { return plan_grads(M, N, K); });
-}
 
 // Sum of the split partials in split order, then the epilogue; a thread
 // takes 8 columns of a row.
@@ -278,15 +113,6 @@ hipError_t launch_forward(TileParams p, const Plan& pl, void* part,
   return hipGetLastError();
 }
 
-// Few rows: one pass over the weights.  Up to 16 rows the MFMA form saves
-// the tile kernel's second launch (4 x 768 x 2048: 4.7 against 7.6 us; 16 x
-// 4096 x 4096: 10.2 against 11.9), but it reads large weights more slowly (16 x
-// 14336 x 4096: 40.9 against 28.1) and does not split a long K over
-// work-groups (16 x 100 x 8192: 16.1 against 10.1).
-bool is_skinny(int64_t M, int64_t N, int64_t K) {
-  return M <= 2 || (M <= kSkinnyMaxM && K <= 4096 &&
-                    N * K <= (int64_t)1 << 24);
-}
 hipError_t launch_skinny(const TileParams& p, hipStream_t stream) {
   KernelScope ks("linear_skinny", stream);
   auto go = [&](auto kern, int rows, int wv) {
@@ -424,18 +250,6 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(
   }
 }
 
-// Row chunks of the dz pass.  Few rows are bound by a thread's chain of
-// derivatives: 8 rows per chunk (one per thread) while that takes no more than
-// two blocks per CU; more chunks cost db's sum more than they save (backward of
-// 1001 x 2047: 27.5 us with 8 rows, 26.3 with 16 or 32; 658 x 35: 9.0 with 8,
-// 10.5 with 32).  Many rows: about four blocks per CU.
-int64_t dz_chunks(int64_t M, int N) {
-  const int64_t cb = cdiv(pad8(N), 256);
-  return std::max<int64_t>(
-      {1, std::min<int64_t>(cdiv(M, 8), 2 * kCus / cb),
-       std::min<int64_t>(cdiv(M, 32), cdiv(4 * kCus, cb))});
-}
-
 }  // namespace
 
 size_t linear_fwd_ws_bytes(int64_t M, int N, int K) {
@@ -475,14 +289,6 @@ hipError_t launch_linear_fwd(int64_t M, int N, int K, int act, const void* x,
 
 // The dz buffer is skipped where dy can be the products' operand itself.
 static bool needs_dz(int N, int act) { return act != ACT_NONE || N % 8 != 0; }
-
-// Tiles and splits are those of both gradients whichever is asked for, so
-// that a gradient's bits do not depend on the other.
-static GradPlan wanted_plan(int64_t M, int N, int K, bool dx, bool dw) {
-  GradPlan g = grad_plan(M, N, K);
-  g.joint = g.joint && dx && dw;
-  return g;
-}
 
 size_t linear_bwd_ws_bytes(int64_t M, int N, int K, int act, bool want_dx,
                            bool want_dw, bool want_db) {

@@ -22,8 +22,6 @@ namespace lin {
 
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kSkinnyMaxM = 16;
-
 // MR rows of x; KS waves per row of W (4: a work-group per row, for few
 // rows of W; 1: a row per wave)
 template <int MR, int KS>
