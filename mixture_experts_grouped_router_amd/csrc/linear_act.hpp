@@ -16,8 +16,8 @@ __device__ __forceinline__ float sigm(float x) {
 // Normal distribution function Phi(z), and e^(-z^2 / 2) in *e.  The tail
 // Phi(-a), a = |z|, is e^(-a^2 / 2) times a function that is smooth in
 // t = 1 / (1 + 0.3 a): a degree-8 polynomial in t without constant term,
-// fitted to erfcx (relative error 1.5e-7 for a <= 14; 4e-6 in float32, from
-// the exponential's argument).  The form keeps the tail's relative accuracy,
+// fitted to erfcx (relative error at most 1.9e-7 for a <= 14, reached at 0;
+// 4e-6 in float32, from the exponential's argument).  The form keeps the tail's relative accuracy,
 // which z Phi(z) shows for negative z.  The library's erfc gave the same
 // bf16 outputs and took 13% of a 8192 x 14336 x 4096 product's time.
 __device__ __forceinline__ float ndtr(float z, float* e) {
