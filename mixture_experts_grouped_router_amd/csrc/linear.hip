@@ -126,7 +126,7 @@ hipError_t launch_skinny(const TileParams& p, hipStream_t stream) {
     if (p.N >= 4 * kCus) go(linear_dot_kernel<2, 1>, 4, 4);
     else go(linear_dot_kernel<2, 4>, 1, 4);
   } else {
-    go(linear_skinny_kernel<1, 1, 8, 4>, 16, 8);
+    go(linear_skinny_kernel, 16, kSkinnyWaves);
   }
   return hipGetLastError();
 }

@@ -86,16 +86,17 @@ __global__ __launch_bounds__(256) void linear_dot_kernel(TileParams p) {
   }
 }
 
-// MB: 16-row blocks of x; NB: 16-row blocks of W; WV: waves; U: 32-wide K
-// steps in flight per wave
-template <int MB, int NB, int WV, int U>
-__global__ __launch_bounds__(64 * WV) void linear_skinny_kernel(TileParams p) {
-  __shared__ float red[WV][NB * MB][256];
+constexpr int kSkinnyWaves = 8;
+constexpr int kSkinnySteps = 4;   // 32-wide K steps in flight per wave
+
+__global__ __launch_bounds__(64 * kSkinnyWaves) void linear_skinny_kernel(
+    TileParams p) {
+  __shared__ float red[kSkinnyWaves][256];
   const int t = threadIdx.x;
   const int lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int n0 = blockIdx.x * (16 * NB);
-  const int nrows = min(16 * NB, p.N - n0);
+  const int n0 = blockIdx.x * 16;
+  const int nrows = min(16, p.N - n0);
   const uint32_t ld = (uint32_t)p.ldb;
   // rows of W or x past the end, and the K tail, read as zeros
   const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
@@ -106,59 +107,35 @@ __global__ __launch_bounds__(64 * WV) void linear_skinny_kernel(TileParams p) {
   const uint32_t kbytes = ld;                  // 2 K
   const uint32_t lk = 16u * (lane >> 4);       // the lane's bytes of a step
   const uint32_t row = (uint32_t)(lane & 15) * ld;
-  f32x4_t acc[NB][MB];
+  f32x4_t acc = {};
+  constexpr uint32_t kChunk = 64u * kSkinnySteps;   // bytes of K per trip
+  for (uint32_t kb = wave * kChunk; kb < kbytes; kb += kSkinnyWaves * kChunk) {
+    bf16x8_t w[kSkinnySteps], x[kSkinnySteps];
 #pragma unroll
-  for (int i = 0; i < NB; ++i)
-#pragma unroll
-    for (int j = 0; j < MB; ++j) acc[i][j] = f32x4_t{};
-  constexpr uint32_t kChunk = 64u * U;         // bytes of K per trip
-  for (uint32_t kb = wave * kChunk; kb < kbytes; kb += WV * kChunk) {
-    bf16x8_t w[U][NB], x[U][MB];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < kSkinnySteps; ++u) {
       const uint32_t k = kb + 64u * u + lk;
-      const bool in = k < kbytes;
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-        w[u][i] = __builtin_bit_cast(
-            bf16x8_t, __builtin_amdgcn_raw_buffer_load_b128(
-                          rw, in ? row + k + 16u * i * ld : kFar, 0, 0));
-#pragma unroll
-      for (int j = 0; j < MB; ++j)
-        x[u][j] = __builtin_bit_cast(
-            bf16x8_t, __builtin_amdgcn_raw_buffer_load_b128(
-                          rx, in ? row + k + 16u * j * ld : kFar, 0, 0));
+      const uint32_t at = k < kbytes ? row + k : kFar;
+      w[u] = __builtin_bit_cast(
+          bf16x8_t, __builtin_amdgcn_raw_buffer_load_b128(rw, at, 0, 0));
+      x[u] = __builtin_bit_cast(
+          bf16x8_t, __builtin_amdgcn_raw_buffer_load_b128(rx, at, 0, 0));
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-#pragma unroll
-        for (int j = 0; j < MB; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              w[u][i], x[u][j], acc[i][j], 0, 0, 0);
+    for (int u = 0; u < kSkinnySteps; ++u)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[u], x[u], acc, 0, 0, 0);
   }
-  // lane: n = 16 i + 4 (lane / 16) + r, m = 16 j + lane % 16
+  // lane: n = 4 (lane / 16) + r, m = lane % 16
 #pragma unroll
-  for (int i = 0; i < NB; ++i)
-#pragma unroll
-    for (int j = 0; j < MB; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        red[wave][i * MB + j][(lane & 15) * 16 + 4 * (lane >> 4) + r] =
-            acc[i][j][r];
+  for (int r = 0; r < 4; ++r)
+    red[wave][(lane & 15) * 16 + 4 * (lane >> 4) + r] = acc[r];
   __syncthreads();
   // outputs, n fastest
-  for (int e = t; e < 256 * NB * MB; e += 64 * WV) {
-    const int n = e % (16 * NB), m = e / (16 * NB);
-    if (n >= nrows || m >= p.M) continue;
-    const int blk = (n >> 4) * MB + (m >> 4);
-    const int at = (m & 15) * 16 + (n & 15);
-    float s = 0.0f;
+  const int n = t & 15, m = t >> 4;
+  if (t >= 256 || n >= nrows || m >= p.M) return;
+  float s = 0.0f;
 #pragma unroll
-    for (int v = 0; v < WV; ++v) s += red[v][blk][at];
-    finish1(p, m, n0 + n, s);
-  }
+  for (int v = 0; v < kSkinnyWaves; ++v) s += red[v][t];
+  finish1(p, m, n0 + n, s);
 }
 
 }  // namespace lin
