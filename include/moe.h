@@ -230,7 +230,8 @@ moe_status_t moe_route_topk(moe_ctx_t ctx, const float* logits, int64_t T,
  * [PG3, practical-implications paragraph: Top-k routing, load imbalance.]
  * The page names top-k routing and load balance but no formula; the library
  * takes these.  Per token, in float64:
- *   score  s_e = softmax over all E logits, or sigmoid of the logit
+ *   score  s_e = softmax over all E logits, or sigmoid 1 / (1 + e^-l) of the
+ *          logit (0 where e^-l overflows, l < -709.78)
  *   key    c_e = s_e + bias_e; without a bias the logit (it orders alike)
  *   groups the E experts in n_group consecutive runs of E / n_group; a run
  *          scores its largest key (MOE_GROUP_MAX) or the sum of the two

@@ -32,9 +32,12 @@ struct Plan {
 // (lat: one K step with a CU to itself, thr: its share of a busy CU, fix:
 // prologue and epilogue; the 64 x 64 tile takes two steps at a time); a
 // split adds a launch, the float32 partials' round trip at 6 TB/s (they mostly
-// stay in the caches) and their sum's chain.  The constants come from 4000
-// timed (shape, tile, split) combinations of the three products; the choice is
-// 1% slower than the best combination on average, 22% at worst.
+// stay in the caches) and their sum's chain.  The constants come from 3985
+// timed (shape, tile, split) combinations of 204 products, before whole tiles
+// stored their outputs past the caches; there the choice was 0.9% slower than
+// the best combination on average, 22% at worst.  There is no term for memory
+// traffic otherwise: where bytes decide (3 to 64 rows over a large W, many
+// rows of few columns) the estimates are too low.
 struct TileCost {
   int tm, tn, per_cu, groups;
   double lat, thr, fix;
@@ -100,9 +103,9 @@ inline Plan plan_product(int64_t M, int64_t N, int64_t K, double* us = nullptr) 
 // both where that is estimated to be faster than two (small products leave
 // CUs idle, large ones their last round), else each by itself.
 //
-// The joint launch has its own constants (75 layers, 5000 timed combinations
-// of tile and splits; the choice is 1% slower than the best one on average, 8%
-// at worst).  It takes
+// The joint launch has its own constants (75 layers, 4981 timed combinations
+// of tile and splits; where it is taken and its choice was timed, that is 1.8%
+// slower than the best one on average, 11% at worst).  It takes
 //   all work-groups resident, each on its own CU: the longer product's
 //     steps * lat + fix
 //   else the work divided by the slots and part of a work-group's time on a

@@ -33,8 +33,11 @@
 //
 // Bound by VALU work (one float64 exponential per logit with a bias or
 // group sums, the networks, one exponential and division per weight); the
-// row is read once.  16384 tokens, E 128, k 8: 7.5 us without a bias, 12.7
-// with sigmoid scores, bias and groups; one token 5.2 (one wave's chain).
+// row is read once.  16384 tokens, E 128, k 8: 8.0 us without a bias, 12.7
+// with sigmoid scores, bias and groups, about 1100 vector instructions per
+// wave that keep the VALUs busy 61% of the time (94% at 262144 tokens, 150
+// us: four waves per SIMD start and end together).  One token 5.2 us in a
+// profiler's trace (one wave's chain).
 #include <type_traits>
 
 #include "common.hpp"
