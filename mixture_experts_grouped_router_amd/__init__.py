@@ -438,9 +438,9 @@ def moe_router_bwd(logits: torch.Tensor, topk_idx: torch.Tensor,
 
 def _route_opts(score: int, n_group: int, topk_group: int, group_score: int,
                 renormalize: bool, scale: float) -> _RouteOpts:
-    _need_i32(score, n_group, topk_group, group_score)
-    return _RouteOpts(int(score), int(n_group), int(topk_group),
-                      int(group_score), int(bool(renormalize)), float(scale))
+    c = int(score), int(n_group), int(topk_group), int(group_score)
+    _need_i32(*c)
+    return _RouteOpts(*c, int(bool(renormalize)), float(scale))
 
 
 def moe_route_scored(logits: torch.Tensor, k: int,
@@ -711,7 +711,7 @@ def moe_linear_fwd(x: torch.Tensor, w: torch.Tensor,
     residual."""
     M, K = x.shape
     N = w.shape[0]
-    _need_i32(N, K, act)
+    _need_i32(N, K, int(act))
     dev = x.device
     _need(x, torch.bfloat16, (M, K), "x")
     _need_on(dev, w, torch.bfloat16, (N, K), "w")
@@ -752,7 +752,7 @@ def moe_linear_bwd(dy: torch.Tensor, x: Optional[torch.Tensor],
     if ref is None and not want_db:
         raise ValueError("no gradient asked for")
     K = ref.shape[1] if ref is not None else 8
-    _need_i32(N, K, act)
+    _need_i32(N, K, int(act))
     _need(dy, torch.bfloat16, (M, N), "dy")
     _need_on(dev, x, torch.bfloat16, (M, K), "x")
     _need_on(dev, w, torch.bfloat16, (N, K), "w")

@@ -67,3 +67,12 @@ def test_limits():
     for v in (1 << 31, -(1 << 31) - 1):
         with pytest.raises(ValueError, match="32 bits"):
             m._need_i32(3, v)
+
+
+def test_whole_floats_are_still_taken():
+    o = m._route_opts(1.0, 8.0, 4.0, 1.0, True, 2.5)
+    assert (o.score, o.n_group, o.topk_group, o.group_score) == (1, 8, 4, 1)
+    with pytest.raises(ValueError, match="device tensor"):
+        m.moe_linear_fwd(t(BF, 1, 8), t(BF, 8, 8), act=2.0)
+    with pytest.raises(ValueError, match="device tensor"):
+        m.moe_linear_bwd(t(BF, 1, 8), t(BF, 1, 8), t(BF, 8, 8), act=2.0)
