@@ -64,7 +64,10 @@ typedef enum moe_precision {
   MOE_PREC_BF16 = 0,
   MOE_PREC_MXFP8_E4M3 = 1,
   /* E4M3 with one float32 scale per tensor (forward only) */
-  MOE_PREC_FP8_TENSOR = 2
+  MOE_PREC_FP8_TENSOR = 2,
+  /* E2M1 elements, two per byte, one E8M0 scale per 32 consecutive values
+   * along K (forward only; see mxfp4_quantize) */
+  MOE_PREC_MXFP4 = 3
 } moe_precision_t;
 
 typedef enum moe_mx_axis {
@@ -84,6 +87,8 @@ typedef struct moe_ctx* moe_ctx_t;
 #define MOE_MAX_EXPERTS 1024
 #define MOE_MAX_TOPK 32
 #define MOE_MAX_ROUTE_GROUPS 64
+#define MOE_FEW_MAX_TOKENS 64        /* moe_layer_few */
+#define MOE_LAYERNORM_MAX_H 16384
 
 /* ------------------------------------------------------------------------
  * Context.  moe_ctx_create checks that `device` is a gfx950 GPU, records its
@@ -650,15 +655,16 @@ typedef struct moe_mlp_fwd_args {
   moe_precision_t precision;
   /* x_perm: bf16 [rows, H]; in MXFP8 mode either E4M3 codes [rows, H] with
    * x_perm_scale [rows, H/32], or bf16 with x_perm_scale NULL (then
-   * quantised row-wise inside the call). */
+   * quantised row-wise inside the call); MXFP4 likewise, codes [rows, H/2]. */
   const void* x_perm;
   const uint8_t* x_perm_scale;
   const void* w_gu;              /* bf16 [E, 2F, H]: gate rows 0..F-1, up F..2F-1 */
   const void* w_dn;              /* bf16 [E, H, F] */
-  /* MXFP8 only, optional: weights already quantised row-wise along K
+  /* MXFP8 and MXFP4, optional: weights already quantised row-wise along K
    * (w_gu_q [E, 2F, H] + w_gu_s [E, 2F, H/32]; w_dn_q [E, H, F] +
-   * w_dn_s [E, H, F/32]).  NULL: quantised from w_gu / w_dn inside the
-   * call (in the workspace). */
+   * w_dn_s [E, H, F/32]; MXFP4 codes [E, 2F, H/2] and [E, H, F/2], all four
+   * pointers or none).  NULL: quantised from w_gu / w_dn inside the call (in
+   * the workspace); with all of them w_gu / w_dn may be NULL. */
   const uint8_t* w_gu_q; const uint8_t* w_gu_s;
   const uint8_t* w_dn_q; const uint8_t* w_dn_s;
   const float* w_perm;           /* float32 [rows] or NULL (weight 1) */
@@ -772,6 +778,116 @@ moe_status_t moe_grouped_mlp_bwd_workspace_size(const moe_mlp_bwd_args* args,
                                                 size_t* bytes);
 moe_status_t moe_grouped_mlp_bwd(moe_ctx_t ctx, const moe_mlp_bwd_args* args,
                                  void* stream);
+
+/* ------------------------------------------------------------------------
+ * MXFP4: E2M1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign) and one E8M0
+ * scale per 32 consecutive values of a row.
+ * [PG1, section "Reducing memory and quantisation cost", one step further:
+ *  the same blocks and scales with 4-bit elements.]
+ * mxfp4_quantize: s = floor(log2 amax) - 2 clamped to [-127, 127] (-127 for
+ * an all-zero block), scale byte s + 127; element = v 2^-s rounded to the
+ * nearest E2M1 value (ties to the even code), magnitudes beyond 6 become 6,
+ * a zero keeps its sign.  Code bit 3 is the sign; element 2 i of a row is
+ * the low half of byte i.  src: bf16 [rows, cols], finite, cols % 32 == 0;
+ * codes uint8 [rows, cols / 2] (16-byte aligned); scales uint8 [rows,
+ * cols / 32].
+ * mxfp4_dequantize: dst bf16 [rows, cols] = element 2^(scale - 127), exact
+ * (magnitudes past the bf16 range become infinite).  A scale byte of 255
+ * stands for no number: its block's values are undefined.
+ * Errors: MOE_ERR_INVALID_ARG (negative size, null pointer),
+ * MOE_ERR_UNSUPPORTED (cols % 32, alignment, rows * cols >= 2^62),
+ * MOE_ERR_HIP.
+ * ---------------------------------------------------------------------- */
+moe_status_t mxfp4_quantize(moe_ctx_t ctx, const void* src, int64_t rows,
+                            int64_t cols, uint8_t* codes, uint8_t* scales,
+                            void* stream);
+moe_status_t mxfp4_dequantize(moe_ctx_t ctx, const uint8_t* codes,
+                              const uint8_t* scales, int64_t rows,
+                              int64_t cols, void* dst, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_layer_few -- the whole mixture-of-experts layer for a few tokens
+ * (generation, drafted tokens): router, top-k, the chosen experts' MLPs and
+ * the combine, in as few launches as the data dependences need, each reached
+ * expert's weights read once and nothing permuted.
+ * [PG1, section "Grouped experts instead of a Python loop": one call covers
+ *  every expert; here for token counts at which the weights' bytes, not the
+ *  products, are the work.]
+ *   y[t] = residual[t] + sum_j W_dn[e_tj] a_tj
+ *   a_tj = w_tj * silu(W_gu[e_tj] gate rows x_t) * (up rows x_t)
+ * Products and sums are float32 (a_tj is rounded once to bf16, the operand
+ * of the second product), y is rounded once.
+ * Routing: with w_r, topk_idx and topk_w are outputs: logits = x w_r^T +
+ * router_bias summed in float64 and rounded to float32, then the rule of
+ * moe_route_topk with `renormalize`.  Without w_r they are inputs (from
+ * moe_route_scored, say); an expert may be named twice by a token, an id
+ * outside [0, E) is skipped and recorded as MOE_DEVERR_EXPERT_ID.
+ * Weights: MOE_PREC_BF16 (w_gu, w_dn) or MOE_PREC_MXFP4 (w_gu_q / w_gu_s /
+ * w_dn_q / w_dn_s as mxfp4_quantize returns them, x and a stay bf16).
+ * Limits: T <= MOE_FEW_MAX_TOKENS; H and F multiples of 8 (MXFP4: of 32); an
+ * expert's W_gu in bf16 and all of a below 4 GiB.  y may be the residual.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE,
+ * MOE_ERR_HIP.
+ * ---------------------------------------------------------------------- */
+typedef struct moe_layer_few_args {
+  int32_t T, H, F, E, k;
+  moe_precision_t precision;
+  int32_t renormalize;
+  const void* x;                 /* bf16 [T, H] */
+  const void* w_r;               /* bf16 [E, H] or NULL */
+  const float* router_bias;      /* float32 [E] or NULL; only with w_r */
+  int32_t* topk_idx;             /* int32 [T, k]: out with w_r, else in */
+  float* topk_w;                 /* float32 [T, k]: likewise */
+  const void* w_gu;              /* bf16 [E, 2F, H] */
+  const void* w_dn;              /* bf16 [E, H, F] */
+  const uint8_t* w_gu_q; const uint8_t* w_gu_s;
+  const uint8_t* w_dn_q; const uint8_t* w_dn_s;
+  const void* residual;          /* bf16 [T, H] or NULL */
+  void* y;                       /* out: bf16 [T, H] */
+  void* ws;                      /* workspace, 16-byte aligned */
+  size_t ws_bytes;
+} moe_layer_few_args;
+
+moe_status_t moe_layer_few_workspace_size(const moe_layer_few_args* args,
+                                          size_t* bytes);
+moe_status_t moe_layer_few(moe_ctx_t ctx, const moe_layer_few_args* args,
+                           void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_layernorm_fwd / moe_layernorm_bwd -- layer norm over the last
+ * dimension, the norm ahead of the router and the experts.
+ *   mean = sum_h x / H, rstd = 1 / sqrt(sum_h (x - mean)^2 / H + eps),
+ *   y = (x - mean) rstd weight + bias
+ *   xh = (x - mean) rstd, g = dy weight,
+ *   dx = rstd (g - sum_h g / H - xh sum_h (g xh) / H) + dresidual,
+ *   dw = sum_t dy xh, db = sum_t dy
+ * All in float32, y and a bf16 dx rounded once.  x: bf16, or float32 with
+ * x_is_f32 (a float32 residual stream; dresidual and dx then are float32
+ * too); y and dy bf16; weight, bias, mean, rstd, dw, db float32.  weight and
+ * bias NULL: 1 and 0.  Forward: mean and rstd nullable outputs.  Backward:
+ * mean and rstd are the forward's; dresidual (the gradient that reaches x
+ * past the norm) nullable; any of dx, dw, db may be NULL; dx may be
+ * dresidual.  T = 0 gives dw = db = 0.  eps >= 0 and finite; a constant row
+ * with eps = 0 has no defined result.
+ * H <= MOE_LAYERNORM_MAX_H (any; multiples of 8 run on 16-byte accesses).
+ * The backward's workspace holds partial sums of dw and db (0 bytes if
+ * neither is asked for or T is small).
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE,
+ * MOE_ERR_HIP.
+ * ---------------------------------------------------------------------- */
+moe_status_t moe_layernorm_fwd(moe_ctx_t ctx, const void* x, int32_t x_is_f32,
+                               const float* weight, const float* bias,
+                               int64_t T, int32_t H, float eps, void* y,
+                               float* mean, float* rstd, void* stream);
+moe_status_t moe_layernorm_bwd_workspace_size(int64_t T, int32_t H,
+                                              int32_t want_sums,
+                                              size_t* bytes);
+moe_status_t moe_layernorm_bwd(moe_ctx_t ctx, const void* dy, const void* x,
+                               int32_t x_is_f32, const float* mean,
+                               const float* rstd, const float* weight,
+                               const void* dresidual, int64_t T, int32_t H,
+                               void* dx, float* dw, float* db, void* ws,
+                               size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -18,7 +18,7 @@ import torch
 
 __all__ = [
     "lib_path", "load_library", "MoEError", "PREC_BF16", "PREC_MXFP8",
-    "PREC_FP8_TENSOR", "fp8_tensor_quantize",
+    "PREC_FP8_TENSOR", "PREC_MXFP4", "fp8_tensor_quantize",
     "ROWWISE", "COLWISE", "moe_router_logits", "moe_router_bwd",
     "moe_route_topk", "moe_route_scored", "moe_route_scored_bwd",
     "moe_router_proj_bwd", "SCORE_SOFTMAX", "SCORE_SIGMOID", "GROUP_MAX",
@@ -29,7 +29,8 @@ __all__ = [
     "moe_linear_fwd", "moe_linear_bwd", "ACT_NONE", "ACT_RELU", "ACT_GELU",
     "ACT_GELU_TANH", "ACT_SILU",
     "moe_unpermute", "moe_unpermute_probs_grad", "mxfp8_quantize",
-    "mxfp8_quantize_f32",
+    "mxfp8_quantize_f32", "mxfp4_quantize", "mxfp4_dequantize",
+    "moe_layer_few", "moe_layernorm_fwd", "moe_layernorm_bwd",
     "moe_grouped_mlp_fwd", "moe_expert_loop_mlp_fwd", "moe_grouped_mlp_bwd",
     "check_device_status",
     "mx_segment_ld", "set_kernel_timing", "reset_kernel_timing",
@@ -42,6 +43,7 @@ lib_path = os.path.join(_HERE, "libmoe.so")
 PREC_BF16 = 0
 PREC_MXFP8 = 1
 PREC_FP8_TENSOR = 2
+PREC_MXFP4 = 3
 ROWWISE = 0
 COLWISE = 1
 SCORE_SOFTMAX = 0
@@ -122,6 +124,18 @@ class _LinearBwdArgs(ctypes.Structure):
     ]
 
 
+class _LayerFewArgs(ctypes.Structure):
+    _fields_ = [
+        ("T", _c_i32), ("H", _c_i32), ("F", _c_i32), ("E", _c_i32),
+        ("k", _c_i32), ("precision", ctypes.c_int), ("renormalize", _c_i32),
+        ("x", _c_p), ("w_r", _c_p), ("router_bias", _c_p),
+        ("topk_idx", _c_p), ("topk_w", _c_p), ("w_gu", _c_p), ("w_dn", _c_p),
+        ("w_gu_q", _c_p), ("w_gu_s", _c_p), ("w_dn_q", _c_p),
+        ("w_dn_s", _c_p), ("residual", _c_p), ("y", _c_p),
+        ("ws", _c_p), ("ws_bytes", _c_sz),
+    ]
+
+
 _SIGS = {
     "moe_ctx_create": [ctypes.c_int, ctypes.POINTER(_c_p)],
     "moe_ctx_destroy": [_c_p],
@@ -181,6 +195,18 @@ _SIGS = {
     "moe_grouped_mlp_bwd_workspace_size": [ctypes.POINTER(_BwdArgs),
                                            ctypes.POINTER(_c_sz)],
     "moe_grouped_mlp_bwd": [_c_p, ctypes.POINTER(_BwdArgs), _c_p],
+    "mxfp4_quantize": [_c_p, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_p],
+    "mxfp4_dequantize": [_c_p, _c_p, _c_p, _c_i64, _c_i64, _c_p, _c_p],
+    "moe_layer_few_workspace_size": [ctypes.POINTER(_LayerFewArgs),
+                                     ctypes.POINTER(_c_sz)],
+    "moe_layer_few": [_c_p, ctypes.POINTER(_LayerFewArgs), _c_p],
+    "moe_layernorm_fwd": [_c_p, _c_p, _c_i32, _c_p, _c_p, _c_i64, _c_i32,
+                          ctypes.c_float, _c_p, _c_p, _c_p, _c_p],
+    "moe_layernorm_bwd_workspace_size": [_c_i64, _c_i32, _c_i32,
+                                         ctypes.POINTER(_c_sz)],
+    "moe_layernorm_bwd": [_c_p, _c_p, _c_p, _c_i32, _c_p, _c_p, _c_p, _c_p,
+                          _c_i64, _c_i32, _c_p, _c_p, _c_p, _c_p, _c_sz,
+                          _c_p],
     "moe_hbm_stream_reference": [_c_p, _c_p, _c_i64, _c_i32, _c_p, _c_p],
     "moe_hbm_stream_mix": [_c_p, _c_p, _c_i64, _c_i32, _c_i32, _c_p, _c_p],
     "moe_ctx_set_kernel_timing": [_c_p, _c_i32],
@@ -287,6 +313,16 @@ def _need_i32(a: int, b: int, c: int = 0, d: int = 0) -> None:
         for v in (a, b, c, d):
             if not -0x80000000 <= v <= 0x7fffffff:
                 raise ValueError(f"{v} does not fit 32 bits")
+
+
+def _need_mx(q, shape, per_byte: int, dev: torch.device, name: str) -> None:
+    """(codes, E8M0 scales) of a tensor of ``shape`` in blocks of 32 along
+    its last dimension, ``per_byte`` elements to a byte; None passes."""
+    if q is None:
+        return
+    lead, n = tuple(shape[:-1]), shape[-1]
+    _need_on(dev, q[0], torch.uint8, lead + (n // per_byte,), name + " codes")
+    _need_on(dev, q[1], torch.uint8, lead + (n // 32,), name + " scales")
 
 
 def _u64(v: int, name: str) -> int:
@@ -851,8 +887,8 @@ def mxfp8_quantize_f32(src: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     return codes, scales
 
 
-def moe_grouped_mlp_fwd(x_perm: torch.Tensor, w_gu: torch.Tensor,
-                        w_dn: torch.Tensor, offsets: torch.Tensor,
+def moe_grouped_mlp_fwd(x_perm: torch.Tensor, w_gu: Optional[torch.Tensor],
+                        w_dn: Optional[torch.Tensor], offsets: torch.Tensor,
                         w_perm: Optional[torch.Tensor] = None,
                         precision: int = PREC_BF16,
                         x_perm_scale: Optional[torch.Tensor] = None,
@@ -868,20 +904,45 @@ def moe_grouped_mlp_fwd(x_perm: torch.Tensor, w_gu: torch.Tensor,
     "a_s", A's MXFP8 codes and row-major scales, when save_a_codes=True in
     MXFP8 mode).  w_gu_q / w_dn_q (optional, both or neither): the weights
     quantised beforehand, (codes, E8M0 scales) from mxfp8_quantize ROWWISE
-    in MXFP8 mode, (codes, float32 scale per expert) from
-    fp8_tensor_quantize(w, E) in tensor-scaled FP8 mode."""
-    E, F2, H = w_gu.shape
+    in MXFP8 mode and from mxfp4_quantize in MXFP4 mode, (codes, float32
+    scale per expert) from fp8_tensor_quantize(w, E) in tensor-scaled FP8
+    mode; w_gu and w_dn may then be None."""
+    mx4 = precision == PREC_MXFP4
+    if w_gu is None or w_dn is None:
+        if precision == PREC_BF16 or w_gu_q is None or w_dn_q is None:
+            raise ValueError("w_gu and w_dn are needed without quantised "
+                             "weights")
+        E, F2, H = w_gu_q[0].shape
+        H = 2 * H if mx4 else H
+    else:
+        E, F2, H = w_gu.shape
     F = F2 // 2
     rows = x_perm.shape[0]
     dev = x_perm.device
-    _need(w_gu, torch.bfloat16, (E, 2 * F, H), "w_gu")
-    _need(w_dn, torch.bfloat16, (E, H, F), "w_dn")
+    if w_gu is not None:
+        _need(w_gu, torch.bfloat16, (E, 2 * F, H), "w_gu")
+    if w_dn is not None:
+        _need(w_dn, torch.bfloat16, (E, H, F), "w_dn")
     _need(offsets, torch.int32, (E + 1,), "offsets")
     if precision == PREC_BF16 or x_perm_scale is None:
         _need(x_perm, torch.bfloat16, (rows, H), "x_perm")
     else:
-        _need(x_perm, torch.uint8, (rows, H), "x_perm")
+        _need(x_perm, torch.uint8, (rows, H // 2 if mx4 else H), "x_perm")
         _need(x_perm_scale, torch.uint8, (rows, H // 32), "x_perm_scale")
+    if precision == PREC_MXFP8 and w_gu is None:
+        _need_mx(w_gu_q, (E, 2 * F, H), 1, dev, "w_gu_q")
+        _need_mx(w_dn_q, (E, H, F), 1, dev, "w_dn_q")
+    if mx4:
+        _need_i32(H, F, E)
+        for t, name in ((offsets, "offsets"), (w_perm, "w_perm"),
+                        (w_gu, "w_gu"), (w_dn, "w_dn"),
+                        (x_perm_scale, "x_perm_scale"), (out, "out")):
+            if t is not None and t.device != dev:
+                raise ValueError(f"{name}: on {t.device}, expected {dev}")
+        if (w_gu_q is None) != (w_dn_q is None):
+            raise ValueError("w_gu_q and w_dn_q go together")
+        _need_mx(w_gu_q, (E, 2 * F, H), 2, dev, "w_gu_q")
+        _need_mx(w_dn_q, (E, H, F), 2, dev, "w_dn_q")
     if w_perm is not None:
         _need(w_perm, torch.float32, (rows,), "w_perm")
     z = out if out is not None else torch.empty((rows, H), dtype=torch.bfloat16,
@@ -1054,4 +1115,200 @@ def moe_grouped_mlp_bwd(dz_perm: torch.Tensor, x_perm: torch.Tensor,
     res = {"dx_perm": dx, "dw_gu": dw_gu, "dw_dn": dw_dn}
     if dw_perm is not None:
         res["dw_perm"] = dw_perm
+    return res
+
+
+def mxfp4_quantize(src: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    """MXFP4 of a bf16 tensor [.., cols] along its rows: (codes uint8 [..,
+    cols / 2], the even element of a pair in the low half, E8M0 scales uint8
+    [.., cols / 32])."""
+    if src.dim() < 1:
+        raise ValueError("src must have a dimension")
+    lead, cols = tuple(src.shape[:-1]), src.shape[-1]
+    _need(src, torch.bfloat16, lead + (cols,), "src")
+    if cols % 32:
+        raise ValueError("the last dimension must be a multiple of 32")
+    dev = src.device
+    codes = torch.empty(lead + (cols // 2,), dtype=torch.uint8, device=dev)
+    scales = torch.empty(lead + (cols // 32,), dtype=torch.uint8, device=dev)
+    rows = src.numel() // cols if cols else 0
+    _check(load_library().mxfp4_quantize(_context(dev), _ptr(src), rows, cols,
+                                         _ptr(codes), _ptr(scales),
+                                         _stream()))
+    return codes, scales
+
+
+def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The bf16 values [.., cols] of mxfp4_quantize's (codes, scales)."""
+    if codes.dim() < 1:
+        raise ValueError("codes must have a dimension")
+    lead, cols = tuple(codes.shape[:-1]), 2 * codes.shape[-1]
+    if cols % 32:
+        raise ValueError("rows must hold whole blocks of 16 code bytes")
+    dev = codes.device
+    _need(codes, torch.uint8, lead + (cols // 2,), "codes")
+    _need_on(dev, scales, torch.uint8, lead + (cols // 32,), "scales")
+    dst = _out_or_new(out, lead + (cols,), torch.bfloat16, dev)
+    rows = dst.numel() // cols if cols else 0
+    _check(load_library().mxfp4_dequantize(_context(dev), _ptr(codes),
+                                           _ptr(scales), rows, cols,
+                                           _ptr(dst), _stream()))
+    return dst
+
+
+def moe_layer_few(x: torch.Tensor, w_gu: Optional[torch.Tensor] = None,
+                  w_dn: Optional[torch.Tensor] = None,
+                  topk_idx: Optional[torch.Tensor] = None,
+                  topk_w: Optional[torch.Tensor] = None,
+                  w_r: Optional[torch.Tensor] = None, k: int = 0,
+                  router_bias: Optional[torch.Tensor] = None,
+                  renormalize: bool = True, precision: int = PREC_BF16,
+                  w_gu_q: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                  w_dn_q: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                  residual: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None,
+                  ws: Optional[torch.Tensor] = None
+                  ) -> Dict[str, torch.Tensor]:
+    """The whole layer for up to 64 tokens: x bf16 [T, H] -> {"y" bf16
+    [T, H], "topk_idx" int32 [T, k], "topk_w" float32 [T, k]}.  Routing: the
+    router's w_r bf16 [E, H] with k, or topk_idx and topk_w from another
+    router.  Weights: w_gu bf16 [E, 2F, H] and w_dn bf16 [E, H, F], or, with
+    PREC_MXFP4, w_gu_q and w_dn_q as mxfp4_quantize returns them.  out may be
+    the residual."""
+    T, H = x.shape
+    dev = x.device
+    mx4 = precision == PREC_MXFP4
+    ref = w_gu_q[0] if mx4 and w_gu_q is not None else w_gu
+    if ref is None or (w_dn_q if mx4 else w_dn) is None:
+        raise ValueError("PREC_MXFP4 needs w_gu_q and w_dn_q, PREC_BF16 "
+                         "w_gu and w_dn")
+    E, F = ref.shape[0], ref.shape[1] // 2
+    _need(x, torch.bfloat16, (T, H), "x")
+    if w_r is not None:
+        if topk_idx is not None or topk_w is not None:
+            raise ValueError("either w_r or topk_idx and topk_w")
+        if k < 1:
+            raise ValueError("k must be positive")
+        _need_on(dev, w_r, torch.bfloat16, (E, H), "w_r")
+        _need_on(dev, router_bias, torch.float32, (E,), "router_bias")
+        _need_i32(k, T)
+        topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+        topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+    else:
+        if topk_idx is None or topk_w is None:
+            raise ValueError("either w_r or topk_idx and topk_w")
+        if router_bias is not None:
+            raise ValueError("router_bias needs w_r")
+        if k not in (0, topk_idx.shape[1]):
+            raise ValueError("k differs from topk_idx")
+        k = topk_idx.shape[1]
+        _need_on(dev, topk_idx, torch.int32, (T, k), "topk_idx")
+        _need_on(dev, topk_w, torch.float32, (T, k), "topk_w")
+    _need_i32(T, H, F, E)
+    _need_i32(k, int(precision))
+    a = _LayerFewArgs()
+    a.T, a.H, a.F, a.E, a.k = T, H, F, E, k
+    a.precision, a.renormalize = int(precision), int(bool(renormalize))
+    if mx4:
+        _need_mx(w_gu_q, (E, 2 * F, H), 2, dev, "w_gu_q")
+        _need_mx(w_dn_q, (E, H, F), 2, dev, "w_dn_q")
+        a.w_gu_q, a.w_gu_s = _ptr(w_gu_q[0]), _ptr(w_gu_q[1])
+        a.w_dn_q, a.w_dn_s = _ptr(w_dn_q[0]), _ptr(w_dn_q[1])
+    else:
+        if w_gu_q is not None or w_dn_q is not None:
+            raise ValueError("quantised weights need PREC_MXFP4")
+        _need_on(dev, w_gu, torch.bfloat16, (E, 2 * F, H), "w_gu")
+        _need_on(dev, w_dn, torch.bfloat16, (E, H, F), "w_dn")
+        a.w_gu, a.w_dn = _ptr(w_gu), _ptr(w_dn)
+    _need_on(dev, residual, torch.bfloat16, (T, H), "residual")
+    y = _out_or_new(out, (T, H), torch.bfloat16, dev)
+    a.x, a.w_r, a.router_bias = _ptr(x), _ptr(w_r), _ptr(router_bias)
+    a.topk_idx, a.topk_w = _ptr(topk_idx), _ptr(topk_w)
+    a.residual, a.y = _ptr(residual), _ptr(y)
+    lib = load_library()
+    n = _c_sz(0)
+    _check(lib.moe_layer_few_workspace_size(ctypes.byref(a), ctypes.byref(n)))
+    ws = _workspace(ws, int(n.value), dev)
+    a.ws, a.ws_bytes = _ptr(ws), 0 if ws is None else ws.numel()
+    _check(lib.moe_layer_few(_context(dev), ctypes.byref(a), _stream()))
+    return {"y": y, "topk_idx": topk_idx, "topk_w": topk_w}
+
+
+def _norm_input(x: torch.Tensor) -> Tuple[int, int]:
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"x: dtype {x.dtype}, expected bfloat16 or float32")
+    T, H = x.shape
+    _need_i32(H, 0)
+    _need(x, x.dtype, (T, H), "x")
+    return T, H
+
+
+def moe_layernorm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                      bias: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                      save: bool = False, out: Optional[torch.Tensor] = None
+                      ) -> Dict[str, torch.Tensor]:
+    """Layer norm of the rows of x (bf16 or float32 [T, H]) with float32
+    weight and bias [H]: {"y": bf16 [T, H]} (+ "mean", "rstd" float32 [T]
+    when save=True)."""
+    T, H = _norm_input(x)
+    dev = x.device
+    _need_on(dev, weight, torch.float32, (H,), "weight")
+    _need_on(dev, bias, torch.float32, (H,), "bias")
+    y = _out_or_new(out, (T, H), torch.bfloat16, dev)
+    mean = rstd = None
+    if save:
+        mean = torch.empty(T, dtype=torch.float32, device=dev)
+        rstd = torch.empty(T, dtype=torch.float32, device=dev)
+    _check(load_library().moe_layernorm_fwd(
+        _context(dev), _ptr(x), int(x.dtype == torch.float32), _ptr(weight),
+        _ptr(bias), T, H, float(eps), _ptr(y), _ptr(mean), _ptr(rstd),
+        _stream()))
+    return {"y": y, "mean": mean, "rstd": rstd} if save else {"y": y}
+
+
+def moe_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
+                      rstd: torch.Tensor,
+                      weight: Optional[torch.Tensor] = None,
+                      dresidual: Optional[torch.Tensor] = None,
+                      want_dx: bool = True, want_dw: bool = True,
+                      want_db: bool = True,
+                      out: Optional[torch.Tensor] = None,
+                      ws: Optional[torch.Tensor] = None
+                      ) -> Dict[str, torch.Tensor]:
+    """Gradients of moe_layernorm_fwd with its saved mean and rstd: {"dx" (x's
+    type) [T, H], "dw", "db" float32 [H]} as asked for.  dresidual (x's
+    type): the gradient that reaches x past the norm, added to dx; out (of
+    dx) may be dresidual."""
+    T, H = _norm_input(x)
+    dev = x.device
+    _need_on(dev, dy, torch.bfloat16, (T, H), "dy")
+    _need_on(dev, mean, torch.float32, (T,), "mean")
+    _need_on(dev, rstd, torch.float32, (T,), "rstd")
+    _need_on(dev, weight, torch.float32, (H,), "weight")
+    _need_on(dev, dresidual, x.dtype, (T, H), "dresidual")
+    if not (want_dx or want_dw or want_db):
+        raise ValueError("no gradient asked for")
+    dx = _out_or_new(out, (T, H), x.dtype, dev) if want_dx else None
+    dw = torch.empty(H, dtype=torch.float32, device=dev) if want_dw else None
+    db = torch.empty(H, dtype=torch.float32, device=dev) if want_db else None
+    lib = load_library()
+    n = _c_sz(0)
+    _check(lib.moe_layernorm_bwd_workspace_size(
+        T, H, int(want_dw or want_db), ctypes.byref(n)))
+    ws = _workspace(ws, int(n.value), dev)
+    _check(lib.moe_layernorm_bwd(
+        _context(dev), _ptr(dy), _ptr(x), int(x.dtype == torch.float32),
+        _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dresidual), T, H, _ptr(dx),
+        _ptr(dw), _ptr(db), _ptr(ws), 0 if ws is None else ws.numel(),
+        _stream()))
+    res = {}
+    if want_dx:
+        res["dx"] = dx
+    if want_dw:
+        res["dw"] = dw
+    if want_db:
+        res["db"] = db
     return res

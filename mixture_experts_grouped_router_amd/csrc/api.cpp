@@ -776,9 +776,10 @@ moe_status_t check_mlp_dims(int32_t E, int32_t H, int32_t F, int64_t rows,
   MOE_REQUIRE(E <= MOE_MAX_EXPERTS, MOE_ERR_UNSUPPORTED, "E > %d",
               MOE_MAX_EXPERTS);
   MOE_REQUIRE(prec == MOE_PREC_BF16 || prec == MOE_PREC_MXFP8_E4M3 ||
-                  prec == MOE_PREC_FP8_TENSOR,
+                  prec == MOE_PREC_FP8_TENSOR || prec == MOE_PREC_MXFP4,
               MOE_ERR_INVALID_ARG, "bad precision");
-  // K steps of 64 (bf16) / 128 (8-bit) without masking; N tails are masked
+  // K steps of 64 (bf16) / 128 (8-bit) without masking, of 256 (4-bit) whose
+  // last may be half; N tails are masked
   const int kq = prec == MOE_PREC_BF16 ? 64 : 128;
   MOE_REQUIRE(H % kq == 0 && F % kq == 0, MOE_ERR_UNSUPPORTED,
               "H and F must be multiples of %d", kq);
@@ -807,6 +808,10 @@ moe_status_t moe_grouped_mlp_fwd_workspace_size(const moe_mlp_fwd_args* a,
     *bytes = moe::mlp_fwd_fp8t_ws_bytes(a->E, a->H, a->F, a->rows,
                                         a->a_save == nullptr,
                                         a->w_gu_q == nullptr);
+  else if (a->precision == MOE_PREC_MXFP4)
+    *bytes = moe::mlp_fwd_mx4_ws_bytes(a->E, a->H, a->F, a->rows,
+                                       a->x_perm_scale == nullptr,
+                                       a->w_gu_q == nullptr);
   else
     *bytes = moe::mlp_fwd_mx_ws_bytes(
         a->E, a->H, a->F, a->rows, a->x_perm_scale == nullptr,
@@ -841,7 +846,17 @@ moe_status_t moe_grouped_mlp_fwd(moe_ctx_t ctx, const moe_mlp_fwd_args* a,
     MOE_REQUIRE(!a->w_gu_ts && !a->w_dn_ts, MOE_ERR_INVALID_ARG,
                 "w_gu_ts / w_dn_ts are FP8 tensor-scaled inputs");
   }
-  const bool preq = (mx || f8t) && a->w_gu_q != nullptr &&
+  const bool mx4 = a->precision == MOE_PREC_MXFP4;
+  if (mx4) {
+    const bool any = a->w_gu_q || a->w_gu_s || a->w_dn_q || a->w_dn_s;
+    MOE_REQUIRE(!any || (a->w_gu_q && a->w_gu_s && a->w_dn_q && a->w_dn_s),
+                MOE_ERR_INVALID_ARG,
+                "pre-quantised MXFP4 weights: all of w_gu_q, w_gu_s, w_dn_q, "
+                "w_dn_s or none");
+    MOE_REQUIRE(aligned16(a->h1_save) && aligned16(a->a_save),
+                MOE_ERR_UNSUPPORTED, "saves must be 16-byte aligned");
+  }
+  const bool preq = (mx || f8t || mx4) && a->w_gu_q != nullptr &&
                     a->w_dn_q != nullptr;
   if (!preq)
     MOE_REQUIRE(a->w_gu && a->w_dn, MOE_ERR_INVALID_ARG, "null weights");
@@ -851,9 +866,9 @@ moe_status_t moe_grouped_mlp_fwd(moe_ctx_t ctx, const moe_mlp_fwd_args* a,
   auto al4 = [](const void* q) {
     return (reinterpret_cast<uintptr_t>(q) & 3u) == 0;
   };
-  if (mx)
+  if (mx || mx4)
     MOE_REQUIRE(al4(a->x_perm_scale) && al4(a->w_gu_s) && al4(a->w_dn_s),
-                MOE_ERR_UNSUPPORTED, "MXFP8 scale arrays must be 4-byte aligned");
+                MOE_ERR_UNSUPPORTED, "MX scale arrays must be 4-byte aligned");
   MOE_REQUIRE(mx || (!a->a_q_save && !a->a_s_save), MOE_ERR_INVALID_ARG,
               "a_q_save / a_s_save are MXFP8 outputs");
   MOE_REQUIRE(aligned16(a->a_q_save), MOE_ERR_UNSUPPORTED,
@@ -877,6 +892,14 @@ moe_status_t moe_grouped_mlp_fwd(moe_ctx_t ctx, const moe_mlp_fwd_args* a,
                                  a->z_perm, a->h1_save, a->a_save, a->ws,
                                  ctx->cu_count, ctx->status,
                                  as_stream(stream));
+  } else if (mx4) {
+    const bool xq = a->x_perm_scale != nullptr;
+    e = moe::launch_mlp_fwd_mx4(
+        a->E, a->H, a->F, a->rows, xq ? nullptr : a->x_perm,
+        xq ? static_cast<const uint8_t*>(a->x_perm) : nullptr,
+        a->x_perm_scale, a->w_gu, a->w_dn, a->w_gu_q, a->w_gu_s, a->w_dn_q,
+        a->w_dn_s, a->w_perm, a->offsets, a->z_perm, a->h1_save, a->a_save,
+        a->ws, ctx->cu_count, ctx->status, as_stream(stream));
   } else if (!mx) {
     e = moe::launch_mlp_fwd_bf16(a->E, a->H, a->F, a->rows, a->x_perm, a->w_gu,
                                  a->w_dn, a->w_perm, a->offsets, a->z_perm,
@@ -955,6 +978,8 @@ moe_status_t moe_grouped_mlp_bwd_workspace_size(const moe_mlp_bwd_args* a,
   if (s != MOE_OK) return s;
   MOE_REQUIRE(a->precision != MOE_PREC_FP8_TENSOR, MOE_ERR_UNSUPPORTED,
               "the FP8 tensor-scaled mode is forward only");
+  MOE_REQUIRE(a->precision != MOE_PREC_MXFP4, MOE_ERR_UNSUPPORTED,
+              "the MXFP4 mode is forward only");
   if (a->precision == MOE_PREC_MXFP8_E4M3) {
     // token-direction operands [max(H, 2F)][rows + 128 E (+128)] are
     // addressed with 32-bit byte offsets
@@ -982,6 +1007,8 @@ moe_status_t moe_grouped_mlp_bwd(moe_ctx_t ctx, const moe_mlp_bwd_args* a,
   if (s != MOE_OK) return s;
   MOE_REQUIRE(a->precision != MOE_PREC_FP8_TENSOR, MOE_ERR_UNSUPPORTED,
               "the FP8 tensor-scaled mode is forward only");
+  MOE_REQUIRE(a->precision != MOE_PREC_MXFP4, MOE_ERR_UNSUPPORTED,
+              "the MXFP4 mode is forward only");
   MOE_REQUIRE(a->offsets && a->w_gu && a->w_dn && a->dw_gu && a->dw_dn,
               MOE_ERR_INVALID_ARG, "null offsets / weights / weight grads");
   if (a->rows > 0)
@@ -1118,6 +1145,209 @@ moe_status_t moe_linear_bwd(moe_ctx_t ctx, const moe_linear_bwd_args* a,
                              a->w, a->z, a->dx, a->dw, a->db, a->ws,
                              as_stream(stream)),
       "linear_bwd");
+}
+
+namespace {
+
+moe_status_t check_mx4(const void* bf16, const uint8_t* codes,
+                       const uint8_t* scales, int64_t rows, int64_t cols) {
+  MOE_REQUIRE(rows >= 0 && cols >= 0, MOE_ERR_INVALID_ARG, "negative size");
+  MOE_REQUIRE(cols % 32 == 0, MOE_ERR_UNSUPPORTED, "cols %% 32 != 0");
+  MOE_REQUIRE(cols == 0 || rows < ((int64_t)1 << 62) / cols,
+              MOE_ERR_UNSUPPORTED, "tensor too large");
+  MOE_REQUIRE(rows * cols == 0 || (bf16 && codes && scales),
+              MOE_ERR_INVALID_ARG, "null pointer");
+  MOE_REQUIRE(aligned16(bf16) && aligned16(codes), MOE_ERR_UNSUPPORTED,
+              "values and codes must be 16-byte aligned");
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status_t mxfp4_quantize(moe_ctx_t ctx, const void* src, int64_t rows,
+                            int64_t cols, uint8_t* codes, uint8_t* scales,
+                            void* stream) {
+  moe_status_t s = check_mx4(src, codes, scales, rows, cols);
+  if (s != MOE_OK) return s;
+  s = check_ctx(ctx);
+  if (s != MOE_OK) return s;
+  TimerGuard tg(ctx);
+  return hip_status(moe::launch_mx4_quant_rows(src, rows, cols, codes, scales,
+                                               as_stream(stream)),
+                    "mxfp4 rows");
+}
+
+moe_status_t mxfp4_dequantize(moe_ctx_t ctx, const uint8_t* codes,
+                              const uint8_t* scales, int64_t rows,
+                              int64_t cols, void* dst, void* stream) {
+  moe_status_t s = check_mx4(dst, codes, scales, rows, cols);
+  if (s != MOE_OK) return s;
+  s = check_ctx(ctx);
+  if (s != MOE_OK) return s;
+  TimerGuard tg(ctx);
+  return hip_status(moe::launch_mx4_dequant(codes, scales, rows * cols, dst,
+                                            as_stream(stream)),
+                    "mxfp4 dequantize");
+}
+
+moe_status_t moe_layer_few_workspace_size(const moe_layer_few_args* a,
+                                          size_t* bytes) {
+  static_assert(moe::kFewMaxTokens == MOE_FEW_MAX_TOKENS, "token limit");
+  MOE_REQUIRE(a && bytes, MOE_ERR_INVALID_ARG, "null pointer");
+  MOE_REQUIRE(a->T >= 0 && a->H >= 1 && a->F >= 1 && a->E >= 1 && a->k >= 1 &&
+                  a->k <= a->E,
+              MOE_ERR_INVALID_ARG, "bad sizes (T=%d H=%d F=%d E=%d k=%d)",
+              a->T, a->H, a->F, a->E, a->k);
+  MOE_REQUIRE(a->precision == MOE_PREC_BF16 ||
+                  a->precision == MOE_PREC_MXFP8_E4M3 ||
+                  a->precision == MOE_PREC_FP8_TENSOR ||
+                  a->precision == MOE_PREC_MXFP4,
+              MOE_ERR_INVALID_ARG, "bad precision");
+  MOE_REQUIRE(a->precision == MOE_PREC_BF16 || a->precision == MOE_PREC_MXFP4,
+              MOE_ERR_UNSUPPORTED, "weights in bf16 or MXFP4 only");
+  MOE_REQUIRE(a->T <= MOE_FEW_MAX_TOKENS, MOE_ERR_UNSUPPORTED,
+              "T <= %d required", MOE_FEW_MAX_TOKENS);
+  MOE_REQUIRE(a->E <= MOE_MAX_EXPERTS && a->k <= MOE_MAX_TOPK,
+              MOE_ERR_UNSUPPORTED, "E <= %d and k <= %d required",
+              MOE_MAX_EXPERTS, MOE_MAX_TOPK);
+  const int q = a->precision == MOE_PREC_BF16 ? 8 : 32;
+  MOE_REQUIRE(a->H % q == 0 && a->F % q == 0, MOE_ERR_UNSUPPORTED,
+              "H and F must be multiples of %d", q);
+  // operands are addressed with 32-bit byte offsets; a launch holds fewer
+  // than 2^32 threads (32 per FFN column and expert)
+  const int64_t lim = ((int64_t)1 << 32) - 256;
+  MOE_REQUIRE((int64_t)a->F * 4 <= lim / a->H &&
+                  (int64_t)MOE_FEW_MAX_TOKENS * a->H * 2 <= lim &&
+                  (int64_t)a->T * a->k * a->F * 2 <= lim &&
+                  (int64_t)a->F + 16 <= lim / 32 / a->E,
+              MOE_ERR_UNSUPPORTED, "tensor too large");
+  *bytes = moe::layer_few_ws_bytes(a->T, a->F, a->E, a->k, a->w_r != nullptr);
+  return ok();
+}
+
+moe_status_t moe_layer_few(moe_ctx_t ctx, const moe_layer_few_args* a,
+                           void* stream) {
+  size_t need = 0;
+  moe_status_t s = moe_layer_few_workspace_size(a, &need);
+  if (s != MOE_OK) return s;
+  const bool mx4 = a->precision == MOE_PREC_MXFP4;
+  MOE_REQUIRE(a->w_r || !a->router_bias, MOE_ERR_INVALID_ARG,
+              "router_bias needs w_r");
+  MOE_REQUIRE(mx4 || (!a->w_gu_q && !a->w_gu_s && !a->w_dn_q && !a->w_dn_s),
+              MOE_ERR_INVALID_ARG, "quantised weights in bf16 mode");
+  if (a->T > 0) {
+    MOE_REQUIRE(a->x && a->topk_idx && a->topk_w && a->y, MOE_ERR_INVALID_ARG,
+                "null tensor pointer");
+    MOE_REQUIRE(mx4 ? a->w_gu_q && a->w_gu_s && a->w_dn_q && a->w_dn_s
+                    : a->w_gu && a->w_dn,
+                MOE_ERR_INVALID_ARG, "null weights");
+    MOE_REQUIRE(a->ws && a->ws_bytes >= need, MOE_ERR_WORKSPACE,
+                "layer_few workspace needs %zu bytes", need);
+  }
+  MOE_REQUIRE(aligned16(a->x) && aligned16(a->w_r) && aligned16(a->w_gu) &&
+                  aligned16(a->w_dn) && aligned16(a->w_gu_q) &&
+                  aligned16(a->w_dn_q) && aligned16(a->residual) &&
+                  aligned16(a->y) && aligned16(a->ws),
+              MOE_ERR_UNSUPPORTED, "operands must be 16-byte aligned");
+  s = check_ctx(ctx);
+  if (s != MOE_OK) return s;
+  TimerGuard tg(ctx);
+  if (a->T == 0) return ok();
+  moe::LayerFew f{};
+  f.T = a->T;
+  f.H = a->H;
+  f.F = a->F;
+  f.E = a->E;
+  f.k = a->k;
+  f.x = a->x;
+  f.w_r = a->w_r;
+  f.bias = a->router_bias;
+  f.renorm = a->renormalize != 0;
+  f.topk_idx = a->topk_idx;
+  f.topk_w = a->topk_w;
+  f.w_gu = mx4 ? a->w_gu_q : a->w_gu;
+  f.s_gu = mx4 ? a->w_gu_s : nullptr;
+  f.w_dn = mx4 ? a->w_dn_q : a->w_dn;
+  f.s_dn = mx4 ? a->w_dn_s : nullptr;
+  f.residual = a->residual;
+  f.y = a->y;
+  f.ws = a->ws;
+  f.status = ctx->status;
+  return hip_status(moe::launch_layer_few(f, as_stream(stream)),
+                    "layer_few launch");
+}
+
+namespace {
+
+moe_status_t check_layernorm(int64_t T, int32_t H) {
+  MOE_REQUIRE(T >= 0 && H >= 1, MOE_ERR_INVALID_ARG, "bad sizes");
+  MOE_REQUIRE(H <= MOE_LAYERNORM_MAX_H, MOE_ERR_UNSUPPORTED,
+              "H <= %d required", MOE_LAYERNORM_MAX_H);
+  MOE_REQUIRE(T < ((int64_t)1 << 58) / H, MOE_ERR_UNSUPPORTED, "T too large");
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status_t moe_layernorm_fwd(moe_ctx_t ctx, const void* x, int32_t x_is_f32,
+                               const float* weight, const float* bias,
+                               int64_t T, int32_t H, float eps, void* y,
+                               float* mean, float* rstd, void* stream) {
+  moe_status_t s = check_layernorm(T, H);
+  if (s != MOE_OK) return s;
+  MOE_REQUIRE(std::isfinite(eps) && eps >= 0.0f, MOE_ERR_INVALID_ARG,
+              "eps must be finite and not negative");
+  MOE_REQUIRE(T == 0 || (x && y), MOE_ERR_INVALID_ARG, "null pointer");
+  MOE_REQUIRE(aligned16(x) && aligned16(weight) && aligned16(bias) &&
+                  aligned16(y),
+              MOE_ERR_UNSUPPORTED, "tensors must be 16-byte aligned");
+  s = check_ctx(ctx);
+  if (s != MOE_OK) return s;
+  TimerGuard tg(ctx);
+  if (T == 0) return ok();
+  return hip_status(moe::launch_layernorm_fwd(x, x_is_f32 != 0, weight, bias,
+                                              y, mean, rstd, T, H, eps,
+                                              as_stream(stream)),
+                    "layernorm_fwd launch");
+}
+
+moe_status_t moe_layernorm_bwd_workspace_size(int64_t T, int32_t H,
+                                              int32_t want_sums,
+                                              size_t* bytes) {
+  MOE_REQUIRE(bytes != nullptr, MOE_ERR_INVALID_ARG, "null output pointer");
+  const moe_status_t s = check_layernorm(T, H);
+  if (s != MOE_OK) return s;
+  *bytes = moe::layernorm_bwd_ws_bytes(T, H, want_sums != 0);
+  return ok();
+}
+
+moe_status_t moe_layernorm_bwd(moe_ctx_t ctx, const void* dy, const void* x,
+                               int32_t x_is_f32, const float* mean,
+                               const float* rstd, const float* weight,
+                               const void* dresidual, int64_t T, int32_t H,
+                               void* dx, float* dw, float* db, void* ws,
+                               size_t ws_bytes, void* stream) {
+  moe_status_t s = check_layernorm(T, H);
+  if (s != MOE_OK) return s;
+  MOE_REQUIRE(T == 0 || (dy && x && mean && rstd), MOE_ERR_INVALID_ARG,
+              "null pointer");
+  MOE_REQUIRE(aligned16(dy) && aligned16(x) && aligned16(weight) &&
+                  aligned16(dresidual) && aligned16(dx) && aligned16(dw) &&
+                  aligned16(db),
+              MOE_ERR_UNSUPPORTED, "tensors must be 16-byte aligned");
+  const size_t need = moe::layernorm_bwd_ws_bytes(T, H, dw || db);
+  MOE_REQUIRE(need == 0 || (ws && ws_bytes >= need), MOE_ERR_WORKSPACE,
+              "layernorm_bwd workspace needs %zu bytes", need);
+  MOE_REQUIRE(need == 0 || aligned16(ws), MOE_ERR_UNSUPPORTED,
+              "the workspace must be 16-byte aligned");
+  s = check_ctx(ctx);
+  if (s != MOE_OK) return s;
+  TimerGuard tg(ctx);
+  return hip_status(moe::launch_layernorm_bwd(dy, x, x_is_f32 != 0, mean,
+                                              rstd, weight, dresidual, dx, dw,
+                                              db, T, H, ws,
+                                              as_stream(stream)),
+                    "layernorm_bwd launch");
 }
 
 }  // extern "C"

@@ -59,7 +59,8 @@ enum Epi {
   EPI_STORE = 0,       // bf16 C
   EPI_SWIGLU = 1,      // bf16 A = w * silu(g) * u (+ g, u save)
   EPI_SWIGLU_BWD = 2,  // dgrad of the down projection + SwiGLU backward
-  EPI_SWIGLU_MX = 3    // as EPI_SWIGLU, A quantised to MXFP8 along f
+  EPI_SWIGLU_MX = 3,   // as EPI_SWIGLU, A quantised to MXFP8 along f
+  EPI_SWIGLU_MX4 = 4   // as EPI_SWIGLU, A quantised to MXFP4 along f
 };
 // P_FP8: MXFP8 (E8M0 scale per 32 along K, scaled MFMA); P_FP8T: E4M3
 // with one float32 scale per tensor (unit MFMA scales, the tensor scales
@@ -917,7 +918,8 @@ __device__ __forceinline__ bool split_reduce(const Params& p,
 template <int EPI>
 struct Shape8 {
   static constexpr int MI =                             // 32-row A blocks
-      EPI == EPI_SWIGLU || EPI == EPI_SWIGLU_MX ? 2 : 4;
+      EPI == EPI_SWIGLU || EPI == EPI_SWIGLU_MX || EPI == EPI_SWIGLU_MX4 ? 2
+                                                                         : 4;
   static constexpr int NJ = 8 / MI;                     // 32-row B blocks
   static constexpr int WN = 8 / (8 / MI);               // waves along N
 };

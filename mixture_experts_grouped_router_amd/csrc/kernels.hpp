@@ -219,4 +219,66 @@ hipError_t launch_mlp_bwd_mx(int E, int H, int F, int64_t rows,
                              const uint8_t* w_dn_st, void* ws,
                              int32_t* status, hipStream_t stream);
 
+// layer norm (layernorm.hip); f32: x, dresidual and dx are float32, else bf16
+hipError_t launch_layernorm_fwd(const void* x, bool f32, const float* w,
+                                const float* b, void* y, float* mean,
+                                float* rstd, int64_t T, int H, float eps,
+                                hipStream_t stream);
+size_t layernorm_bwd_ws_bytes(int64_t T, int H, bool want_sums);
+hipError_t launch_layernorm_bwd(const void* dy, const void* x, bool f32,
+                                const float* mean, const float* rstd,
+                                const float* w, const void* dres, void* dx,
+                                float* dw, float* db, int64_t T, int H,
+                                void* ws, hipStream_t stream);
+
+// MXFP4 (mxfp4_quant.hip).  tiled: scales in the layout of the 4-bit GEMM
+// (mx4_tile_off), else row-major [rows][cols / 32]; cols % 32 == 0 (tiled and
+// retile: % 128)
+hipError_t launch_mx4_quant_rows(const void* src, int64_t rows, int64_t cols,
+                                 uint8_t* codes, uint8_t* scales,
+                                 hipStream_t stream, bool tiled = false);
+hipError_t launch_mx4_dequant(const uint8_t* codes, const uint8_t* scales,
+                              int64_t values, void* dst, hipStream_t stream);
+hipError_t launch_mx4_scales_retile(const uint8_t* src, int64_t rows,
+                                    int64_t k, uint8_t* dst,
+                                    hipStream_t stream);
+
+// MXFP4 grouped MLP forward (gemm_mxfp4.hip); quant_x / quant_w: the
+// activations / weights are quantised inside the call
+size_t mlp_fwd_mx4_ws_bytes(int E, int H, int F, int64_t rows, bool quant_x,
+                            bool quant_w);
+hipError_t launch_mlp_fwd_mx4(int E, int H, int F, int64_t rows,
+                              const void* x_perm_bf16, const uint8_t* xq,
+                              const uint8_t* xs, const void* w_gu,
+                              const void* w_dn, const uint8_t* w_gu_q,
+                              const uint8_t* w_gu_s, const uint8_t* w_dn_q,
+                              const uint8_t* w_dn_s, const float* w_perm,
+                              const int32_t* offsets, void* z_perm,
+                              void* h1_save, void* a_save, void* ws,
+                              int cu_count, int32_t* status,
+                              hipStream_t stream);
+
+// the whole layer for a few tokens (layer_few.hip).  w_r null: topk_idx and
+// topk_w are inputs; s_gu / s_dn null: bf16 weights, else MXFP4 codes
+constexpr int kFewMaxTokens = 64;   // MOE_FEW_MAX_TOKENS
+struct LayerFew {
+  int T, H, F, E, k;
+  const void* x;
+  const void* w_r;
+  const float* bias;
+  int renorm;
+  int32_t* topk_idx;
+  float* topk_w;
+  const void* w_gu;
+  const uint8_t* s_gu;
+  const void* w_dn;
+  const uint8_t* s_dn;
+  const void* residual;
+  void* y;
+  void* ws;
+  int32_t* status;
+};
+size_t layer_few_ws_bytes(int T, int F, int E, int k, bool router);
+hipError_t launch_layer_few(const LayerFew& a, hipStream_t stream);
+
 }  // namespace moe

@@ -1,0 +1,196 @@
+// MXFP4 quantisation of bf16 tensors along their rows, the way back to
+// bf16, and the rearrangement of row-major scales into the layout of the
+// 4-bit GEMM.  Streaming passes bound by HBM: 2 bytes read and 17/32 written
+// per value, and the other way round.
+#include <algorithm>
+
+#include "common.hpp"
+#include "kernels.hpp"
+#include "mxfp4.hpp"
+#include "timer.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kUnroll = 4;   // independent 16-byte chunks per thread
+
+__device__ __forceinline__ uint32_t amax8(const uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t a = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    a = max(a, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+  return a;
+}
+// block exponent of the 32 values held by a quad of lanes, 8 each
+__device__ __forceinline__ int quad_exp(const uint4 v) {
+  uint32_t a = amax8(v);
+  a = max(a, (uint32_t)__shfl_xor((int)a, 1, 64));
+  a = max(a, (uint32_t)__shfl_xor((int)a, 2, 64));
+  return mx4_exp_from_bf16_amax(a);
+}
+
+// n chunks of 8 values (a multiple of 4: quads are whole)
+__global__ __launch_bounds__(256) void mx4_rows_kernel(
+    const uint4* __restrict__ src, int64_t n, uint32_t* __restrict__ codes,
+    uint8_t* __restrict__ scales) {
+  const int64_t S = (int64_t)gridDim.x * 256;
+  for (int64_t c0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
+       c0 - threadIdx.x % 4 < n; c0 += kUnroll * S) {
+    uint4 v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t c = c0 + u * S;
+      v[u] = c < n ? ld_nt(src + c) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t c = c0 + u * S;
+      const int s = quad_exp(v[u]);
+      if (c < n) {
+        codes[c] = e2m1x8_bf16(v[u], mx_scale_f32(s));
+        if ((c & 3) == 0) scales[c >> 2] = (uint8_t)(s + 127);
+      }
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void mx4_dequant_kernel(
+    const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+    int64_t n, uint4* __restrict__ dst) {
+  const int64_t S = (int64_t)gridDim.x * 256;
+  for (int64_t c0 = (int64_t)blockIdx.x * 256 + threadIdx.x; c0 < n;
+       c0 += kUnroll * S) {
+    uint32_t q[kUnroll];
+    uint32_t s[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t c = c0 + u * S;
+      q[u] = c < n ? codes[c] : 0;
+      s[u] = c < n ? scales[c >> 2] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t c = c0 + u * S;
+      if (c < n) dst[c] = e2m1x8_to_bf16(q[u], mx4_scale_of(s[u]));
+    }
+  }
+}
+
+// Rows into the GEMM scale layout: a work-group covers 32 rows x 256 values
+// (one K step); lane l % 32 of a half-wave takes the row's chunk l % 32, so
+// a row's 512 bytes are one run.  The 32 x 8 scale bytes are gathered in LDS
+// and leave as 256 contiguous bytes.  Blocks past K or past the last row
+// carry the scale 1 (their codes read as zeros in the GEMM).
+__global__ __launch_bounds__(256) void mx4_rows_tiled_kernel(
+    const uint4* __restrict__ src, int64_t rows, int cols8, uint32_t nks,
+    uint32_t* __restrict__ codes, uint32_t* __restrict__ scales) {
+  __shared__ uint32_t sc[64];
+  const int64_t g = blockIdx.x / nks;
+  const uint32_t step = (uint32_t)(blockIdx.x - g * nks);
+  const int t = threadIdx.x;
+  const int ch = t & 31, c = (int)step * 32 + ch;
+  uint4 v[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int64_t row = g * 32 + 8 * u + (t >> 5);
+    v[u] = row < rows && c < cols8 ? ld_nt(src + row * cols8 + c)
+                                   : make_uint4(0, 0, 0, 0);
+  }
+  uint8_t* scb = reinterpret_cast<uint8_t*>(sc);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int r = 8 * u + (t >> 5);
+    const int64_t row = g * 32 + r;
+    const bool in = row < rows && c < cols8;
+    const int s = quad_exp(v[u]);
+    if (in) codes[row * cols8 + c] = e2m1x8_bf16(v[u], mx_scale_f32(s));
+    if ((ch & 3) == 0) {
+      const int kb = ch >> 2;
+      scb[(kb & 1) * 128 + r * 4 + (kb >> 1)] = in ? (uint8_t)(s + 127) : 127;
+    }
+  }
+  __syncthreads();
+  if (t < 64) scales[(g * nks + step) * 64 + t] = sc[t];
+}
+
+// row-major scales [rows][k / 32] (k % 128 == 0: whole dwords) -> GEMM
+// layout; a thread takes one row's eight blocks of a K step
+__global__ __launch_bounds__(256) void mx4_retile_kernel(
+    const uint32_t* __restrict__ src, int64_t rows, uint32_t k128,
+    uint32_t nks, int64_t n, uint32_t* __restrict__ dst) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;   // n = row groups x K steps x 32
+  const int64_t gs = i >> 5;
+  const int r = (int)(i & 31);
+  const int64_t g = gs / nks;
+  const uint32_t step = (uint32_t)(gs - g * nks);
+  const int64_t row = g * 32 + r;
+  const uint32_t one = 0x7f7f7f7fu;   // scale 1
+  uint32_t a = one, b = one;
+  if (row < rows) {
+    a = src[row * k128 + 2 * step];
+    if (2 * step + 1 < k128) b = src[row * k128 + 2 * step + 1];
+  }
+  // bytes 0, 2 of a and b are the even blocks
+  dst[gs * 64 + r] = __builtin_amdgcn_perm(b, a, 0x06040200u);
+  dst[gs * 64 + 32 + r] = __builtin_amdgcn_perm(b, a, 0x07050301u);
+}
+
+unsigned stream_grid(int64_t n) {
+  return (unsigned)std::min<int64_t>((n + 256 * kUnroll - 1) /
+                                         (256 * kUnroll),
+                                     65536);
+}
+
+}  // namespace
+
+hipError_t launch_mx4_quant_rows(const void* src, int64_t rows, int64_t cols,
+                                 uint8_t* codes, uint8_t* scales,
+                                 hipStream_t stream, bool tiled) {
+  if (rows * cols == 0) return hipSuccess;
+  KernelScope ks("mxfp4_quantize", stream);
+  if (tiled) {
+    const uint32_t nks = (uint32_t)((cols + 255) / 256);
+    hipLaunchKernelGGL(mx4_rows_tiled_kernel,
+                       dim3((unsigned)((rows + 31) / 32 * nks)), dim3(256), 0,
+                       stream, static_cast<const uint4*>(src), rows,
+                       (int)(cols / 8), nks,
+                       reinterpret_cast<uint32_t*>(codes),
+                       reinterpret_cast<uint32_t*>(scales));
+  } else {
+    const int64_t n = rows * cols / 8;
+    hipLaunchKernelGGL(mx4_rows_kernel, dim3(stream_grid(n)), dim3(256), 0,
+                       stream, static_cast<const uint4*>(src), n,
+                       reinterpret_cast<uint32_t*>(codes), scales);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_mx4_dequant(const uint8_t* codes, const uint8_t* scales,
+                              int64_t values, void* dst, hipStream_t stream) {
+  if (values == 0) return hipSuccess;
+  KernelScope ks("mxfp4_dequantize", stream);
+  const int64_t n = values / 8;
+  hipLaunchKernelGGL(mx4_dequant_kernel, dim3(stream_grid(n)), dim3(256), 0,
+                     stream, reinterpret_cast<const uint32_t*>(codes), scales,
+                     n, static_cast<uint4*>(dst));
+  return hipGetLastError();
+}
+
+hipError_t launch_mx4_scales_retile(const uint8_t* src, int64_t rows,
+                                    int64_t k, uint8_t* dst,
+                                    hipStream_t stream) {
+  if (rows == 0) return hipSuccess;
+  KernelScope ks("mxfp4_scales_retile", stream);
+  const uint32_t nks = (uint32_t)((k + 255) / 256);
+  const int64_t n = (rows + 31) / 32 * 32 * nks;
+  hipLaunchKernelGGL(mx4_retile_kernel, dim3((unsigned)((n + 255) / 256)),
+                     dim3(256), 0, stream,
+                     reinterpret_cast<const uint32_t*>(src), rows,
+                     (uint32_t)(k / 128), nks, n,
+                     reinterpret_cast<uint32_t*>(dst));
+  return hipGetLastError();
+}
+
+}  // namespace moe
