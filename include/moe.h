@@ -813,10 +813,11 @@ moe_status_t mxfp4_dequantize(moe_ctx_t ctx, const uint8_t* codes,
  * [PG1, section "Grouped experts instead of a Python loop": one call covers
  *  every expert; here for token counts at which the weights' bytes, not the
  *  products, are the work.]
- *   y[t] = residual[t] + sum_j W_dn[e_tj] a_tj
- *   a_tj = w_tj * silu(W_gu[e_tj] gate rows x_t) * (up rows x_t)
+ *   y[t] = residual[t] + sum_j w_tj W_dn[e_tj] a_tj
+ *   a_tj = silu(W_gu[e_tj] gate rows x_t) * (up rows x_t)
  * Products and sums are float32 (a_tj is rounded once to bf16, the operand
- * of the second product), y is rounded once.
+ * of the second product), the weighting follows the second product, slots
+ * add up in order, y is rounded once.
  * Routing: with w_r, topk_idx and topk_w are outputs: logits = x w_r^T +
  * router_bias summed in float64 and rounded to float32, then the rule of
  * moe_route_topk with `renormalize`.  Without w_r they are inputs (from

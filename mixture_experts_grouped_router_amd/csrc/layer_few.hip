@@ -1,31 +1,40 @@
 // The whole mixture-of-experts layer for a few tokens: router logits, top-k,
 // the chosen experts' gate/up and down products and the combine.
 //
-//   y[t] = residual[t] + sum_j W_dn[e_tj] a_tj,
-//   a_tj = bf16(w_tj silu(W_g[e_tj] x_t) * (W_u[e_tj] x_t))
+//   a_tj = bf16(silu(W_g[e_tj] x_t) * (W_u[e_tj] x_t))
+//   y[t] = residual[t] + sum_j w_tj W_dn[e_tj] a_tj
 //
 // Bound by reading the reached experts' weights once (6 F H bytes each in
 // bf16, 1.59 F H in MXFP4), so the weights stream from HBM straight into
-// MFMA operands and nothing else matters but that enough loads are in
-// flight.  The product is v_mfma_f32_16x16x32_bf16 with the weights as the
-// 16-row operand and the tokens as the 16 columns.  Few tokens would leave
-// most columns empty and 16 weight rows per load make 64-byte runs, so K is
-// split S ways across rows and columns: matrix row (hr, s) holds the s-th
-// 16-byte-times-four piece of weight row hr, column (tok, s') the s'-th
-// piece of a token, and only the products with s = s' are kept (the others
-// are free).  A load then covers 16 / S weight rows in runs of 64 S bytes.
+// MFMA operands and what matters is how many loads are in flight.  The
+// product is v_mfma_f32_16x16x32_bf16 with the weights as the 16-row operand
+// and the tokens as the 16 columns.  16 weight rows per load would make
+// 64-byte runs and leave most columns empty, so K is split two ways across
+// rows and columns: matrix row (r, s) holds the s-th half of a 128-byte piece
+// of weight row r, column (t, s') the s'-th half of token t's piece, and only
+// the products with s = s' are kept (the others are free).  A load then
+// covers eight weight rows in whole 128-byte lines, and eight tokens make a
+// column set.
 //
 // MXFP4 weights are read as they are (one 16-byte load is one block of 32
 // with its scale) and widened to bf16 in registers; E2M1 times a power of
 // two is exact there.
 //
-// Launches: router logits and top-k (only if asked for), gate/up, down with
-// the combine.  The second product keeps float32 sums per token over all of
-// a token's experts, so no per-pair output is ever written.
+// The pairs (token, slot) are sorted by expert into entries of one expert
+// and a few of its pairs; an expert with more of them makes several
+// entries and its weights come from the caches again.  Every work-group of
+// the first product sorts for itself (a few hundred pairs in LDS), which
+// costs less than a launch of its own; one of them leaves the plan for the
+// second product.
+//
+// Launches: router logits (if asked for; with more than kFuseTopk tokens
+// also moe_route_topk's kernel, below that every work-group picks the
+// experts for itself), gate/up, down with the combine.
 #include <algorithm>
 
 #include "common.hpp"
 #include "kernels.hpp"
+#include "lanes.hpp"
 #include "mxfp4.hpp"
 #include "timer.hpp"
 
@@ -36,8 +45,20 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int32_t kDevErrExpertId = 1;   // include/moe.h MOE_DEVERR_*
+constexpr int32_t kDevErrLogits = 3;
 constexpr uint32_t kFar = 0xfffffff0u;   // an offset no descriptor covers
 constexpr int kBufFlags = 0x00020000;    // raw buffer, 32-bit data format
+constexpr int kRows = 8;                 // weight rows of a load, tokens of a
+                                         // column set
+constexpr int kMaxPairs = kFewMaxTokens * 32;   // MOE_MAX_TOPK
+constexpr int kFuseTopk = 4;             // tokens whose experts every
+                                         // work-group picks for itself
+// Gate/up: from this many items on a wave takes whole items and the grid is
+// two work-groups per CU; below, four waves share each item and the grid is
+// at most three per CU (the register file's limit).  Qwen3-shaped bf16, one
+// token (768 items): 11.4 us against 14; 64 tokens (12288): 265 us for the
+// layer against 270.
+constexpr int kWholeItems = 4096;
 
 struct FewParams {
   const char* x;            // bf16 [T, H]
@@ -45,9 +66,12 @@ struct FewParams {
   const uint8_t* s_gu;      // scales [E, 2F, H / 32]
   const char* w_dn;
   const uint8_t* s_dn;
-  const int32_t* idx;       // [T, k]
-  const float* w;           // [T, k]
+  const float* logits;      // [T, E]: the first product picks the experts
+  int32_t* idx;             // [T, k]: read, or written with logits
+  float* w;                 // [T, k]: likewise
+  int renorm;
   uint16_t* a;              // bf16 [T k, F]
+  int32_t* plan;            // [0] entries, [4 ..] entries, then the pair list
   const uint16_t* res;      // bf16 [T, H] or null
   uint16_t* y;              // bf16 [T, H]
   int T, H, F, E, k;
@@ -67,11 +91,14 @@ __device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t r,
 __device__ __forceinline__ bf16x8_t as_bf16x8(const uint4 v) {
   return __builtin_bit_cast(bf16x8_t, v);
 }
+__device__ __forceinline__ int uniform(int v) {
+  return __builtin_amdgcn_readfirstlane(v);
+}
 
-// Weights of one format: bytes of a 16-byte piece's K values, MFMAs per
-// piece, and the piece as MFMA operands.
+// Weights of one format: K values of a 16-byte piece, MFMAs per piece, and
+// the piece as MFMA operands.
 struct FmtBf16 {
-  static constexpr int kValues = 8;   // K values per 16 bytes
+  static constexpr int kValues = 8;
   static constexpr int kMfma = 1;
   static __device__ __forceinline__ void widen(const uint4 c, uint32_t,
                                                bf16x8_t (&o)[1]) {
@@ -91,34 +118,64 @@ struct FmtMx4 {
   }
 };
 
-// A wave's pieces of RS row sets (16 / S weight rows each) and NS column
-// sets (16 / S tokens each) for U chunks of K.
-template <class FMT, int S, int RS, int NS, int U>
-struct Chunk {
+template <int N>
+__device__ __forceinline__ bf16x8_t rotate_row(const uint4 v) {
+  if constexpr (N == 0) {
+    return as_bf16x8(v);
+  } else {   // lane i of 16 <- lane i + N
+    constexpr int C = kDppRor0 + 16 - N;
+    return as_bf16x8(make_uint4((uint32_t)dpp_i<C>((int)v.x),
+                                (uint32_t)dpp_i<C>((int)v.y),
+                                (uint32_t)dpp_i<C>((int)v.z),
+                                (uint32_t)dpp_i<C>((int)v.w)));
+  }
+}
+
+// U chunks (128 bytes of each weight row) of RS row sets and NS column sets.
+// Loads are issued whether there is something to read or not (an offset past
+// the descriptor reads zeros without touching memory), so that the number in
+// flight is known and a batch is waited for without waiting for the next.
+//
+// Column sets of CT = 8 tokens load one operand per MFMA of a piece, most of
+// whose lanes are idle with few tokens: for MXFP4, four loads of activations
+// per load of weights.  Column sets of CT = 2 tokens take the four operands
+// of a piece in one load, lane 8 t + 2 m + s of 16 holding token t's half s
+// for MFMA m, and rotate them into the columns 8 t + s; the other columns
+// multiply whatever comes along and are not kept.
+template <class FMT, int CT, int RS, int NS, int U>
+struct Batch {
   static constexpr bool kMx = FMT::kMfma > 1;
+  static_assert(CT == 8 || (CT == 2 && FMT::kMfma == 4), "column sets");
+  static constexpr int kX = CT == 8 ? FMT::kMfma : 1;
+  static constexpr int kCols = NS * CT;
   uint4 wv[U][RS];
   uint32_t sv[U][RS];
-  uint4 xv[U][NS][FMT::kMfma];
-  // chunk c0 + u * cstep of K; kbytes: bytes of a weight row; rowoff: byte
-  // offsets of the lane's weight rows (kFar: none), srow the rows' scale
-  // offsets; xoff: byte offset of the lane's token (kFar: none)
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rw,
-                                       __amdgpu_buffer_rsrc_t rs,
-                                       __amdgpu_buffer_rsrc_t rx,
-                                       const uint32_t (&rowoff)[RS],
-                                       const uint32_t (&srow)[RS],
-                                       const uint32_t (&xoff)[NS], int c0,
-                                       int cstep, int cend, uint32_t kbytes,
-                                       uint32_t piece) {
+  uint4 xv[U][NS][kX];
+  // the lane's token of column set q, to load (a negative one: none) or to
+  // keep results of
+  static __device__ __forceinline__ int load_place(int lane, int q) {
+    return CT == 8 ? q * 8 + ((lane & 15) >> 1) : q * 2 + ((lane >> 3) & 1);
+  }
+  static __device__ __forceinline__ int keep_place(int lane, int q) {
+    return CT == 8 || (lane & 6) == 0 ? load_place(lane, q) : kFewMaxTokens;
+  }
+  // chunks c0 + u cstep below cend; row: the lane's byte offset in each row
+  // set (kFar: none), srow its scale offset, xoff: the lane's token (kFar:
+  // none); piece: the lane's bytes of a chunk
+  __device__ __forceinline__ void load(
+      __amdgpu_buffer_rsrc_t rw, __amdgpu_buffer_rsrc_t rs,
+      __amdgpu_buffer_rsrc_t rx, const uint32_t (&row)[RS],
+      const uint32_t (&srow)[RS], const uint32_t (&xoff)[NS], int c0,
+      int cstep, int cend, uint32_t kbytes, uint32_t piece, int lane) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = c0 + u * cstep;
-      const uint32_t kb = (uint32_t)c * (64u * S) + piece;
+      const uint32_t kb = (uint32_t)c * 128u + piece;
       const bool in = c < cend && kb < kbytes;
 #pragma unroll
       for (int i = 0; i < RS; ++i) {
-        const bool ok = in && rowoff[i] != kFar;
-        wv[u][i] = load16(rw, ok ? rowoff[i] + kb : kFar);
+        const bool ok = in && row[i] != kFar;
+        wv[u][i] = load16(rw, ok ? row[i] + kb : kFar);
         if constexpr (kMx)
           sv[u][i] = __builtin_amdgcn_raw_buffer_load_b8(
               rs, ok ? srow[i] + (kb >> 4) : kFar, 0, 0);
@@ -126,11 +183,12 @@ struct Chunk {
           sv[u][i] = 0;
       }
       // the piece's kValues activations, 16 bytes each eight
-      const uint32_t xb = kb * (uint32_t)(2 * FMT::kValues / 16);
+      const uint32_t xb = kb * (uint32_t)(2 * FMT::kValues / 16) +
+                          (CT == 2 ? 16u * ((lane >> 1) & 3) : 0u);
 #pragma unroll
       for (int n = 0; n < NS; ++n)
 #pragma unroll
-        for (int m = 0; m < FMT::kMfma; ++m)
+        for (int m = 0; m < kX; ++m)
           xv[u][n][m] =
               load16(rx, in && xoff[n] != kFar ? xoff[n] + xb + 16u * m
                                                : kFar);
@@ -138,7 +196,21 @@ struct Chunk {
   }
   __device__ __forceinline__ void mma(f32x4_t (&acc)[RS][NS]) const {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      bf16x8_t x[NS][FMT::kMfma];
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        if constexpr (CT == 2) {
+          x[n][0] = rotate_row<0>(xv[u][n][0]);
+          x[n][1] = rotate_row<2>(xv[u][n][0]);
+          x[n][2] = rotate_row<4>(xv[u][n][0]);
+          x[n][3] = rotate_row<6>(xv[u][n][0]);
+        } else {
+#pragma unroll
+          for (int m = 0; m < FMT::kMfma; ++m)
+            x[n][m] = as_bf16x8(xv[u][n][m]);
+        }
+      }
 #pragma unroll
       for (int i = 0; i < RS; ++i) {
         bf16x8_t o[FMT::kMfma];
@@ -148,400 +220,627 @@ struct Chunk {
 #pragma unroll
           for (int m = 0; m < FMT::kMfma; ++m)
             acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                o[m], as_bf16x8(xv[u][n][m]), acc[i][n], 0, 0, 0);
+                o[m], x[n][m], acc[i][n], 0, 0, 0);
       }
+    }
   }
 };
 
 // The kept products of a 16 x 16 result: lane l holds rows 4 (l / 16) + r of
-// column l % 16; row (hr, s) and column (tok, s') count where s = s'.  Each
-// goes to red[(hr, tok, s)].
-template <int S>
-__device__ __forceinline__ void keep_diagonal(const f32x4_t& acc, int lane,
-                                              float* red) {
-  constexpr int R = 16 / S;
-  const int c = lane & 15, q = lane >> 4;
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int row = 4 * q + r;
-    if (row % S == c % S)
-      red[((row / S) * R + c / S) * S + c % S] = acc[r];
-  }
+// column c = l % 16, of which those with row % 2 = c % 2 count; the other
+// half of K is the neighbouring lane's.  Returns the sum of weight row
+// 2 (l / 16) + c % 2 and the token of column c / 2.
+__device__ __forceinline__ float keep(const f32x4_t& acc, int lane) {
+  const bool odd = lane & 1;
+  float t0 = odd ? acc[1] : acc[0];
+  float t1 = odd ? acc[3] : acc[2];
+  t0 += dpp_f<kDppXor1>(t0);
+  t1 += dpp_f<kDppXor1>(t1);
+  return odd ? t1 : t0;
 }
 
-constexpr int kMaxPairs = kFewMaxTokens * 32;   // MOE_MAX_TOPK
+// ---- plan --------------------------------------------------------------------
+// An entry: expert, first place in the pair list, pairs (at most 32).
+__device__ __forceinline__ int make_entry(int e, int start, int n) {
+  return e | start << 10 | n << 21;
+}
+__device__ __forceinline__ int entry_expert(int v) { return v & 1023; }
+__device__ __forceinline__ int entry_start(int v) { return v >> 10 & 2047; }
+__device__ __forceinline__ int entry_pairs(int v) { return v >> 21; }
+// A place of the pair list: pair, token.
+__device__ __forceinline__ int place_pair(int v) { return v & 2047; }
+__device__ __forceinline__ int place_token(int v) { return v >> 11; }
 
-// ---- gate/up ---------------------------------------------------------------
-// A work-group takes RSF x 16 / S FFN columns (their gate and up rows) of
-// one expert for all of its pairs; its waves take K chunks in turn and add
-// their sums through LDS in wave order.  slot (blockIdx.y): with fewer pairs
-// than experts a pair, which stands for its expert if no earlier pair has
-// the same one; else an expert.
-template <class FMT, int S, int RSF, int NS>
-__device__ __forceinline__ void gate_up_pass(const FewParams& p, int e,
-                                             const uint16_t* list, int n,
-                                             int c0, float* red) {
-  constexpr int R = 16 / S, RS = 2 * RSF;
-  constexpr int U = NS >= 4 ? 1 : 2;
+struct PlanLds {
+  int ent[kMaxPairs];
+  int lst[kMaxPairs];
+  int count[1024];           // MOE_MAX_EXPERTS
+  int16_t sidx[kMaxPairs];   // expert of a pair, -1: none
+  uint16_t pos[kMaxPairs];   // its place among the expert's pairs
+};
+
+// float -> integer of the same order (-0 as +0; a total order with NaN too)
+__device__ __forceinline__ int order_key(float v) {
+  const int b = __float_as_int(v + 0.0f);
+  return b < 0 ? b ^ 0x7fffffff : b;
+}
+
+// The k experts of the tokens with the largest logits (equal ones: lower id
+// first): an expert's slot is the number of experts ahead of it, counted by
+// 256 / E threads each.  key, rank: E values of LDS each.  The work-group
+// with `out` also writes ids and weights: softmax over the chosen or over
+// all, in float64.
+__device__ __forceinline__ void pick_experts(const FewParams& p, PlanLds& s,
+                                             uint64_t* key, int* rank,
+                                             bool out) {
   const int t = threadIdx.x, lane = t & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int f0 = blockIdx.x * (R * RSF);
-  const uint32_t kbytes = (uint32_t)p.H / FMT::kValues * 16u;
-  const uint32_t rows = 2u * p.F;
-  const int row = (lane & 15) / S, sp = (lane & 15) % S, g = lane >> 4;
-  const uint32_t piece = (uint32_t)(sp * 4 + g) * 16u;
-  const __amdgpu_buffer_rsrc_t rw =
-      rsrc(p.w_gu + (int64_t)e * rows * kbytes, rows * kbytes);
-  const uint32_t sbytes = (uint32_t)p.H / 32;
-  const __amdgpu_buffer_rsrc_t rsc =
-      rsrc(p.s_gu ? p.s_gu + (int64_t)e * rows * sbytes : nullptr,
-           p.s_gu ? rows * sbytes : 0u);
-  const __amdgpu_buffer_rsrc_t rx = rsrc(p.x, (uint32_t)p.T * p.H * 2u);
-  uint32_t rowoff[RS], srow[RS], xoff[NS];
-#pragma unroll
-  for (int i = 0; i < RS; ++i) {
-    const int f = f0 + (i >> 1) * R + row;
-    const uint32_t rr = (uint32_t)((i & 1) ? p.F + f : f);
-    rowoff[i] = f < p.F ? rr * kbytes : kFar;
-    srow[i] = rr * sbytes;
-  }
-#pragma unroll
-  for (int m = 0; m < NS; ++m) {
-    const int j = c0 + m * R + row;   // column (tok, s) is laid out like (hr, s)
-    xoff[m] = j < n ? (uint32_t)(list[j] / p.k) * (uint32_t)p.H * 2u : kFar;
-  }
-  f32x4_t acc[RS][NS];
-#pragma unroll
-  for (int i = 0; i < RS; ++i)
-#pragma unroll
-    for (int m = 0; m < NS; ++m) acc[i][m] = f32x4_t{};
-  const int nch = (int)((kbytes + 64 * S - 1) / (64 * S));
-  for (int c = wave; c < nch; c += 4 * U) {
-    Chunk<FMT, S, RS, NS, U> ch;
-    ch.load(rw, rsc, rx, rowoff, srow, xoff, c, 4, nch, kbytes, piece);
-    ch.mma(acc);
-  }
-  constexpr int kSet = R * R * S;   // kept products of a 16 x 16 result
-#pragma unroll
-  for (int i = 0; i < RS; ++i)
-#pragma unroll
-    for (int m = 0; m < NS; ++m)
-      keep_diagonal<S>(acc[i][m], lane,
-                       red + ((wave * RS + i) * NS + m) * kSet);
-  __syncthreads();
-  // one (f, pair) per thread and turn, f fastest
-  for (int o = t; o < RSF * R * NS * R; o += 256) {
-    const int fl = o % (RSF * R), jl = o / (RSF * R);
-    const int f = f0 + fl, j = c0 + jl;
-    if (f < p.F && j < n) {
-      float v[2] = {0.0f, 0.0f};
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        for (int w = 0; w < 4; ++w) {
-          const float* q = red +
-                           ((w * RS + 2 * (fl / R) + h) * NS + jl / R) * kSet +
-                           ((fl % R) * R + jl % R) * S;
-#pragma unroll
-          for (int s = 0; s < S; ++s) v[h] += q[s];
-        }
-      const int pr = list[j];
-      const float sg = v[0] * __builtin_amdgcn_rcpf(1.0f + __expf(-v[0]));
-      p.a[(int64_t)pr * p.F + f] = (uint16_t)f32_to_bf16(p.w[pr] * (sg * v[1]));
+  const int E = p.E, k = p.k;
+  const int per = E <= 32 ? 8 : E <= 64 ? 4 : E <= 128 ? 2 : 1;
+  for (int tok = 0; tok < p.T; ++tok) {
+    const float* row = p.logits + (int64_t)tok * E;
+    for (int e = t; e < E; e += 256) {
+      const float v = row[e];
+      if (out && !__builtin_isfinite(v)) report_error(p.status, kDevErrLogits);
+      // larger logit, then lower id: one unsigned order without ties
+      key[e] = (uint64_t)((uint32_t)order_key(v) ^ 0x80000000u) << 32 |
+               (uint32_t)(1023 - e);
+      rank[e] = 0;
     }
-  }
-  __syncthreads();   // red and list are reused
-}
-
-template <class FMT, int S, int RSF, int NSMAX>
-__global__ __launch_bounds__(256) void few_gate_up_kernel(FewParams p) {
-  constexpr int R = 16 / S;
-  __shared__ uint16_t list[kMaxPairs];
-  __shared__ int cnt[4];
-  __shared__ float red[4 * 2 * RSF * NSMAX * R * R * S];
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const int P = p.T * p.k;
-  const bool by_pair = P <= p.E;
-  const int slot = blockIdx.y;
-  if (slot == 0 && blockIdx.x == 0)
-    for (int i = t; i < P; i += 256)
-      if ((uint32_t)p.idx[i] >= (uint32_t)p.E)
-        report_error(p.status, kDevErrExpertId);
-  const int e = by_pair ? p.idx[slot] : slot;
-  if ((uint32_t)e >= (uint32_t)p.E) return;
-  int n = 0;
-  for (int b = 0; b < P; b += 256) {
-    const int i = b + t;
-    const bool hit = i < P && p.idx[i] == e;
-    const uint64_t m = __ballot(hit);
-    if (lane == 0) cnt[wave] = __popcll(m);
-    // (an earlier pair has this expert: its work-group does the work)
-    if (__syncthreads_or(hit && by_pair && i < slot)) return;
-    int at = n;
-    for (int w = 0; w < 4; ++w) {
-      if (w < wave) at += cnt[w];
-      n += cnt[w];
+    if (t == 0) key[E] = 0;   // pairs of keys are read
+    __syncthreads();
+    for (int i = t; i < E * per; i += 256) {
+      const int e = i / per, part = i - e * per;
+      const uint64_t mine = key[e];
+      const int half = (E + 1) / 2, j1 = half * (part + 1) / per;
+      int n = 0;
+#pragma unroll 4
+      for (int j = half * part / per; j < j1; ++j) {
+        const ulonglong2 o = reinterpret_cast<const ulonglong2*>(key)[j];
+        n += (o.x > mine) + (o.y > mine);
+      }
+      atomicAdd(&rank[e], n);
     }
-    if (hit) list[at + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)i;
+    __syncthreads();
+    for (int e = t; e < E; e += 256)
+      if (rank[e] < k) s.sidx[tok * k + rank[e]] = (int16_t)e;
     __syncthreads();
   }
-  for (int c0 = 0; c0 < n; c0 += NSMAX * R) {
-    const int left = n - c0;
-    if constexpr (NSMAX >= 4) {
-      if (left > 2 * R) {
-        gate_up_pass<FMT, S, RSF, 4>(p, e, list, n, c0, red);
-        continue;
-      }
+  if (!out) return;
+  const int tok = t >> 6;   // kFuseTopk = 4 tokens, four waves
+  if (tok >= p.T) return;
+  const float* row = p.logits + (int64_t)tok * E;
+  const double top = (double)row[s.sidx[tok * k]];
+  double num = 0.0, part = 0.0;
+  int e = 0;
+  if (lane < k) {
+    e = s.sidx[tok * k + lane];
+    num = exp((double)row[e] - top);
+  }
+  if (p.renorm) {
+    part = num;
+  } else {
+    for (int j = lane; j < E; j += 64) part += exp((double)row[j] - top);
+  }
+  part = lanes_sum<64>(part);
+  if (lane < k) {
+    p.idx[tok * k + lane] = e;
+    p.w[tok * k + lane] = (float)(num / part);
+  }
+}
+
+// Sorts the pairs by expert into entries of at most `cols` pairs; returns
+// the number of entries.  256 threads.
+__device__ __forceinline__ int build_plan(const FewParams& p, PlanLds& s,
+                                          uint64_t* keys, int cols) {
+  const int t = threadIdx.x, P = p.T * p.k;
+  const bool first = blockIdx.x == 0;
+  if (p.logits) {
+    pick_experts(p, s, keys, s.count, first);
+  } else {
+    for (int i = t; i < P; i += 256) {
+      const int e = p.idx[i];
+      const bool ok = (uint32_t)e < (uint32_t)p.E;
+      s.sidx[i] = ok ? (int16_t)e : (int16_t)-1;
+      if (!ok && first) report_error(p.status, kDevErrExpertId);
     }
-    if constexpr (NSMAX >= 2) {
-      if (left > R) {
-        gate_up_pass<FMT, S, RSF, 2>(p, e, list, n, c0, red);
-        continue;
-      }
+  }
+  int n;
+  if (p.T == 1) {   // every pair is an entry; P <= 32
+    __syncthreads();
+    const int e = t < P ? s.sidx[t] : -1;
+    const uint64_t m = __ballot(e >= 0);
+    if (e >= 0) {   // wave 0
+      const int at = __popcll(m & ((1ull << t) - 1));
+      s.ent[at] = make_entry(e, at, 1);
+      s.lst[at] = t;
     }
-    gate_up_pass<FMT, S, RSF, 1>(p, e, list, n, c0, red);
+    if (t == 0) s.count[0] = __popcll(m);
+    __syncthreads();
+    n = s.count[0];
+  } else {
+    for (int i = t; i < p.E; i += 256) s.count[i] = 0;
+    __syncthreads();
+    // places by pair number (the same in every work-group: entries of one
+    // expert are told apart by it), 64 pairs at a time by one wave
+    if (t < 64)
+      for (int b = 0; b < P; b += 64) {
+        const int e = b + t < P ? s.sidx[b + t] : -1;
+        uint64_t same = __ballot(e >= 0);
+#pragma unroll
+        for (int bit = 0; bit < 10; ++bit) {
+          const uint64_t m = __ballot((e >> bit) & 1);
+          same &= (e >> bit) & 1 ? m : ~m;
+        }
+        if (e >= 0) {
+          const int before = __popcll(same & ((1ull << t) - 1));
+          const int base = s.count[e];
+          s.pos[b + t] = (uint16_t)(base + before);
+          if (before == 0) s.count[e] = base + __popcll(same);
+        }
+      }
+    __syncthreads();
+    // thread t: experts 4 t .. 4 t + 3
+    int c[4], pairs = 0, ents = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = 4 * t + i < p.E ? s.count[4 * t + i] : 0;
+      pairs += c[i];
+      ents += (c[i] + cols - 1) / cols;
+    }
+    int32_t total;
+    // both prefixes in one scan: at most 2048 of each
+    const int pre = block_exclusive_scan_256(pairs << 12 | ents, &total);
+    int at = pre >> 12, ea = pre & 4095;
+    n = total & 4095;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (4 * t + i < p.E) s.count[4 * t + i] = at;
+      for (int q = 0; q < c[i]; q += cols)
+        s.ent[ea++] = make_entry(4 * t + i, at + q, min(cols, c[i] - q));
+      at += c[i];
+    }
+    __syncthreads();
+    for (int i = t; i < P; i += 256)
+      if (s.sidx[i] >= 0)
+        s.lst[s.count[s.sidx[i]] + s.pos[i]] = i | (i / p.k) << 11;
+    __syncthreads();
+  }
+  if (first) {
+    if (t == 0) p.plan[0] = n;
+    for (int i = t; i < P; i += 256) {
+      p.plan[4 + i] = i < n ? s.ent[i] : 0;
+      p.plan[4 + P + i] = s.lst[i];
+    }
+  }
+  return n;
+}
+
+// ---- gate/up -----------------------------------------------------------------
+// An item is RSF x 8 FFN columns (their gate and up rows) of one entry.  KS =
+// 1: a wave per item, each wave an equal run of the items; KS = 4: the
+// work-group's waves take the item's chunks in turn and add their sums in
+// wave order (few items: more loads in flight for each).
+template <class FMT, int CT, int NS, int RSF, int KS, int U>
+__global__ __launch_bounds__(256) void few_gate_up_kernel(FewParams p) {
+  constexpr int RS = 2 * RSF;
+  using B = Batch<FMT, CT, RS, NS, U>;
+  __shared__ PlanLds s;
+  // the picked experts' keys; then the four waves' sums, two turns
+  constexpr int kRed = KS > 1 ? 2 * 4 * RS * NS * 64 : 0;
+  __shared__ __attribute__((aligned(16))) uint64_t
+      scratch[kRed / 2 > 1026 ? kRed / 2 : 1026];
+  const int n = build_plan(p, s, scratch, B::kCols);
+  const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
+  const int row = (lane & 15) >> 1;
+  const uint32_t piece = (uint32_t)((lane & 1) * 4 + (lane >> 4)) * 16u;
+  const uint32_t kbytes = (uint32_t)p.H / FMT::kValues * 16u;
+  const uint32_t rows = 2u * p.F, sbytes = (uint32_t)p.H / 32;
+  const __amdgpu_buffer_rsrc_t rx = rsrc(p.x, (uint32_t)p.T * p.H * 2u);
+  const int nch = (int)((kbytes + 127) / 128);
+  const int nb = (nch + KS * U - 1) / (KS * U);
+  const int nft = (p.F + kRows * RSF - 1) / (kRows * RSF);
+  const int64_t N = (int64_t)n * nft;
+  const int64_t W = KS == 1 ? gridDim.x * 4 : gridDim.x;
+  const int64_t me = KS == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
+  const int i0 = uniform((int)(N * me / W));
+  const int i1 = uniform((int)(N * (me + 1) / W));
+  if (i0 >= i1) return;   // KS = 4: the whole work-group
+  const int cw = KS == 1 ? 0 : wave;
+
+  auto load = [&](B& b, int it, int bt) {
+    const bool real = it < i1;
+    const int item = real ? it : i0;
+    const int i = item / nft, f0 = (item - i * nft) * (kRows * RSF);
+    const int en = uniform(s.ent[i]);
+    const int e = entry_expert(en), st = entry_start(en), m = entry_pairs(en);
+    uint32_t wrow[RS], srow[RS], xoff[NS];
+#pragma unroll
+    for (int q = 0; q < RS; ++q) {
+      const int f = f0 + (q >> 1) * kRows + row;
+      const uint32_t r = (uint32_t)((q & 1) ? p.F + f : f);
+      wrow[q] = f < p.F ? r * kbytes : kFar;
+      srow[q] = r * sbytes;
+    }
+#pragma unroll
+    for (int q = 0; q < NS; ++q) {
+      const int j = B::load_place(lane, q);
+      xoff[q] = j < m ? (uint32_t)place_token(s.lst[st + j]) *
+                            (uint32_t)p.H * 2u
+                      : kFar;
+    }
+    b.load(rsrc(p.w_gu + (int64_t)e * rows * kbytes, rows * kbytes),
+           rsrc(p.s_gu + (int64_t)e * rows * sbytes,
+                B::kMx ? rows * sbytes : 0u),
+           rx, wrow, srow, xoff, bt * U * KS + cw, KS, real ? nch : 0, kbytes,
+           piece, lane);
+  };
+  f32x4_t acc[RS][NS];
+  auto clear = [&]() {
+#pragma unroll
+    for (int q = 0; q < RS; ++q)
+#pragma unroll
+      for (int m = 0; m < NS; ++m) acc[q][m] = f32x4_t{};
+  };
+  // the lane's value: FFN column 2 (lane / 16) + lane % 2 of a row set
+  const int fl = 2 * (lane >> 4) + (lane & 1);
+  int turn = 0;
+  auto finish = [&](int it) {
+    const int i = it / nft, f0 = (it - i * nft) * (kRows * RSF);
+    const int en = uniform(s.ent[i]);
+    const int st = entry_start(en), m = entry_pairs(en);
+    float* red = reinterpret_cast<float*>(scratch) + turn * (kRed / 2);
+    turn ^= 1;
+    if constexpr (KS > 1) {
+#pragma unroll
+      for (int q = 0; q < RS; ++q)
+#pragma unroll
+        for (int c = 0; c < NS; ++c)
+          red[((wave * RS + q) * NS + c) * 64 + lane] = keep(acc[q][c], lane);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int q = 0; q < RSF; ++q)
+#pragma unroll
+      for (int c = 0; c < NS; ++c) {
+        // KS = 4: the waves share the (q, c) out among themselves
+        if (KS > 1 && (q * NS + c) % 4 != wave) continue;
+        float g, u;
+        if constexpr (KS == 1) {
+          g = keep(acc[2 * q][c], lane);
+          u = keep(acc[2 * q + 1][c], lane);
+        } else {
+          g = u = 0.0f;
+#pragma unroll
+          for (int w = 0; w < KS; ++w) {
+            g += red[((w * RS + 2 * q) * NS + c) * 64 + lane];
+            u += red[((w * RS + 2 * q + 1) * NS + c) * 64 + lane];
+          }
+        }
+        const int f = f0 + q * kRows + fl, j = B::keep_place(lane, c);
+        if (f < p.F && j < m) {
+          const float sg = g * __builtin_amdgcn_rcpf(1.0f + __expf(-g));
+          p.a[(int64_t)place_pair(s.lst[st + j]) * p.F + f] =
+              (uint16_t)f32_to_bf16(sg * u);
+        }
+      }
+    clear();
+  };
+
+  clear();
+  int it = i0, bt = 0;   // next to load
+  int ci = i0, cb = 0;   // next to multiply
+  auto fetch = [&](B& b) {
+    load(b, it, bt);
+    if (++bt == nb) {
+      bt = 0;
+      ++it;
+    }
+  };
+  auto step = [&](const B& b) {
+    b.mma(acc);
+    if (++cb == nb) {
+      finish(ci);
+      cb = 0;
+      ++ci;
+    }
+  };
+  B b0, b1;
+  fetch(b0);
+  while (true) {
+    fetch(b1);
+    step(b0);
+    if (ci >= i1) break;
+    fetch(b0);
+    step(b1);
+    if (ci >= i1) break;
   }
 }
 
 // ---- down and combine --------------------------------------------------------
-// A work-group takes 16 / S rows of every reached expert's W_dn for all
-// tokens.  The chunks of all experts form one list, dealt to the eight waves
-// in equal runs.  Columns are the tokens themselves; a token that an expert
-// was not chosen for keeps its sum untouched (a selection, not an addition
-// of zero: an infinite weight of another token's expert stays out).  An
-// expert that a token names twice is taken up again for the second pair.
+// A work-group takes eight rows of every reached expert's W_dn.  The chunks
+// of all entries form one list, dealt to the eight waves in equal runs, so
+// an entry may be shared by neighbouring waves: the one that has its first
+// chunk leaves the sums in z (per pair), the others in a head of their own,
+// added in wave order.  A token's pairs are weighted and added in slot order.
 constexpr int kDownWaves = 8;
 
-template <class FMT, int S, int NS>
+template <class FMT, int CT, int NS, int U>
 __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(
     FewParams p) {
-  constexpr int R = 16 / S;
-  constexpr int kSet = R * R * S;
-  constexpr int U = NS >= 8 ? 2 : 4;
-  __shared__ int16_t sidx[kMaxPairs];
-  __shared__ uint16_t ent[kMaxPairs];   // pair; bit 15: that pair alone
-  __shared__ int first[1024];           // MOE_MAX_EXPERTS
-  __shared__ int cnt[kDownWaves];
-  __shared__ float red[kDownWaves * NS * kSet];
-  const int t = threadIdx.x, lane = t & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int P = p.T * p.k, k = p.k;
-  for (int i = t; i < p.E; i += 64 * kDownWaves) first[i] = 0x7fffffff;
-  for (int i = t; i < P; i += 64 * kDownWaves) {
-    const int e = p.idx[i];
-    sidx[i] = (uint32_t)e < (uint32_t)p.E ? (int16_t)e : (int16_t)-1;
+  using B = Batch<FMT, CT, 1, NS, U>;
+  constexpr int kThreads = 64 * kDownWaves;
+  constexpr int kCols = B::kCols;
+  extern __shared__ float dyn[];
+  const int P = p.T * p.k;
+  float* z = dyn;                                   // [P][8]
+  float* head = z + P * kRows;                      // [waves][kCols][8]
+  int* ent = reinterpret_cast<int*>(head + kDownWaves * kCols * kRows);
+  int* lst = ent + P;
+  int* hent = lst + P;                              // [waves] entry or -1
+  const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
+  const int n = uniform(p.plan[0]);
+  for (int i = t; i < P; i += kThreads) {
+    ent[i] = p.plan[4 + i];
+    lst[i] = p.plan[4 + P + i];
   }
+  for (int i = t; i < P * kRows; i += kThreads) z[i] = 0.0f;
   __syncthreads();
-  auto again = [&](int i) {   // an earlier slot of the token has the expert
-    bool dup = false;
-    for (int j = i / k * k; j < i; ++j) dup |= sidx[j] == sidx[i];
-    return dup;
-  };
-  for (int i = t; i < P; i += 64 * kDownWaves)
-    if (sidx[i] >= 0 && !again(i)) atomicMin(&first[sidx[i]], i);
-  __syncthreads();
-  int n = 0;
-  for (int b = 0; b < P; b += 64 * kDownWaves) {
-    const int i = b + t;
-    const bool in = i < P && sidx[i] >= 0;
-    const bool dup = in && again(i);
-    const bool take = in && (dup || first[sidx[i]] == i);
-    const uint64_t m = __ballot(take);
-    if (lane == 0) cnt[wave] = __popcll(m);
-    __syncthreads();
-    int at = n;
-    for (int w = 0; w < kDownWaves; ++w) {
-      if (w < wave) at += cnt[w];
-      n += cnt[w];
-    }
-    if (take)
-      ent[at + __popcll(m & ((1ull << lane) - 1))] =
-          (uint16_t)(i | (dup ? 0x8000 : 0));
-    __syncthreads();
-  }
 
-  const int row = (lane & 15) / S, sp = (lane & 15) % S, g = lane >> 4;
-  const uint32_t piece = (uint32_t)(sp * 4 + g) * 16u;
-  const int h0 = blockIdx.x * R;
+  const int row = (lane & 15) >> 1;
+  const uint32_t piece = (uint32_t)((lane & 1) * 4 + (lane >> 4)) * 16u;
+  const int h0 = blockIdx.x * kRows;   // H % 8 == 0
   const uint32_t kbytes = (uint32_t)p.F / FMT::kValues * 16u;
   const uint32_t sbytes = (uint32_t)p.F / 32;
   const __amdgpu_buffer_rsrc_t ra =
       rsrc(p.a, (uint32_t)P * (uint32_t)p.F * 2u);
-  uint32_t rowoff[1], srow[1];
-  rowoff[0] = h0 + row < p.H ? (uint32_t)(h0 + row) * kbytes : kFar;
-  srow[0] = (uint32_t)(h0 + row) * sbytes;
-  f32x4_t sum[NS];
-#pragma unroll
-  for (int m = 0; m < NS; ++m) sum[m] = f32x4_t{};
-  const int nch = (int)((kbytes + 64 * S - 1) / (64 * S));
+  const uint32_t wrow[1] = {(uint32_t)(h0 + row) * kbytes};
+  const uint32_t srow[1] = {(uint32_t)(h0 + row) * sbytes};
+  const int nch = (int)((kbytes + 127) / 128);
   const int64_t total = (int64_t)n * nch;
-  int64_t at = total * wave / kDownWaves;
+  const int64_t at = total * wave / kDownWaves;
   const int64_t end = total * (wave + 1) / kDownWaves;
-  while (at < end) {
-    const int i = (int)(at / nch);
-    const int c0 = (int)(at - (int64_t)i * nch);
-    const int c1 = (int)min((int64_t)nch, end - (int64_t)i * nch);
-    const int en = ent[i], pr = en & 0x7fff;
-    const int e = __builtin_amdgcn_readfirstlane(sidx[pr]);
+  const int e0 = uniform((int)(at / nch)), e1 = uniform((int)(end / nch));
+  const int c0 = uniform((int)(at - (int64_t)e0 * nch));
+  const int cl = uniform((int)(end - (int64_t)e1 * nch));   // of entry e1
+  if (lane == 0) hent[wave] = at < end && c0 > 0 ? e0 : -1;
+  // last chunk (exclusive) of entry i in this wave's run
+  auto stop = [&](int i) { return i < e1 ? nch : i == e1 ? cl : 0; };
+
+  auto load = [&](B& b, int i, int c) {
+    const int cend = stop(i);
+    const int en = uniform(ent[cend ? i : 0]);
+    const int e = entry_expert(en), st = entry_start(en), m = entry_pairs(en);
     uint32_t xoff[NS];
-    bool used[NS];
 #pragma unroll
-    for (int m = 0; m < NS; ++m) {
-      const int tok = m * R + row;
-      int mine = -1;
-      if (en & 0x8000) {
-        if (tok == pr / k) mine = pr;
-      } else if (tok < p.T) {
-        for (int j = k - 1; j >= 0; --j)
-          if (sidx[tok * k + j] == e) mine = tok * k + j;
+    for (int q = 0; q < NS; ++q) {
+      const int j = B::load_place(lane, q);
+      xoff[q] = j < m ? (uint32_t)place_pair(lst[st + j]) *
+                            (uint32_t)p.F * 2u
+                      : kFar;
+    }
+    b.load(rsrc(p.w_dn + (int64_t)e * p.H * kbytes, (uint32_t)p.H * kbytes),
+           rsrc(p.s_dn + (int64_t)e * p.H * sbytes,
+                B::kMx ? (uint32_t)p.H * sbytes : 0u),
+           ra, wrow, srow, xoff, c, 1, cend, kbytes, piece, lane);
+  };
+  f32x4_t acc[1][NS];
+  auto clear = [&]() {
+#pragma unroll
+    for (int q = 0; q < NS; ++q) acc[0][q] = f32x4_t{};
+  };
+  clear();
+  const int hl = 2 * (lane >> 4) + (lane & 1);
+  auto finish = [&](int i) {
+    const int en = uniform(ent[i]);
+    const int st = entry_start(en), m = entry_pairs(en);
+    const bool mine = i > e0 || c0 == 0;
+#pragma unroll
+    for (int q = 0; q < NS; ++q) {
+      const float v = keep(acc[0][q], lane);
+      const int j = B::keep_place(lane, q);
+      if (mine) {
+        if (j < m) z[place_pair(lst[st + j]) * kRows + hl] = v;
+      } else if (j < kCols) {
+        head[(wave * kCols + j) * kRows + hl] = v;
       }
-      used[m] = mine >= 0;
-      xoff[m] = used[m] ? (uint32_t)mine * (uint32_t)p.F * 2u : kFar;
     }
-    const __amdgpu_buffer_rsrc_t rw =
-        rsrc(p.w_dn + (int64_t)e * p.H * kbytes, (uint32_t)p.H * kbytes);
-    const __amdgpu_buffer_rsrc_t rsc =
-        rsrc(p.s_dn ? p.s_dn + (int64_t)e * p.H * sbytes : nullptr,
-             p.s_dn ? (uint32_t)p.H * sbytes : 0u);
-    f32x4_t acc[1][NS];
-#pragma unroll
-    for (int m = 0; m < NS; ++m) acc[0][m] = f32x4_t{};
-    for (int c = c0; c < c1; c += U) {
-      Chunk<FMT, S, 1, NS, U> ch;
-      ch.load(rw, rsc, ra, rowoff, srow, xoff, c, 1, c1, kbytes, piece);
-      ch.mma(acc);
+    clear();
+  };
+  if (at < end) {
+    int li = e0, lc = c0;   // next to load
+    int ci = e0, cc = c0;   // next to multiply
+    auto fetch = [&](B& b) {
+      load(b, li, lc);
+      lc += U;
+      if (lc >= stop(li)) {
+        lc = 0;
+        ++li;
+      }
+    };
+    bool more = true;
+    auto step = [&](const B& b) {
+      b.mma(acc);
+      cc += U;
+      if (cc >= stop(ci)) {
+        finish(ci);
+        cc = 0;
+        ++ci;
+        more = stop(ci) > 0;
+      }
+    };
+    B b0, b1;
+    fetch(b0);
+    while (true) {
+      fetch(b1);
+      step(b0);
+      if (!more) break;
+      fetch(b0);
+      step(b1);
+      if (!more) break;
     }
-#pragma unroll
-    for (int m = 0; m < NS; ++m)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        sum[m][r] = used[m] ? sum[m][r] + acc[0][m][r] : sum[m][r];
-    at = (int64_t)i * nch + c1;
   }
-#pragma unroll
-  for (int m = 0; m < NS; ++m)
-    keep_diagonal<S>(sum[m], lane, red + (wave * NS + m) * kSet);
   __syncthreads();
-  for (int o = t; o < R * NS * R; o += 64 * kDownWaves) {
-    const int hl = o % R, tok = o / R;
-    const int h = h0 + hl;
-    if (h < p.H && tok < p.T) {
-      float v = 0.0f;
-      for (int w = 0; w < kDownWaves; ++w) {
-        const float* q = red + (w * NS + tok / R) * kSet +
-                         (hl * R + tok % R) * S;
-#pragma unroll
-        for (int s = 0; s < S; ++s) v += q[s];
-      }
-      if (p.res) v += bf16_to_f32(p.res[(int64_t)tok * p.H + h]);
-      p.y[(int64_t)tok * p.H + h] = (uint16_t)f32_to_bf16(v);
+  // the heads, in wave order; a thread owns one place and row of all entries
+  for (int o = t; o < kCols * kRows; o += kThreads) {
+    const int j = o / kRows, r = o % kRows;
+    for (int w = 0; w < kDownWaves; ++w) {
+      const int i = hent[w];
+      if (i < 0) continue;
+      const int en = ent[i];
+      if (j < entry_pairs(en))
+        z[place_pair(lst[entry_start(en) + j]) * kRows + r] +=
+            head[(w * kCols + j) * kRows + r];
     }
+  }
+  __syncthreads();
+  for (int o = t; o < p.T * kRows; o += kThreads) {
+    const int tok = o / kRows, r = o % kRows;
+    const int64_t at_y = (int64_t)tok * p.H + h0 + r;
+    float v = 0.0f;
+    for (int j = 0; j < p.k; ++j)
+      v = fmaf(p.w[tok * p.k + j], z[(tok * p.k + j) * kRows + r], v);
+    if (p.res) v += bf16_to_f32(p.res[at_y]);
+    p.y[at_y] = (uint16_t)f32_to_bf16(v);
   }
 }
 
 // ---- router logits -----------------------------------------------------------
-// A wave per expert and group of TT tokens: exact bf16 products summed in
-// float64 (16 bits below a float32 ulp over any order), rounded once.
-constexpr int kLogitTokens = 4;
-
+// A wave per expert and TT tokens: exact bf16 products summed in float64
+// (whose order moves the sum 2^-29 of a float32 rounding), rounded once.
+template <int TT>
 __global__ __launch_bounds__(256) void few_logits_kernel(
     const uint16_t* __restrict__ x, const uint16_t* __restrict__ w_r,
     const float* __restrict__ bias, int T, int H, int E,
     float* __restrict__ logits) {
+  constexpr int U = 4;   // 16-byte loads in flight per row
   const int lane = threadIdx.x & 63;
   const int e = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (e >= E) return;
-  const int t0 = blockIdx.y * kLogitTokens;
-  double acc[kLogitTokens] = {};
-  for (int h = lane * 8; h < H; h += 512) {
-    const uint4 w = *reinterpret_cast<const uint4*>(w_r + (int64_t)e * H + h);
-    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+  const int t0 = blockIdx.y * TT;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  double acc[TT] = {};
+  for (int h0 = lane * 8; h0 < H; h0 += 512 * U) {
+    uint4 w[U], v[U][TT];
 #pragma unroll
-    for (int m = 0; m < kLogitTokens; ++m) {
-      const uint4 v = t0 + m < T ? *reinterpret_cast<const uint4*>(
-                                       x + (int64_t)(t0 + m) * H + h)
-                                 : make_uint4(0, 0, 0, 0);
-      const uint32_t b[4] = {v.x, v.y, v.z, v.w};
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + 512 * u;
+      w[u] = h < H ? *reinterpret_cast<const uint4*>(w_r + (int64_t)e * H + h)
+                   : zero;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[m] = fma((double)bf16lo(a[i]), (double)bf16lo(b[i]), acc[m]);
-        acc[m] = fma((double)bf16hi(a[i]), (double)bf16hi(b[i]), acc[m]);
+      for (int m = 0; m < TT; ++m)
+        v[u][m] = h < H && t0 + m < T
+                      ? *reinterpret_cast<const uint4*>(
+                            x + (int64_t)(t0 + m) * H + h)
+                      : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t a[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+      for (int m = 0; m < TT; ++m) {
+        const uint32_t b[4] = {v[u][m].x, v[u][m].y, v[u][m].z, v[u][m].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[m] = fma((double)bf16lo(a[i]), (double)bf16lo(b[i]), acc[m]);
+          acc[m] = fma((double)bf16hi(a[i]), (double)bf16hi(b[i]), acc[m]);
+        }
       }
     }
   }
 #pragma unroll
-  for (int m = 0; m < kLogitTokens; ++m) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1)
-      acc[m] += __shfl_xor(acc[m], off, 64);
+  for (int m = 0; m < TT; ++m) {
+    const double v = lanes_sum<64>(acc[m]);
     if (lane == 0 && t0 + m < T)
       logits[(int64_t)(t0 + m) * E + e] =
-          (float)(bias ? acc[m] + (double)bias[e] : acc[m]);
+          (float)(bias ? v + (double)bias[e] : v);
   }
 }
 
-template <class FMT>
+// CT, NS: column sets; UG1 / UG4: chunks per batch of the gate/up product
+// with one and four waves per item, UD: of the down product
+template <class FMT, int CT, int NS, int UG1, int UG4, int UD>
 hipError_t launch_experts(const FewParams& p, hipStream_t stream) {
-  constexpr int S = 2, R = 16 / S;
   constexpr int RSF = FMT::kMfma > 1 ? 2 : 1;
+  const int P = p.T * p.k;
   {
     KernelScope ks("few_gate_up", stream);
-    const dim3 grid((unsigned)((p.F + R * RSF - 1) / (R * RSF)),
-                    (unsigned)std::min(p.T * p.k, p.E));
-    if (p.T <= R)
-      hipLaunchKernelGGL((few_gate_up_kernel<FMT, S, RSF, 1>), grid, dim3(256),
-                         0, stream, p);
+    // items if every pair reached an expert of its own
+    const int64_t items = (int64_t)std::min(P, p.E) *
+                          ((p.F + kRows * RSF - 1) / (kRows * RSF));
+    if (items < kWholeItems)
+      hipLaunchKernelGGL((few_gate_up_kernel<FMT, CT, NS, RSF, 4, UG4>),
+                         dim3((unsigned)std::min<int64_t>(items, 768)),
+                         dim3(256), 0, stream, p);
     else
-      hipLaunchKernelGGL((few_gate_up_kernel<FMT, S, RSF, 4>), grid, dim3(256),
-                         0, stream, p);
+      hipLaunchKernelGGL((few_gate_up_kernel<FMT, CT, NS, RSF, 1, UG1>),
+                         dim3(512), dim3(256), 0, stream, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   KernelScope ks("few_down", stream);
-  const dim3 grid((unsigned)((p.H + R - 1) / R));
-  const dim3 block(64 * kDownWaves);
-  if (p.T <= R)
-    hipLaunchKernelGGL((few_down_kernel<FMT, S, 1>), grid, block, 0, stream, p);
-  else if (p.T <= 2 * R)
-    hipLaunchKernelGGL((few_down_kernel<FMT, S, 2>), grid, block, 0, stream, p);
-  else if (p.T <= 4 * R)
-    hipLaunchKernelGGL((few_down_kernel<FMT, S, 4>), grid, block, 0, stream, p);
-  else
-    hipLaunchKernelGGL((few_down_kernel<FMT, S, 8>), grid, block, 0, stream, p);
+  auto* down = &few_down_kernel<FMT, CT, NS, UD>;
+  const size_t lds = ((size_t)P * kRows + kDownWaves * CT * NS * kRows +
+                      2 * P + kDownWaves) * 4;
+  if (lds > 65536) {   // (more than 1300 pairs)
+    const hipError_t e = hipFuncSetAttribute(
+        reinterpret_cast<const void*>(down),
+        hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(down, dim3((unsigned)(p.H / kRows)),
+                     dim3(64 * kDownWaves), lds, stream, p);
   return hipGetLastError();
+}
+
+struct FewWs {
+  size_t plan, logits, bytes;   // offsets; a is first
+};
+FewWs few_ws(int T, int F, int E, int k, bool router) {
+  FewWs w;
+  const size_t P = (size_t)T * k;
+  w.plan = mx4_align256(P * F * 2);
+  w.logits = w.plan + mx4_align256((4 + 2 * P) * 4);
+  w.bytes = w.logits + (router ? mx4_align256((size_t)T * E * 4) : 0);
+  return w;
 }
 
 }  // namespace
 
 size_t layer_few_ws_bytes(int T, int F, int E, int k, bool router) {
-  return mx4_align256((size_t)T * k * F * 2) +
-         (router ? mx4_align256((size_t)T * E * 4) : 0);
+  return few_ws(T, F, E, k, router).bytes;
 }
 
 hipError_t launch_layer_few(const LayerFew& a, hipStream_t stream) {
   if (a.T == 0) return hipSuccess;
   char* ws = static_cast<char*>(a.ws);
+  const FewWs w = few_ws(a.T, a.F, a.E, a.k, a.w_r != nullptr);
+  FewParams p{};
   if (a.w_r) {
-    float* logits = reinterpret_cast<float*>(
-        ws + mx4_align256((size_t)a.T * a.k * a.F * 2));
+    float* logits = reinterpret_cast<float*>(ws + w.logits);
     {
       KernelScope ks("few_logits", stream);
-      hipLaunchKernelGGL(few_logits_kernel,
-                         dim3((unsigned)((a.E + 3) / 4),
-                              (unsigned)((a.T + kLogitTokens - 1) /
-                                         kLogitTokens)),
-                         dim3(256), 0, stream,
-                         static_cast<const uint16_t*>(a.x),
-                         static_cast<const uint16_t*>(a.w_r), a.bias, a.T,
-                         a.H, a.E, logits);
+      const unsigned gx = (unsigned)((a.E + 3) / 4);
+      const uint16_t* x = static_cast<const uint16_t*>(a.x);
+      const uint16_t* w_r = static_cast<const uint16_t*>(a.w_r);
+      if (a.T == 1)
+        hipLaunchKernelGGL(few_logits_kernel<1>, dim3(gx), dim3(256), 0,
+                           stream, x, w_r, a.bias, a.T, a.H, a.E, logits);
+      else
+        hipLaunchKernelGGL(few_logits_kernel<4>,
+                           dim3(gx, (unsigned)((a.T + 3) / 4)), dim3(256), 0,
+                           stream, x, w_r, a.bias, a.T, a.H, a.E, logits);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
-    const hipError_t e =
-        launch_route_topk(logits, a.T, a.E, a.k, a.renorm, a.topk_idx,
-                          a.topk_w, a.status, stream);
-    if (e != hipSuccess) return e;
+    if (a.T <= kFuseTopk) {
+      p.logits = logits;
+    } else {
+      const hipError_t e =
+          launch_route_topk(logits, a.T, a.E, a.k, a.renorm, a.topk_idx,
+                            a.topk_w, a.status, stream);
+      if (e != hipSuccess) return e;
+    }
   }
-  FewParams p{};
   p.x = static_cast<const char*>(a.x);
   p.w_gu = static_cast<const char*>(a.w_gu);
   p.s_gu = a.s_gu;
@@ -549,7 +848,9 @@ hipError_t launch_layer_few(const LayerFew& a, hipStream_t stream) {
   p.s_dn = a.s_dn;
   p.idx = a.topk_idx;
   p.w = a.topk_w;
+  p.renorm = a.renorm;
   p.a = reinterpret_cast<uint16_t*>(ws);
+  p.plan = reinterpret_cast<int32_t*>(ws + w.plan);
   p.res = static_cast<const uint16_t*>(a.residual);
   p.y = static_cast<uint16_t*>(a.y);
   p.T = a.T;
@@ -558,8 +859,22 @@ hipError_t launch_layer_few(const LayerFew& a, hipStream_t stream) {
   p.E = a.E;
   p.k = a.k;
   p.status = a.status;
-  return a.s_gu ? launch_experts<FmtMx4>(p, stream)
-                : launch_experts<FmtBf16>(p, stream);
+  // Columns of an entry: twice the mean of an expert's pairs (never more than
+  // the tokens); the few experts that exceed it make another entry.  MXFP4,
+  // Qwen3-shaped, one call: 8 tokens 37.2 us with two columns, 39.2 with
+  // four, 42.4 with eight; 16 tokens 55.0 / 53.4 / 59.3; 32 tokens 82.7 /
+  // 75.2 / 80.2; 64 tokens 135 / 110.8 / 111.9.
+  const int most = std::min(a.T, std::max(1, 2 * a.T * a.k / a.E));
+  if (a.s_gu) {
+    return most <= 1 || a.T <= 2
+               ? launch_experts<FmtMx4, 2, 1, 2, 1, 3>(p, stream)
+           : most <= 4 ? launch_experts<FmtMx4, 2, 2, 2, 1, 3>(p, stream)
+           : most <= 8 ? launch_experts<FmtMx4, 8, 1, 2, 1, 3>(p, stream)
+                       : launch_experts<FmtMx4, 8, 2, 1, 1, 2>(p, stream);
+  }
+  return most <= 8    ? launch_experts<FmtBf16, 8, 1, 4, 2, 4>(p, stream)
+         : most <= 16 ? launch_experts<FmtBf16, 8, 2, 4, 2, 4>(p, stream)
+                      : launch_experts<FmtBf16, 8, 4, 2, 2, 2>(p, stream);
 }
 
 }  // namespace moe

@@ -153,15 +153,15 @@ def layer_few(x, w_gu, w_dn, topk_idx=None, topk_w=None, w_r=None, k=0,
             g, u = h[:F], h[F:]
             with np.errstate(over="ignore"):
                 sg = g / (1.0 + np.exp(-g))
-            a = w * sg * u
+            a = sg * u
             # slope of silu below 1.1; exponential and reciprocal 2^-18; one
             # bf16 rounding
-            ea = np.abs(w) * (1.1 * eh[:F] * np.abs(u) + np.abs(sg) * eh[F:] +
-                              1.1 * eh[:F] * eh[F:]) + 2.0 ** -18 * np.abs(a)
+            ea = 1.1 * eh[:F] * np.abs(u) + np.abs(sg) * eh[F:] + \
+                1.1 * eh[:F] * eh[F:] + 2.0 ** -18 * np.abs(a)
             ea = ea + 2.0 ** -8 * (np.abs(a) + ea)
-            y[t] += w_dn[e] @ a
-            bound[t] += np.abs(w_dn[e]) @ (ea + (F + 32) * u24 *
-                                           (np.abs(a) + ea))
+            y[t] += w * (w_dn[e] @ a)
+            bound[t] += np.abs(w) * (np.abs(w_dn[e]) @ (
+                ea + (F + 32) * u24 * (np.abs(a) + ea)))
     if residual is not None:
         y = y + _as_f64(residual)
     return {"y": y, "topk_idx": topk_idx, "topk_w": topk_w, "bound": bound}
