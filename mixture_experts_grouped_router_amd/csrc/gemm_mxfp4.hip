@@ -39,7 +39,7 @@ Mx4Ws carve(void* base, int E, int H, int F, int64_t rows, bool quant_x,
     return reinterpret_cast<uint8_t*>(q);
   };
   w.ts1 = reinterpret_cast<int32_t*>(take(tile_table_bytes(E, rows)));
-  w.ts2 = reinterpret_cast<int32_t*>(take(tile_table_bytes(E, rows)));
+  w.ts2 = reinterpret_cast<int32_t*>(take((size_t)(E + 1) * 4));
   w.aq = take((size_t)rows * F / 2);
   w.as = take(mx4_tile_bytes(rows, F));
   if (quant_x) w.xq = take((size_t)rows * H / 2);
@@ -81,28 +81,41 @@ hipError_t launch_mlp_fwd_mx4(int E, int H, int F, int64_t rows,
     err = launch_mx4_quant_rows(w_gu, ngu, H, w.guq, w.gus, stream, true);
     if (err == hipSuccess)
       err = launch_mx4_quant_rows(w_dn, ndn, F, w.dnq, w.dns, stream, true);
+    if (err != hipSuccess) return err;
     w_gu_q = w.guq;
     w_dn_q = w.dnq;
-  } else {
-    err = launch_mx4_scales_retile(w_gu_s, ngu, H, w.gus, stream);
-    if (err == hipSuccess)
-      err = launch_mx4_scales_retile(w_dn_s, ndn, F, w.dns, stream);
   }
-  if (err != hipSuccess) return err;
-  if (quant_x) {
-    err = launch_mx4_quant_rows(x_perm_bf16, rows, H, w.xq, w.xs, stream,
-                                true);
-    xq = w.xq;
-  } else {
-    err = launch_mx4_scales_retile(xs, rows, H, w.xs, stream);
-  }
-  if (err != hipSuccess) return err;
   const int tn1 = (F + BN / 2 - 1) / (BN / 2);
   const int tn2 = (H + BN - 1) / BN;
-  err = launch_tile_table(offsets, E, rows, tn1, w.ts1, status, stream);
-  if (err == hipSuccess)
-    err = launch_tile_table(offsets, E, rows, tn2, w.ts2, status, stream);
+  auto dwords = [](const uint8_t* q) {
+    return reinterpret_cast<const uint32_t*>(q);
+  };
+  Mx4Prepare pre{};
+  pre.offsets = offsets;
+  pre.E = E;
+  pre.H = H;
+  pre.F = F;
+  pre.unit = BM;
+  pre.tn1 = tn1;
+  pre.tn2 = tn2;
+  pre.rows = rows;
+  pre.gu_rows = ngu;
+  pre.dn_rows = ndn;
+  pre.ts1 = w.ts1;
+  pre.ts2 = w.ts2;
+  pre.mrec = w.ts1 + tile_rec_offset(E);
+  pre.status = status;
+  pre.x = quant_x ? x_perm_bf16 : nullptr;
+  pre.x_rm = dwords(quant_x ? nullptr : xs);
+  pre.gu_rm = dwords(quant_w ? nullptr : w_gu_s);
+  pre.dn_rm = dwords(quant_w ? nullptr : w_dn_s);
+  pre.xq = reinterpret_cast<uint32_t*>(w.xq);
+  pre.xs = reinterpret_cast<uint32_t*>(w.xs);
+  pre.gus = reinterpret_cast<uint32_t*>(w.gus);
+  pre.dns = reinterpret_cast<uint32_t*>(w.dns);
+  err = launch_mx4_prepare(pre, stream);
   if (err != hipSuccess) return err;
+  if (quant_x) xq = w.xq;
 
   Params p1{};
   p1.a = reinterpret_cast<const char*>(xq);
@@ -152,7 +165,7 @@ hipError_t launch_mlp_fwd_mx4(int E, int H, int F, int64_t rows,
   p2.E = E;
   p2.offsets = offsets;
   p2.tile_start = w.ts2;
-  p2.mrec = tile_records(w.ts2, E);
+  p2.mrec = tile_records(w.ts1, E);
   p2.tiles_n = tn2;
   p2.c = static_cast<uint16_t*>(z_perm);
   p2.ldc = H;

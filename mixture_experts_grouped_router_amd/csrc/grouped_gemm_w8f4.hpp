@@ -202,7 +202,7 @@ __global__ __launch_bounds__(kThreads8) void grouped_gemm_w8f4_kernel(
   using I1 = integral_constant<int, 1>;
   using I2 = integral_constant<int, 2>;
   using I3 = integral_constant<int, 3>;
-  using I6 = integral_constant<int, 6>;
+  using I4 = integral_constant<int, 4>;
   using I8 = integral_constant<int, 8>;
   // this wave's loads but the last four (B two steps ahead) have landed and
   // its reads of the step's buffers are done, then every wave's
@@ -224,29 +224,30 @@ __global__ __launch_bounds__(kThreads8) void grouped_gemm_w8f4_kernel(
     char* const an = buf(integral_constant<int, 2 * j + 3>{});
     char* const bn2 = buf(integral_constant<int, 2 * j + 4>{});
     issue_a(an, k + 1);
-    load_scales(min(k + 1, nk - 1));
     read(f1, a, b, 1);
     mma(I0{}, f0, I0{}, I8{});
-    sched_vmem_reads_mfma<4 + MI + NJ, 6, 8, 2>();
+    sched_vmem_reads_mfma<4, 6, 8, 1>();
     __builtin_amdgcn_sched_barrier(0);
+    // (the scales a slice later: 1640 -> 1597 us, Mixtral-shaped MLP)
+    load_scales(min(k + 1, nk - 1));
     read(f0, a, b, 2);
     mma(I1{}, f1, I0{}, I8{});
-    sched_reads_mfma<6, 8>();
+    sched_vmem_reads_mfma<MI + NJ, 6, 8, 1>();
     __builtin_amdgcn_sched_barrier(0);
     issue_b(bn2, k + 2);
     read(f1, a, b, 3);
     mma(I2{}, f0, I0{}, I8{});
     sched_vmem_reads_mfma<4, 6, 8, 1>();
     __builtin_amdgcn_sched_barrier(0);
-    // the last slice: six MFMAs, publish step k + 1, its first fragments
-    // under the last two
-    mma(I3{}, f1, I0{}, I6{});
+    // the last slice: four MFMAs, publish step k + 1, its first fragments
+    // under the last four (after six: 1597 us, after two: 1596, four: 1585)
+    mma(I3{}, f1, I0{}, I4{});
     __builtin_amdgcn_sched_barrier(0);
     publish();
     read(f0, an, bn, 0);
-    mma(I3{}, f1, I6{}, I8{});
+    mma(I3{}, f1, I4{}, I8{});
     take_scales();
-    sched_reads_mfma<6, 2>();
+    sched_reads_mfma<6, 3>();
     __builtin_amdgcn_sched_barrier(0);
   };
   auto rstep_idle = [&](auto jc) {

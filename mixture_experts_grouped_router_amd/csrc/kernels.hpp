@@ -232,16 +232,30 @@ hipError_t launch_layernorm_bwd(const void* dy, const void* x, bool f32,
                                 void* ws, hipStream_t stream);
 
 // MXFP4 (mxfp4_quant.hip).  tiled: scales in the layout of the 4-bit GEMM
-// (mx4_tile_off), else row-major [rows][cols / 32]; cols % 32 == 0 (tiled and
-// retile: % 128)
+// (mx4_tile_off), else row-major [rows][cols / 32]; cols % 32 == 0 (tiled:
+// % 128)
 hipError_t launch_mx4_quant_rows(const void* src, int64_t rows, int64_t cols,
                                  uint8_t* codes, uint8_t* scales,
                                  hipStream_t stream, bool tiled = false);
 hipError_t launch_mx4_dequant(const uint8_t* codes, const uint8_t* scales,
                               int64_t values, void* dst, hipStream_t stream);
-hipError_t launch_mx4_scales_retile(const uint8_t* src, int64_t rows,
-                                    int64_t k, uint8_t* dst,
-                                    hipStream_t stream);
+// what the 4-bit GEMMs need ahead of them: tile tables of both (M tiles of
+// `unit` rows, tn1 / tn2 N tiles) with shared M-tile records, x_perm
+// quantised (x) or its row-major scales rearranged (x_rm), the weights'
+// row-major scales rearranged (gu_rm, dn_rm; null: already in the layout)
+struct Mx4Prepare {
+  const int32_t* offsets;
+  int E, H, F, unit, tn1, tn2;
+  int64_t rows, gu_rows, dn_rows;
+  int32_t *ts1, *ts2, *mrec, *status;
+  const void* x;
+  const uint32_t *x_rm, *gu_rm, *dn_rm;
+  uint32_t *xq, *xs, *gus, *dns;
+  // set by launch_mx4_prepare
+  uint32_t nks_h, nks_f;
+  int64_t x_items, x_blocks, gu_items, gu_blocks, dn_items;
+};
+hipError_t launch_mx4_prepare(Mx4Prepare p, hipStream_t stream);
 
 // MXFP4 grouped MLP forward (gemm_mxfp4.hip); quant_x / quant_w: the
 // activations / weights are quantised inside the call

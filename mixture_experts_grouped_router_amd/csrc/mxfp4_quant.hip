@@ -77,17 +77,17 @@ __global__ __launch_bounds__(256) void mx4_dequant_kernel(
   }
 }
 
-// Rows into the GEMM scale layout: a work-group covers 32 rows x 256 values
+// Rows into the GEMM scale layout: work-group b covers 32 rows x 256 values
 // (one K step); lane l % 32 of a half-wave takes the row's chunk l % 32, so
 // a row's 512 bytes are one run.  The 32 x 8 scale bytes are gathered in LDS
-// and leave as 256 contiguous bytes.  Blocks past K or past the last row
-// carry the scale 1 (their codes read as zeros in the GEMM).
-__global__ __launch_bounds__(256) void mx4_rows_tiled_kernel(
+// (64 dwords) and leave as 256 contiguous bytes.  Blocks past K or past the
+// last row carry the scale 1 (their codes read as zeros in the GEMM).
+__device__ __forceinline__ void rows_tiled_block(
     const uint4* __restrict__ src, int64_t rows, int cols8, uint32_t nks,
-    uint32_t* __restrict__ codes, uint32_t* __restrict__ scales) {
-  __shared__ uint32_t sc[64];
-  const int64_t g = blockIdx.x / nks;
-  const uint32_t step = (uint32_t)(blockIdx.x - g * nks);
+    uint32_t* __restrict__ codes, uint32_t* __restrict__ scales, int64_t b,
+    uint32_t* sc) {
+  const int64_t g = b / nks;
+  const uint32_t step = (uint32_t)(b - g * nks);
   const int t = threadIdx.x;
   const int ch = t & 31, c = (int)step * 32 + ch;
   uint4 v[4];
@@ -114,13 +114,19 @@ __global__ __launch_bounds__(256) void mx4_rows_tiled_kernel(
   if (t < 64) scales[(g * nks + step) * 64 + t] = sc[t];
 }
 
-// row-major scales [rows][k / 32] (k % 128 == 0: whole dwords) -> GEMM
-// layout; a thread takes one row's eight blocks of a K step
-__global__ __launch_bounds__(256) void mx4_retile_kernel(
-    const uint32_t* __restrict__ src, int64_t rows, uint32_t k128,
-    uint32_t nks, int64_t n, uint32_t* __restrict__ dst) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;   // n = row groups x K steps x 32
+__global__ __launch_bounds__(256) void mx4_rows_tiled_kernel(
+    const uint4* __restrict__ src, int64_t rows, int cols8, uint32_t nks,
+    uint32_t* __restrict__ codes, uint32_t* __restrict__ scales) {
+  __shared__ uint32_t sc[64];
+  rows_tiled_block(src, rows, cols8, nks, codes, scales, blockIdx.x, sc);
+}
+
+// row-major scales [rows][4 k128] -> GEMM layout; thread i (of row groups x
+// K steps x 32) takes one row's eight blocks of a K step
+__device__ __forceinline__ void retile_one(const uint32_t* __restrict__ src,
+                                           int64_t rows, uint32_t k128,
+                                           uint32_t nks, int64_t i,
+                                           uint32_t* __restrict__ dst) {
   const int64_t gs = i >> 5;
   const int r = (int)(i & 31);
   const int64_t g = gs / nks;
@@ -135,6 +141,69 @@ __global__ __launch_bounds__(256) void mx4_retile_kernel(
   // bytes 0, 2 of a and b are the even blocks
   dst[gs * 64 + r] = __builtin_amdgcn_perm(b, a, 0x06040200u);
   dst[gs * 64 + 32 + r] = __builtin_amdgcn_perm(b, a, 0x07050301u);
+}
+
+// Everything ahead of the 4-bit GEMMs in one launch (five launches of a few
+// microseconds each cost a short prompt more than their work): work-group 0
+// makes the tile tables, the next ones quantise x (or rearrange its scales),
+// the others rearrange the weights' scales.
+__global__ __launch_bounds__(256) void mx4_prepare_kernel(Mx4Prepare p) {
+  __shared__ uint32_t sc[64];
+  const int t = threadIdx.x;
+  int64_t b = blockIdx.x;
+  if (b == 0) {
+    // prefix of the M tiles, thread t owning experts 4t .. 4t+3; the tables
+    // of both GEMMs are its multiples and share the M-tile records
+    const bool ok = seg_offsets_ok(p.offsets, p.E, p.rows, t, p.status);
+    int32_t n[4], own = 0, total;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = 4 * t + i;
+      n[i] = ok && e < p.E
+                 ? (p.offsets[e + 1] - p.offsets[e] + p.unit - 1) / p.unit
+                 : 0;
+      own += n[i];
+    }
+    int32_t at = block_exclusive_scan_256(own, &total);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = 4 * t + i;
+      if (e < p.E) {
+        p.ts1[e] = at * p.tn1;
+        p.ts2[e] = at * p.tn2;
+        if (n[i] > 0) {
+          const int o = p.offsets[e];
+          const int4 rec = make_int4(e, at, o, p.offsets[e + 1] - o);
+          for (int k = 0; k < n[i]; ++k)
+            reinterpret_cast<int4*>(p.mrec)[at + k] = rec;
+        }
+      }
+      at += n[i];
+    }
+    if (t == 0) {
+      p.ts1[p.E] = total * p.tn1;
+      p.ts2[p.E] = total * p.tn2;
+    }
+    return;
+  }
+  b -= 1;
+  if (b < p.x_blocks) {
+    if (p.x)
+      rows_tiled_block(static_cast<const uint4*>(p.x), p.rows, p.H / 8,
+                       p.nks_h, p.xq, p.xs, b, sc);
+    else if (b * 256 + t < p.x_items)
+      retile_one(p.x_rm, p.rows, p.H / 128, p.nks_h, b * 256 + t, p.xs);
+    return;
+  }
+  b -= p.x_blocks;
+  if (b < p.gu_blocks) {
+    if (b * 256 + t < p.gu_items)
+      retile_one(p.gu_rm, p.gu_rows, p.H / 128, p.nks_h, b * 256 + t, p.gus);
+    return;
+  }
+  b -= p.gu_blocks;
+  if (b * 256 + t < p.dn_items)
+    retile_one(p.dn_rm, p.dn_rows, p.F / 128, p.nks_f, b * 256 + t, p.dns);
 }
 
 unsigned stream_grid(int64_t n) {
@@ -178,18 +247,23 @@ hipError_t launch_mx4_dequant(const uint8_t* codes, const uint8_t* scales,
   return hipGetLastError();
 }
 
-hipError_t launch_mx4_scales_retile(const uint8_t* src, int64_t rows,
-                                    int64_t k, uint8_t* dst,
-                                    hipStream_t stream) {
-  if (rows == 0) return hipSuccess;
-  KernelScope ks("mxfp4_scales_retile", stream);
-  const uint32_t nks = (uint32_t)((k + 255) / 256);
-  const int64_t n = (rows + 31) / 32 * 32 * nks;
-  hipLaunchKernelGGL(mx4_retile_kernel, dim3((unsigned)((n + 255) / 256)),
-                     dim3(256), 0, stream,
-                     reinterpret_cast<const uint32_t*>(src), rows,
-                     (uint32_t)(k / 128), nks, n,
-                     reinterpret_cast<uint32_t*>(dst));
+hipError_t launch_mx4_prepare(Mx4Prepare p, hipStream_t stream) {
+  KernelScope ks("mxfp4_prepare", stream);
+  auto items = [](int64_t rows, uint32_t nks) {
+    return (rows + 31) / 32 * 32 * (int64_t)nks;
+  };
+  p.nks_h = (uint32_t)((p.H + 255) / 256);
+  p.nks_f = (uint32_t)((p.F + 255) / 256);
+  p.x_items = items(p.rows, p.nks_h);
+  p.x_blocks = p.x ? (p.rows + 31) / 32 * (int64_t)p.nks_h
+                   : (p.x_items + 255) / 256;
+  p.gu_items = p.gu_rm ? items(p.gu_rows, p.nks_h) : 0;
+  p.gu_blocks = (p.gu_items + 255) / 256;
+  p.dn_items = p.dn_rm ? items(p.dn_rows, p.nks_f) : 0;
+  const int64_t grid =
+      1 + p.x_blocks + p.gu_blocks + (p.dn_items + 255) / 256;
+  hipLaunchKernelGGL(mx4_prepare_kernel, dim3((unsigned)grid), dim3(256), 0,
+                     stream, p);
   return hipGetLastError();
 }
 
