@@ -18,7 +18,15 @@ using namespace gg;
 
 namespace {
 
+// Rows per expert, on average, up to which the few-rows kernels run
+#ifndef FEWROWS
+#define FEWROWS 8
+#endif
+constexpr int kFewRows = FEWROWS;
+bool few_rows(int E, int64_t rows) { return rows <= (int64_t)kFewRows * E; }
+
 struct Mx4Ws {
+  void* ent;   // few rows: entries
   int32_t* ts1;
   int32_t* ts2;
   uint8_t *aq, *as;     // A codes [rows, F / 2], scales (GEMM layout)
@@ -38,6 +46,7 @@ Mx4Ws carve(void* base, int E, int H, int F, int64_t rows, bool quant_x,
     off += align256(n);
     return reinterpret_cast<uint8_t*>(q);
   };
+  if (few_rows(E, rows)) w.ent = take(mx4_few_rows_entries_bytes(E, rows));
   w.ts1 = reinterpret_cast<int32_t*>(take(tile_table_bytes(E, rows)));
   w.ts2 = reinterpret_cast<int32_t*>(take((size_t)(E + 1) * 4));
   w.aq = take((size_t)rows * F / 2);
@@ -77,13 +86,37 @@ hipError_t launch_mlp_fwd_mx4(int E, int H, int F, int64_t rows,
   const Mx4Ws w = carve(ws, E, H, F, rows, quant_x, quant_w);
   hipError_t err;
   const int64_t ngu = (int64_t)E * 2 * F, ndn = (int64_t)E * H;   // rows
+  // (the saves are outputs of the tiled GEMM's epilogue)
+  const bool few = few_rows(E, rows) && !h1_save && !a_save;
   if (quant_w) {
-    err = launch_mx4_quant_rows(w_gu, ngu, H, w.guq, w.gus, stream, true);
+    err = launch_mx4_quant_rows(w_gu, ngu, H, w.guq, w.gus, stream, !few);
     if (err == hipSuccess)
-      err = launch_mx4_quant_rows(w_dn, ndn, F, w.dnq, w.dns, stream, true);
+      err = launch_mx4_quant_rows(w_dn, ndn, F, w.dnq, w.dns, stream, !few);
     if (err != hipSuccess) return err;
     w_gu_q = w.guq;
     w_dn_q = w.dnq;
+  }
+  if (few) {
+    Mx4FewRows f{};
+    f.H = H;
+    f.F = F;
+    f.cols = rows <= 5 * (int64_t)E ? 8 : 16;
+    f.rows = rows;
+    f.entries = w.ent;
+    f.xq = quant_x ? w.xq : xq;
+    f.xs = quant_x ? w.xs : xs;
+    f.gu_q = w_gu_q;
+    f.gu_s = quant_w ? w.gus : w_gu_s;
+    f.dn_q = w_dn_q;
+    f.dn_s = quant_w ? w.dns : w_dn_s;
+    f.w_perm = w_perm;
+    f.aq = w.aq;
+    f.as = w.as;
+    f.z = z_perm;
+    err = launch_mx4_entries(offsets, E, rows, f.cols, w.ent,
+                             quant_x ? x_perm_bf16 : nullptr, H, w.xq, w.xs,
+                             status, stream);
+    return err == hipSuccess ? launch_mx4_few_rows(f, stream) : err;
   }
   const int tn1 = (F + BN / 2 - 1) / (BN / 2);
   const int tn2 = (H + BN - 1) / BN;

@@ -257,6 +257,25 @@ struct Mx4Prepare {
 };
 hipError_t launch_mx4_prepare(Mx4Prepare p, hipStream_t stream);
 
+// the MXFP4 MLP for few rows per expert (mxfp4_few_rows.hip).  entries: an
+// int4 holding their number, then {expert, first row, rows (<= cols), 0}
+// each, from launch_mx4_entries, which also quantises x (bf16, or null)
+struct Mx4FewRows {
+  int H, F, cols;   // cols: 8 or 16
+  int64_t rows;
+  const void* entries;
+  const uint8_t *xq, *xs, *gu_q, *gu_s, *dn_q, *dn_s;   // row-major scales
+  const float* w_perm;
+  uint8_t *aq, *as;
+  void* z;
+};
+size_t mx4_few_rows_entries_bytes(int E, int64_t rows);
+hipError_t launch_mx4_entries(const int32_t* offsets, int E, int64_t rows,
+                              int cols, void* entries, const void* x, int H,
+                              uint8_t* xq, uint8_t* xs, int32_t* status,
+                              hipStream_t stream);
+hipError_t launch_mx4_few_rows(const Mx4FewRows& a, hipStream_t stream);
+
 // MXFP4 grouped MLP forward (gemm_mxfp4.hip); quant_x / quant_w: the
 // activations / weights are quantised inside the call
 size_t mlp_fwd_mx4_ws_bytes(int E, int H, int F, int64_t rows, bool quant_x,

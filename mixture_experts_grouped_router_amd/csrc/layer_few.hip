@@ -33,6 +33,7 @@
 #include <algorithm>
 
 #include "common.hpp"
+#include "few_tile.hpp"
 #include "kernels.hpp"
 #include "lanes.hpp"
 #include "mxfp4.hpp"
@@ -41,15 +42,8 @@
 namespace moe {
 namespace {
 
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
-
 constexpr int32_t kDevErrExpertId = 1;   // include/moe.h MOE_DEVERR_*
 constexpr int32_t kDevErrLogits = 3;
-constexpr uint32_t kFar = 0xfffffff0u;   // an offset no descriptor covers
-constexpr int kBufFlags = 0x00020000;    // raw buffer, 32-bit data format
-constexpr int kRows = 8;                 // weight rows of a load, tokens of a
-                                         // column set
 constexpr int kMaxPairs = kFewMaxTokens * 32;   // MOE_MAX_TOPK
 constexpr int kFuseTopk = 4;             // tokens whose experts every
                                          // work-group picks for itself
@@ -78,23 +72,9 @@ struct FewParams {
   int32_t* status;
 };
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p,
-                                                       uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0,
-                                           (int)bytes, kBufFlags);
-}
-__device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t r,
-                                        uint32_t at) {
-  return __builtin_bit_cast(uint4,
-                            __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
-}
 __device__ __forceinline__ bf16x8_t as_bf16x8(const uint4 v) {
   return __builtin_bit_cast(bf16x8_t, v);
 }
-__device__ __forceinline__ int uniform(int v) {
-  return __builtin_amdgcn_readfirstlane(v);
-}
-
 // Weights of one format: K values of a 16-byte piece, MFMAs per piece, and
 // the piece as MFMA operands.
 struct FmtBf16 {
@@ -225,19 +205,6 @@ struct Batch {
     }
   }
 };
-
-// The kept products of a 16 x 16 result: lane l holds rows 4 (l / 16) + r of
-// column c = l % 16, of which those with row % 2 = c % 2 count; the other
-// half of K is the neighbouring lane's.  Returns the sum of weight row
-// 2 (l / 16) + c % 2 and the token of column c / 2.
-__device__ __forceinline__ float keep(const f32x4_t& acc, int lane) {
-  const bool odd = lane & 1;
-  float t0 = odd ? acc[1] : acc[0];
-  float t1 = odd ? acc[3] : acc[2];
-  t0 += dpp_f<kDppXor1>(t0);
-  t1 += dpp_f<kDppXor1>(t1);
-  return odd ? t1 : t0;
-}
 
 // ---- plan --------------------------------------------------------------------
 // An entry: expert, first place in the pair list, pairs (at most 32).

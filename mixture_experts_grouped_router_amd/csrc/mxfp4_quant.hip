@@ -30,13 +30,16 @@ __device__ __forceinline__ int quad_exp(const uint4 v) {
   return mx4_exp_from_bf16_amax(a);
 }
 
-// n chunks of 8 values (a multiple of 4: quads are whole)
-__global__ __launch_bounds__(256) void mx4_rows_kernel(
-    const uint4* __restrict__ src, int64_t n, uint32_t* __restrict__ codes,
-    uint8_t* __restrict__ scales) {
-  const int64_t S = (int64_t)gridDim.x * 256;
-  for (int64_t c0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
-       c0 - threadIdx.x % 4 < n; c0 += kUnroll * S) {
+// n chunks of 8 values (a multiple of 4: quads are whole), by work-groups b
+// of nblocks
+__device__ __forceinline__ void rows_blocks(const uint4* __restrict__ src,
+                                            int64_t n,
+                                            uint32_t* __restrict__ codes,
+                                            uint8_t* __restrict__ scales,
+                                            int64_t b, int64_t nblocks) {
+  const int64_t S = nblocks * 256;
+  for (int64_t c0 = b * 256 + threadIdx.x; c0 - threadIdx.x % 4 < n;
+       c0 += kUnroll * S) {
     uint4 v[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -53,6 +56,39 @@ __global__ __launch_bounds__(256) void mx4_rows_kernel(
       }
     }
   }
+}
+
+__global__ __launch_bounds__(256) void mx4_rows_kernel(
+    const uint4* __restrict__ src, int64_t n, uint32_t* __restrict__ codes,
+    uint8_t* __restrict__ scales) {
+  rows_blocks(src, n, codes, scales, blockIdx.x, gridDim.x);
+}
+
+// Work-group 0: the entries of the few-rows MLP; the others quantise x.
+__global__ __launch_bounds__(256) void mx4_entries_kernel(
+    const int32_t* __restrict__ offsets, int E, int64_t rows, int cols,
+    int4* __restrict__ ent, const uint4* __restrict__ x, int64_t n,
+    uint32_t* __restrict__ xq, uint8_t* __restrict__ xs, int32_t* status) {
+  if (blockIdx.x > 0) {
+    rows_blocks(x, n, xq, xs, blockIdx.x - 1, gridDim.x - 1);
+    return;
+  }
+  const int t = threadIdx.x;
+  const bool ok = seg_offsets_ok(offsets, E, rows, t, status);
+  int own = 0, total, o[5];
+#pragma unroll
+  for (int i = 0; i < 5; ++i)
+    o[i] = ok && 4 * t + i <= E ? offsets[4 * t + i] : 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (ok && 4 * t + i < E) own += (o[i + 1] - o[i] + cols - 1) / cols;
+  int at = block_exclusive_scan_256(own, &total);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (ok && 4 * t + i < E)
+      for (int r = o[i]; r < o[i + 1]; r += cols)
+        ent[1 + at++] = make_int4(4 * t + i, r, min(cols, o[i + 1] - r), 0);
+  if (t == 0) ent[0] = make_int4(total, 0, 0, 0);
 }
 
 __global__ __launch_bounds__(256) void mx4_dequant_kernel(
@@ -244,6 +280,20 @@ hipError_t launch_mx4_dequant(const uint8_t* codes, const uint8_t* scales,
   hipLaunchKernelGGL(mx4_dequant_kernel, dim3(stream_grid(n)), dim3(256), 0,
                      stream, reinterpret_cast<const uint32_t*>(codes), scales,
                      n, static_cast<uint4*>(dst));
+  return hipGetLastError();
+}
+
+hipError_t launch_mx4_entries(const int32_t* offsets, int E, int64_t rows,
+                              int cols, void* entries, const void* x, int H,
+                              uint8_t* xq, uint8_t* xs, int32_t* status,
+                              hipStream_t stream) {
+  KernelScope ks("mxfp4_entries", stream);
+  const int64_t n = x ? rows * H / 8 : 0;
+  hipLaunchKernelGGL(mx4_entries_kernel, dim3(1 + (n ? stream_grid(n) : 0)),
+                     dim3(256), 0, stream, offsets, E, rows, cols,
+                     static_cast<int4*>(entries),
+                     static_cast<const uint4*>(x), n,
+                     reinterpret_cast<uint32_t*>(xq), xs, status);
   return hipGetLastError();
 }
 

@@ -156,6 +156,44 @@ def test_mlp(m, sizes, H, F):
     assert torch.equal(z[0], z[1]) and torch.equal(z[0], z[2])
 
 
+# at most eight rows per expert on average: the kernels for few rows, with
+# entries of up to eight (five and fewer) or sixteen rows, experts that need
+# several entries, one expert, every K tail
+FEW = [([1], 128, 128), ([5, 0, 1, 12], 256, 384), ([8] * 16, 384, 256),
+       ([1] * 40, 512, 640), ([64] + [0] * 15, 1280, 128),
+       ([0, 3, 0, 61, 0, 0, 0, 0], 128, 1408), ([9, 16, 17, 1, 0, 5, 7, 8],
+                                                2048, 768),
+       ([2, 40, 0, 0, 0, 0, 1, 0], 640, 384), ([7], 256, 128), ([8], 128, 256)]
+
+
+@pytest.mark.parametrize("sizes,H,F", FEW)
+def test_mlp_few_rows(m, sizes, H, F):
+    d = make(sizes, H, F, H + F)
+    ref = oracle(d)
+    z = [run(m, d, mode)["z"] for mode in ("bf16 weights", "weight codes",
+                                           "codes")]
+    assert O.rel_err(host(z[0]), ref["z"]) < 5e-3
+    assert torch.equal(z[0], z[1]) and torch.equal(z[0], z[2])
+    # without a weight; and the tiled kernels, which run with the saves
+    a = run(m, d, "codes", weighted=False)["z"]
+    assert O.rel_err(host(a), oracle(d, weighted=False)["z"]) < 5e-3
+    b = run(m, d, "codes", weighted=False, save=True)["z"]
+    assert O.rel_err(host(a), host(b)) < 5e-3
+
+
+def test_mlp_rows_behind_the_last_are_untouched(m):
+    """Outputs of a larger buffer past the rows keep what they held."""
+    for sizes in ([3, 1, 9, 2], [200, 30]):
+        d = make(sizes, 256, 128, 6)
+        rows = sum(sizes)
+        buf = torch.full((rows + 40, 256), 7.0, dtype=torch.bfloat16,
+                         device="cuda")
+        z = run(m, d, "codes", out=buf[:rows])["z"]
+        assert z.data_ptr() == buf.data_ptr()
+        assert bool((buf[rows:] == 7.0).all())
+        assert O.rel_err(host(z), oracle(d)["z"]) < 5e-3
+
+
 def test_mlp_saves_and_no_weight(m):
     d = make([50, 0, 3], 256, 256, 2)
     ref = oracle(d, weighted=False)
@@ -201,8 +239,9 @@ def test_operand_layout_exactly(m, H):
 def test_mlp_empty_and_bad_offsets(m):
     d = make([0, 0], 128, 128, 1)
     assert run(m, d, "weight codes")["z"].shape == (0, 128)
-    d = make([4, 4], 128, 128, 1)
-    d["off"][1] = 9
-    run(m, d, "weight codes")
-    assert m.check_device_status() == 2
-    assert m.check_device_status() == 0
+    for sizes in ([4, 4], [40, 4]):
+        d = make(sizes, 128, 128, 1)
+        d["off"][1] = 60
+        run(m, d, "weight codes")
+        assert m.check_device_status() == 2
+        assert m.check_device_status() == 0
