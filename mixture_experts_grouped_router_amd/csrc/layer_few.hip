@@ -80,14 +80,18 @@ __device__ __forceinline__ bf16x8_t as_bf16x8(const uint4 v) {
 struct FmtBf16 {
   static constexpr int kValues = 8;
   static constexpr int kMfma = 1;
+  static constexpr bool kScaleWords = false;
   static __device__ __forceinline__ void widen(const uint4 c, uint32_t,
                                                bf16x8_t (&o)[1]) {
     o[0] = as_bf16x8(c);
   }
 };
+// kWords: K % 128 == 0 and scales at dword boundaries
+template <bool kWords>
 struct FmtMx4 {
   static constexpr int kValues = 32;
   static constexpr int kMfma = 4;
+  static constexpr bool kScaleWords = kWords;
   static __device__ __forceinline__ void widen(const uint4 c, uint32_t scale,
                                                bf16x8_t (&o)[4]) {
     const float s = mx4_scale_of(scale);
@@ -122,14 +126,22 @@ __device__ __forceinline__ bf16x8_t rotate_row(const uint4 v) {
 // of a piece in one load, lane 8 t + 2 m + s of 16 holding token t's half s
 // for MFMA m, and rotate them into the columns 8 t + s; the other columns
 // multiply whatever comes along and are not kept.
+//
+// MXFP4 scales: a chunk has eight scale bytes per weight row.  Read byte by
+// byte by the lanes that need them they cost as many loads and half as many
+// cache lines again as the weights (a fifth of the time), so a batch of up
+// to four chunks loads one dword per lane, lane 8 r + d the d-th of row r,
+// and the lanes fetch their bytes from each other.
 template <class FMT, int CT, int RS, int NS, int U>
 struct Batch {
   static constexpr bool kMx = FMT::kMfma > 1;
+  static constexpr bool kWords = FMT::kScaleWords;
+  static_assert(!kWords || U <= 4, "a dword per lane");
   static_assert(CT == 8 || (CT == 2 && FMT::kMfma == 4), "column sets");
   static constexpr int kX = CT == 8 ? FMT::kMfma : 1;
   static constexpr int kCols = NS * CT;
   uint4 wv[U][RS];
-  uint32_t sv[U][RS];
+  uint32_t sv[kWords ? 1 : U][RS];
   uint4 xv[U][NS][kX];
   // the lane's token of column set q, to load (a negative one: none) or to
   // keep results of
@@ -139,28 +151,35 @@ struct Batch {
   static __device__ __forceinline__ int keep_place(int lane, int q) {
     return CT == 8 || (lane & 6) == 0 ? load_place(lane, q) : kFewMaxTokens;
   }
-  // chunks c0 + u cstep below cend; row: the lane's byte offset in each row
-  // set (kFar: none), srow its scale offset, xoff: the lane's token (kFar:
-  // none); piece: the lane's bytes of a chunk
+  // chunks c0 + u below cend; row: the lane's byte offset in each row set
+  // (kFar: none), srow: its scale offset (kWords: of row lane / 8 of the
+  // set), xoff: the lane's token (kFar: none); piece: the lane's bytes of a
+  // chunk
   __device__ __forceinline__ void load(
       __amdgpu_buffer_rsrc_t rw, __amdgpu_buffer_rsrc_t rs,
       __amdgpu_buffer_rsrc_t rx, const uint32_t (&row)[RS],
       const uint32_t (&srow)[RS], const uint32_t (&xoff)[NS], int c0,
-      int cstep, int cend, uint32_t kbytes, uint32_t piece, int lane) {
+      int cend, uint32_t kbytes, uint32_t piece, int lane) {
+    if constexpr (kWords) {
+      const uint32_t sb = (uint32_t)c0 * 8u + (lane & 7) * 4u;
+      const bool in = (lane & 7) < 2 * U && c0 < cend && sb < kbytes / 16;
+#pragma unroll
+      for (int i = 0; i < RS; ++i)
+        sv[0][i] = __builtin_amdgcn_raw_buffer_load_b32(
+            rs, in && srow[i] != kFar ? srow[i] + sb : kFar, 0, 0);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = c0 + u * cstep;
+      const int c = c0 + u;
       const uint32_t kb = (uint32_t)c * 128u + piece;
       const bool in = c < cend && kb < kbytes;
 #pragma unroll
       for (int i = 0; i < RS; ++i) {
         const bool ok = in && row[i] != kFar;
         wv[u][i] = load16(rw, ok ? row[i] + kb : kFar);
-        if constexpr (kMx)
+        if constexpr (kMx && !kWords)
           sv[u][i] = __builtin_amdgcn_raw_buffer_load_b8(
               rs, ok ? srow[i] + (kb >> 4) : kFar, 0, 0);
-        else
-          sv[u][i] = 0;
       }
       // the piece's kValues activations, 16 bytes each eight
       const uint32_t xb = kb * (uint32_t)(2 * FMT::kValues / 16) +
@@ -174,7 +193,21 @@ struct Batch {
                                                : kFar);
     }
   }
-  __device__ __forceinline__ void mma(f32x4_t (&acc)[RS][NS]) const {
+  // the lane's scale byte of chunk u, row set i
+  __device__ __forceinline__ uint32_t scale(int u, int i, int lane) const {
+    if constexpr (!kMx) {
+      return 0;
+    } else if constexpr (!kWords) {
+      return sv[u][i];
+    } else {
+      const int from = ((lane & 15) >> 1) * 8 + 2 * u + (lane & 1);
+      const uint32_t w =
+          (uint32_t)__builtin_amdgcn_ds_bpermute(from * 4, (int)sv[0][i]);
+      return w >> (8 * (lane >> 4)) & 0xffu;
+    }
+  }
+  __device__ __forceinline__ void mma(f32x4_t (&acc)[RS][NS],
+                                      int lane) const {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       bf16x8_t x[NS][FMT::kMfma];
@@ -194,7 +227,7 @@ struct Batch {
 #pragma unroll
       for (int i = 0; i < RS; ++i) {
         bf16x8_t o[FMT::kMfma];
-        FMT::widen(wv[u][i], sv[u][i], o);
+        FMT::widen(wv[u][i], scale(u, i, lane), o);
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
@@ -413,6 +446,7 @@ __global__ __launch_bounds__(256) void few_gate_up_kernel(FewParams p) {
   const int i1 = uniform((int)(N * (me + 1) / W));
   if (i0 >= i1) return;   // KS = 4: the whole work-group
   const int cw = KS == 1 ? 0 : wave;
+  const int srow_of = B::kWords ? lane >> 3 : row;   // row of its scales
 
   auto load = [&](B& b, int it, int bt) {
     const bool real = it < i1;
@@ -426,7 +460,8 @@ __global__ __launch_bounds__(256) void few_gate_up_kernel(FewParams p) {
       const int f = f0 + (q >> 1) * kRows + row;
       const uint32_t r = (uint32_t)((q & 1) ? p.F + f : f);
       wrow[q] = f < p.F ? r * kbytes : kFar;
-      srow[q] = r * sbytes;
+      const int fs = f0 + (q >> 1) * kRows + srow_of;
+      srow[q] = fs < p.F ? (uint32_t)((q & 1) ? p.F + fs : fs) * sbytes : kFar;
     }
 #pragma unroll
     for (int q = 0; q < NS; ++q) {
@@ -438,7 +473,7 @@ __global__ __launch_bounds__(256) void few_gate_up_kernel(FewParams p) {
     b.load(rsrc(p.w_gu + (int64_t)e * rows * kbytes, rows * kbytes),
            rsrc(p.s_gu + (int64_t)e * rows * sbytes,
                 B::kMx ? rows * sbytes : 0u),
-           rx, wrow, srow, xoff, bt * U * KS + cw, KS, real ? nch : 0, kbytes,
+           rx, wrow, srow, xoff, (bt * KS + cw) * U, real ? nch : 0, kbytes,
            piece, lane);
   };
   f32x4_t acc[RS][NS];
@@ -504,7 +539,7 @@ __global__ __launch_bounds__(256) void few_gate_up_kernel(FewParams p) {
     }
   };
   auto step = [&](const B& b) {
-    b.mma(acc);
+    b.mma(acc, lane);
     if (++cb == nb) {
       finish(ci);
       cb = 0;
@@ -561,7 +596,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(
   const __amdgpu_buffer_rsrc_t ra =
       rsrc(p.a, (uint32_t)P * (uint32_t)p.F * 2u);
   const uint32_t wrow[1] = {(uint32_t)(h0 + row) * kbytes};
-  const uint32_t srow[1] = {(uint32_t)(h0 + row) * sbytes};
+  const uint32_t srow[1] = {
+      (uint32_t)(h0 + (B::kWords ? lane >> 3 : row)) * sbytes};
   const int nch = (int)((kbytes + 127) / 128);
   const int64_t total = (int64_t)n * nch;
   const int64_t at = total * wave / kDownWaves;
@@ -588,7 +624,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(
     b.load(rsrc(p.w_dn + (int64_t)e * p.H * kbytes, (uint32_t)p.H * kbytes),
            rsrc(p.s_dn + (int64_t)e * p.H * sbytes,
                 B::kMx ? (uint32_t)p.H * sbytes : 0u),
-           ra, wrow, srow, xoff, c, 1, cend, kbytes, piece, lane);
+           ra, wrow, srow, xoff, c, cend, kbytes, piece, lane);
   };
   f32x4_t acc[1][NS];
   auto clear = [&]() {
@@ -626,7 +662,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(
     };
     bool more = true;
     auto step = [&](const B& b) {
-      b.mma(acc);
+      b.mma(acc, lane);
       cc += U;
       if (cc >= stop(ci)) {
         finish(ci);
@@ -828,16 +864,25 @@ hipError_t launch_layer_few(const LayerFew& a, hipStream_t stream) {
   p.status = a.status;
   // Columns of an entry: twice the mean of an expert's pairs (never more than
   // the tokens); the few experts that exceed it make another entry.  MXFP4,
-  // Qwen3-shaped, one call: 8 tokens 37.2 us with two columns, 39.2 with
-  // four, 42.4 with eight; 16 tokens 55.0 / 53.4 / 59.3; 32 tokens 82.7 /
-  // 75.2 / 80.2; 64 tokens 135 / 110.8 / 111.9.
+  // Qwen3-shaped, one call: 8 tokens 35.0 us with two columns, 38.7 with
+  // four, 39.2 with eight; 16 tokens 50.7 / 50.4 / 52.3; 32 tokens 76.5 /
+  // 72.7 / 71.5; 64 tokens 125 / 103 / 100.  Mixtral-shaped, 32 tokens: eight
+  // columns 338 us, sixteen 326.
   const int most = std::min(a.T, std::max(1, 2 * a.T * a.k / a.E));
   if (a.s_gu) {
+    const auto at = reinterpret_cast<uintptr_t>(a.s_gu) |
+                    reinterpret_cast<uintptr_t>(a.s_dn);
+    if (a.H % 128 != 0 || a.F % 128 != 0 || (at & 3) != 0) {
+      using Fmt = FmtMx4<false>;
+      return a.T <= 2 ? launch_experts<Fmt, 2, 1, 2, 1, 3>(p, stream)
+                      : launch_experts<Fmt, 8, 1, 2, 1, 3>(p, stream);
+    }
+    using Fmt = FmtMx4<true>;
     return most <= 1 || a.T <= 2
-               ? launch_experts<FmtMx4, 2, 1, 2, 1, 3>(p, stream)
-           : most <= 4 ? launch_experts<FmtMx4, 2, 2, 2, 1, 3>(p, stream)
-           : most <= 8 ? launch_experts<FmtMx4, 8, 1, 2, 1, 3>(p, stream)
-                       : launch_experts<FmtMx4, 8, 2, 1, 1, 2>(p, stream);
+               ? launch_experts<Fmt, 2, 1, 2, 2, 3>(p, stream)
+           : most <= 3 ? launch_experts<Fmt, 2, 2, 2, 1, 3>(p, stream)
+           : most <= 8 ? launch_experts<Fmt, 8, 1, 2, 1, 3>(p, stream)
+                       : launch_experts<Fmt, 8, 2, 1, 1, 2>(p, stream);
   }
   return most <= 8    ? launch_experts<FmtBf16, 8, 1, 4, 2, 4>(p, stream)
          : most <= 16 ? launch_experts<FmtBf16, 8, 2, 4, 2, 4>(p, stream)

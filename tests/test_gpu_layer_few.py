@@ -118,7 +118,8 @@ def test_tokens(m, T, fmt):
     (4, 1056, 224, 130, 5), (2, 2048, 768, 128, 8), (40, 160, 64, 64, 6),
     (64, 64, 64, 4, 4), (9, 352, 1376, 5, 2), (64, 32, 32, 2, 1),
     (6, 4096, 64, 4, 2), (3, 64, 4128, 4, 2), (1, 64, 64, 1024, 32),
-    (64, 32, 64, 40, 32)])
+    (64, 32, 64, 40, 32), (1, 128, 128, 4, 2), (3, 384, 640, 5, 2),
+    (20, 2048, 256, 6, 2), (8, 128, 1408, 200, 3), (2, 4096, 128, 3, 1)])
 def test_sizes(m, T, H, F, E, k, fmt):
     check(m, make(T, H, F, E, k, H + F), fmt)
 
