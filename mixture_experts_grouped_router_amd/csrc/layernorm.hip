@@ -9,10 +9,10 @@
 // Both directions are bound by HBM: the row is read once and held in
 // registers, so the variance is the sum of squares around the mean (no
 // E[x^2] - mean^2 cancellation), and everything is float32.  A row belongs
-// to one wave (H <= 2048), four (H <= 8192) or sixteen (H <= 16384): at most
-// 32 values per lane (16 in the last form, whose waves have 128 registers),
-// which leaves room for the backward's sums of dw and db, its weights and
-// the next row's loads.
+// to one wave (H <= 1024), four (H <= 4096), eight or sixteen (H <= 16384):
+// at most 16 values per lane, which leaves room for the backward's sums of
+// dw and db, its weights and the next row's loads with three or more waves
+// on a SIMD.
 // Work-groups are persistent: weights are read once per lane, not once per
 // row, and the backward keeps one sum of dw and db per lane over all of its
 // rows; a second launch adds the work-groups' sums in their order.
@@ -30,59 +30,94 @@ constexpr int kCus = 256;
 
 typedef float moe_f32x4_t __attribute__((ext_vector_type(4)));
 
-// VEC consecutive values of a row as they lie in memory
-template <typename XT, int VEC> struct Raw;
-template <> struct Raw<uint16_t, 8> {
+constexpr int kVec = 8;   // values of a chunk
+
+// Eight consecutive values of a row.  AL: the row length is a multiple of
+// eight, so every chunk is whole and 16-byte aligned; else rows start at any
+// element, a whole chunk is still one (unaligned) 16-byte access or two, and
+// a row's last chunk goes value by value.
+struct RawBf16 {
   uint4 a;
-  __device__ __forceinline__ void load(const uint16_t* p) {
-    a = *reinterpret_cast<const uint4*>(p);
-  }
-  __device__ __forceinline__ void clear() { a = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ float at(int i) const {
     const uint32_t w = i < 2 ? a.x : i < 4 ? a.y : i < 6 ? a.z : a.w;
     return (i & 1) ? bf16hi(w) : bf16lo(w);
   }
 };
-template <> struct Raw<float, 8> {
+struct RawF32 {
   moe_f32x4_t a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = *reinterpret_cast<const moe_f32x4_t*>(p);
-    b = *reinterpret_cast<const moe_f32x4_t*>(p + 4);
-  }
-  __device__ __forceinline__ void clear() { a = b = moe_f32x4_t{}; }
   __device__ __forceinline__ float at(int i) const {
     return i < 4 ? a[i & 3] : b[i & 3];
   }
 };
-template <> struct Raw<uint16_t, 1> {
-  uint32_t a;
-  __device__ __forceinline__ void load(const uint16_t* p) { a = *p; }
-  __device__ __forceinline__ void clear() { a = 0; }
-  __device__ __forceinline__ float at(int) const { return bf16_to_f32(a); }
-};
-template <> struct Raw<float, 1> {
-  float a;
-  __device__ __forceinline__ void load(const float* p) { a = *p; }
-  __device__ __forceinline__ void clear() { a = 0.0f; }
-  __device__ __forceinline__ float at(int) const { return a; }
-};
+template <typename XT> struct RawOf;
+template <> struct RawOf<uint16_t> { typedef RawBf16 T; };
+template <> struct RawOf<float> { typedef RawF32 T; };
 
-template <int VEC>
-__device__ __forceinline__ void store_vec(uint16_t* p, const float* v) {
-  if constexpr (VEC == 8)
-    *reinterpret_cast<uint4*>(p) =
-        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                   pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-  else
-    *p = (uint16_t)f32_to_bf16(v[0]);
+// the first n of eight values at p (n <= 0: none), the others 0
+template <bool AL, typename R, typename XT>
+__device__ __forceinline__ void load_chunk(R& r, const XT* p, int n) {
+  r = R{};
+  if (n >= kVec) {
+    if constexpr (AL)
+      r = *reinterpret_cast<const R*>(__builtin_assume_aligned(p, 16));
+    else
+      __builtin_memcpy(&r, p, sizeof(R));
+  } else if constexpr (!AL) {
+    if (n > 0) {
+      uint32_t w[8] = {};
+#pragma unroll
+      for (int i = 0; i < kVec - 1; ++i)
+        if (i < n) {
+          if constexpr (sizeof(XT) == 2)
+            w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+          else
+            w[i] = __float_as_uint(p[i]);
+        }
+      if constexpr (sizeof(XT) == 2) {
+        r.a = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          r.a[i] = __uint_as_float(w[i]);
+          r.b[i] = __uint_as_float(w[4 + i]);
+        }
+      }
+    }
+  }
 }
-template <int VEC>
-__device__ __forceinline__ void store_vec(float* p, const float* v) {
-  if constexpr (VEC == 8) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    *p = v[0];
+
+template <bool AL>
+__device__ __forceinline__ void store_chunk(uint16_t* p, const float* v,
+                                            int n) {
+  if (n >= kVec) {
+    const uint4 o = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                               pack_bf16x2(v[4], v[5]),
+                               pack_bf16x2(v[6], v[7]));
+    if constexpr (AL)
+      *reinterpret_cast<uint4*>(p) = o;
+    else
+      __builtin_memcpy(p, &o, sizeof(o));
+  } else if constexpr (!AL) {
+#pragma unroll
+    for (int i = 0; i < kVec - 1; ++i)
+      if (i < n) p[i] = (uint16_t)f32_to_bf16(v[i]);
+  }
+}
+template <bool AL>
+__device__ __forceinline__ void store_chunk(float* p, const float* v, int n) {
+  if (n >= kVec) {
+    const moe_f32x4_t a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+    if constexpr (AL) {
+      *reinterpret_cast<moe_f32x4_t*>(p) = a;
+      *reinterpret_cast<moe_f32x4_t*>(p + 4) = b;
+    } else {
+      __builtin_memcpy(p, &a, sizeof(a));
+      __builtin_memcpy(p + 4, &b, sizeof(b));
+    }
+  } else if constexpr (!AL) {
+#pragma unroll
+    for (int i = 0; i < kVec - 1; ++i)
+      if (i < n) p[i] = v[i];
   }
 }
 
@@ -124,25 +159,24 @@ struct RowSum {
   }
 };
 
-constexpr int ln_threads(int wpr) { return wpr == 16 ? 1024 : 256; }
+constexpr int ln_threads(int wpr) { return wpr <= 4 ? 256 : 64 * wpr; }
 constexpr int ln_rows(int wpr) { return wpr == 1 ? 4 : 1; }
 
 // the lane's values of a per-column array (absent: the given value)
-template <int VEC, int NV, int L>
+template <bool AL, int NV, int L>
 __device__ __forceinline__ void load_cols(const float* p, float absent, int l,
-                                          int H, float (&v)[NV * VEC]) {
+                                          int H, float (&v)[NV * kVec]) {
 #pragma unroll
   for (int c = 0; c < NV; ++c) {
-    const int col = (c * L + l) * VEC;
-    Raw<float, VEC> r;
-    r.clear();
-    if (p && col < H) r.load(p + col);
+    const int col = (c * L + l) * kVec;
+    RawF32 r = {};
+    if (p) load_chunk<AL>(r, p + col, H - col);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[c * VEC + i] = p ? r.at(i) : absent;
+    for (int i = 0; i < kVec; ++i) v[c * kVec + i] = p ? r.at(i) : absent;
   }
 }
 
-template <typename XT, int VEC, int NV, int WPR>
+template <typename XT, bool AL, int NV, int WPR>
 __global__ __launch_bounds__(ln_threads(WPR)) void ln_fwd_kernel(
     const XT* __restrict__ x, const float* __restrict__ w,
     const float* __restrict__ b, uint16_t* __restrict__ y,
@@ -156,29 +190,29 @@ __global__ __launch_bounds__(ln_threads(WPR)) void ln_fwd_kernel(
   int64_t row = (int64_t)blockIdx.x * ln_rows(WPR) +
                 (WPR == 1 ? threadIdx.x >> 6 : 0);
   if (row >= T) return;   // the whole work-group if a row takes all of it
-  auto load = [&](Raw<XT, VEC> (&r)[NV], int64_t t) {
+  typedef typename RawOf<XT>::T R;
+  auto load = [&](R (&r)[NV], int64_t t) {
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-      const int col = (c * L + l) * VEC;
-      r[c].clear();
-      if (col < H) r[c].load(x + t * H + col);
+      const int col = (c * L + l) * kVec;
+      load_chunk<AL>(r[c], x + t * H + col, H - col);
     }
   };
-  Raw<XT, VEC> r[NV];
+  R r[NV];
   load(r, row);
-  float wv[NV * VEC], bv[NV * VEC];
-  load_cols<VEC, NV, L>(w, 1.0f, l, H, wv);
-  load_cols<VEC, NV, L>(b, 0.0f, l, H, bv);
+  float wv[NV * kVec], bv[NV * kVec];
+  load_cols<AL, NV, L>(w, 1.0f, l, H, wv);
+  load_cols<AL, NV, L>(b, 0.0f, l, H, bv);
   const float inv = 1.0f / (float)H;
   for (; row < T; row += step) {
-    float v[NV * VEC];
+    float v[NV * kVec];
     float s[1] = {0.0f};
 #pragma unroll
     for (int c = 0; c < NV; ++c)
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        v[c * VEC + i] = r[c].at(i);
-        s[0] += v[c * VEC + i];
+      for (int i = 0; i < kVec; ++i) {
+        v[c * kVec + i] = r[c].at(i);
+        s[0] += v[c * kVec + i];
       }
     if (row + step < T) load(r, row + step);
     sum(s);
@@ -186,23 +220,23 @@ __global__ __launch_bounds__(ln_threads(WPR)) void ln_fwd_kernel(
     float q[1] = {0.0f};
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-      const bool in = (c * L + l) * VEC < H;
+      const int n = H - (c * L + l) * kVec;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        v[c * VEC + i] -= mu;
-        if (in) q[0] = fmaf(v[c * VEC + i], v[c * VEC + i], q[0]);
+      for (int i = 0; i < kVec; ++i) {
+        v[c * kVec + i] -= mu;
+        if (AL ? n > 0 : i < n) q[0] = fmaf(v[c * kVec + i], v[c * kVec + i], q[0]);
       }
     }
     sum(q);
     const float rs = 1.0f / sqrtf(q[0] * inv + eps);
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-      const int col = (c * L + l) * VEC;
-      float o[VEC];
+      const int col = (c * L + l) * kVec;
+      float o[kVec];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i)
-        o[i] = fmaf(v[c * VEC + i] * rs, wv[c * VEC + i], bv[c * VEC + i]);
-      if (col < H) store_vec<VEC>(y + row * H + col, o);
+      for (int i = 0; i < kVec; ++i)
+        o[i] = fmaf(v[c * kVec + i] * rs, wv[c * kVec + i], bv[c * kVec + i]);
+      store_chunk<AL>(y + row * H + col, o, H - col);
     }
     if (l == 0) {
       if (mean) mean[row] = mu;
@@ -213,7 +247,7 @@ __global__ __launch_bounds__(ln_threads(WPR)) void ln_fwd_kernel(
 
 // part: [work-groups][2][H] sums of dw and db (one work-group: dw, db
 // themselves, either of which may be null)
-template <typename XT, int VEC, int NV, int WPR>
+template <typename XT, bool AL, int NV, int WPR>
 __global__ __launch_bounds__(ln_threads(WPR)) void ln_bwd_kernel(
     const uint16_t* __restrict__ dy, const XT* __restrict__ x,
     const float* __restrict__ mean, const float* __restrict__ rstd,
@@ -230,47 +264,44 @@ __global__ __launch_bounds__(ln_threads(WPR)) void ln_bwd_kernel(
   // the next row's loads go out ahead of the reductions and the weights stay
   // in registers; sixteen waves per row have no registers left for that
   constexpr bool kAhead = WPR < 16;
-  Raw<XT, VEC> rx[NV], rr[NV];
-  Raw<uint16_t, VEC> rd[NV];
+  typename RawOf<XT>::T rx[NV], rr[NV];
+  RawBf16 rd[NV];
   float mu = 0.0f, rs = 0.0f;
   auto load = [&](int64_t t) {
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-      const int col = (c * L + l) * VEC;
-      rx[c].clear();
-      rd[c].clear();
-      rr[c].clear();
-      if (col < H) {
-        rx[c].load(x + t * H + col);
-        rd[c].load(dy + t * H + col);
-        if (kAhead && dres) rr[c].load(dres + t * H + col);
-      }
+      const int col = (c * L + l) * kVec;
+      const int n = H - col;
+      load_chunk<AL>(rx[c], x + t * H + col, n);
+      load_chunk<AL>(rd[c], dy + t * H + col, n);
+      rr[c] = {};
+      if (kAhead && dres) load_chunk<AL>(rr[c], dres + t * H + col, n);
     }
     mu = mean[t];
     rs = rstd[t];
   };
   if (kAhead && row < T) load(row);
-  float wv[NV * VEC], aw[NV * VEC], ab[NV * VEC];
-  if (kAhead) load_cols<VEC, NV, L>(w, 1.0f, l, H, wv);
+  float wv[NV * kVec], aw[NV * kVec], ab[NV * kVec];
+  if (kAhead) load_cols<AL, NV, L>(w, 1.0f, l, H, wv);
 #pragma unroll
-  for (int i = 0; i < NV * VEC; ++i) aw[i] = ab[i] = 0.0f;
+  for (int i = 0; i < NV * kVec; ++i) aw[i] = ab[i] = 0.0f;
   const float inv = 1.0f / (float)H;
   for (; row < T; row += step) {
-    float xh[NV * VEC], g[NV * VEC], o[NV * VEC];
+    float xh[NV * kVec], g[NV * kVec], o[NV * kVec];
     float s[2] = {0.0f, 0.0f};
     if (!kAhead) {
       load(row);
-      load_cols<VEC, NV, L>(w, 1.0f, l, H, wv);
+      load_cols<AL, NV, L>(w, 1.0f, l, H, wv);
     }
     const float r = rs;
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-      const bool in = (c * L + l) * VEC < H;
+      const int n = H - (c * L + l) * kVec;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const int k = c * VEC + i;
+      for (int i = 0; i < kVec; ++i) {
+        const int k = c * kVec + i;
         const float d = rd[c].at(i);
-        xh[k] = in ? (rx[c].at(i) - mu) * r : 0.0f;
+        xh[k] = (AL ? n > 0 : i < n) ? (rx[c].at(i) - mu) * r : 0.0f;
         if (kAhead) o[k] = rr[c].at(i);
         aw[k] = fmaf(d, xh[k], aw[k]);
         ab[k] += d;
@@ -285,15 +316,16 @@ __global__ __launch_bounds__(ln_threads(WPR)) void ln_bwd_kernel(
       const float c1 = s[0] * inv, c2 = s[1] * inv;
 #pragma unroll
       for (int c = 0; c < NV; ++c) {
-        const int col = (c * L + l) * VEC;
-        if (!kAhead && dres && col < H) rr[c].load(dres + row * H + col);
+        const int col = (c * L + l) * kVec;
+        if (!kAhead && dres)
+          load_chunk<AL>(rr[c], dres + row * H + col, H - col);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const int k = c * VEC + i;
+        for (int i = 0; i < kVec; ++i) {
+          const int k = c * kVec + i;
           if (!kAhead) o[k] = rr[c].at(i);
           o[k] = fmaf(r, g[k] - c1 - xh[k] * c2, o[k]);
         }
-        if (col < H) store_vec<VEC>(dx + row * H + col, o + c * VEC);
+        store_chunk<AL>(dx + row * H + col, o + c * kVec, H - col);
       }
     }
   }
@@ -302,13 +334,13 @@ __global__ __launch_bounds__(ln_threads(WPR)) void ln_bwd_kernel(
   float* ob = part ? ow + H : db;
   if constexpr (WPR == 1) {
     // the four waves' sums, in wave order
-    __shared__ float acc[NV * VEC * 64];
+    __shared__ float acc[NV * kVec * 64];
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       for (int k = 0; k < 4; ++k) {
         if ((threadIdx.x >> 6) == k) {
 #pragma unroll
-          for (int i = 0; i < NV * VEC; ++i) {
+          for (int i = 0; i < NV * kVec; ++i) {
             const float v = which ? ab[i] : aw[i];
             acc[i * 64 + l] = k == 0 ? v : acc[i * 64 + l] + v;
           }
@@ -317,9 +349,9 @@ __global__ __launch_bounds__(ln_threads(WPR)) void ln_bwd_kernel(
       }
       float* out = which ? ob : ow;
       if (out)
-        for (int i = threadIdx.x; i < NV * VEC * 64; i += 256) {
+        for (int i = threadIdx.x; i < NV * kVec * 64; i += 256) {
           // value i / 64 of lane i % 64
-          const int k = i >> 6, col = ((k / VEC) * L + (i & 63)) * VEC + k % VEC;
+          const int k = i >> 6, col = ((k / kVec) * L + (i & 63)) * kVec + k % kVec;
           if (col < H) out[col] = acc[i];
         }
       __syncthreads();
@@ -327,11 +359,10 @@ __global__ __launch_bounds__(ln_threads(WPR)) void ln_bwd_kernel(
   } else {
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-      const int col = (c * L + l) * VEC;
-      if (col < H) {
-        if (ow) store_vec<VEC>(ow + col, aw + c * VEC);
-        if (ob) store_vec<VEC>(ob + col, ab + c * VEC);
-      }
+      const int col = (c * L + l) * kVec;
+      // (partial sums of an odd H start at any element too)
+      if (ow) store_chunk<AL>(ow + col, aw + c * kVec, H - col);
+      if (ob) store_chunk<AL>(ob + col, ab + c * kVec, H - col);
     }
   }
 }
@@ -369,40 +400,47 @@ __global__ __launch_bounds__(256) void ln_finish_kernel(
 
 // Work-groups of a launch: as many as the chip holds at once (persistent
 // rows), fewer for few rows.
-int ln_wpr(int H) { return H <= 2048 ? 1 : H <= 8192 ? 4 : 16; }
+int ln_wpr(int H) {
+  return H <= 1024 ? 1 : H <= 4096 ? 4 : H <= 8192 ? 8 : 16;
+}
 int ln_grid(int64_t T, int H, int per_cu) {
   const int rows = ln_rows(ln_wpr(H));
   return (int)std::min<int64_t>((T + rows - 1) / rows,
                                 (int64_t)kCus * per_cu);
 }
-int ln_fwd_grid(int64_t T, int H) { return ln_grid(T, H, 4); }
+int ln_fwd_grid(int64_t T, int H) {
+  return ln_grid(T, H, H <= 4096 ? 4 : H <= 8192 ? 2 : 1);
+}
+// The backward's work-groups each leave 2 H partial sums, so they are as few
+// as keep the loads going (32768 x 2048: one per CU 120.6 us, two 101.6,
+// three 106.1; 16384 x 4096: 96.5, 108.0, 112.9) and take four rows each at
+// least (512 x 2048: 9.3 us, with one row each 13.8).
 int ln_bwd_grid(int64_t T, int H) {
-  return ln_grid(T, H, ln_wpr(H) == 16 ? 1 : 2);
+  const int rows = ln_rows(ln_wpr(H)) * 4;
+  const int per_cu = H > 1024 && H <= 2048 ? 2 : 1;
+  return (int)std::min<int64_t>((T + rows - 1) / rows,
+                                (int64_t)kCus * per_cu);
 }
 
-// f(VEC, NV, WPR) for H; 16-byte chunks where every row starts on one
+// f(AL, NV, WPR) for H
 template <typename F>
 hipError_t dispatch(int H, F&& f) {
   using std::integral_constant;
-  auto pick = [&](auto wpr, auto vec) -> hipError_t {
-    constexpr int W = decltype(wpr)::value, V = decltype(vec)::value;
-    const int per = (H + 64 * W - 1) / (64 * W);   // values per lane
-    if constexpr (W == 1)
-      if (per <= 8) return f(vec, integral_constant<int, 8 / V>{}, wpr);
-    if (W == 16 || per <= 16)
-      return f(vec, integral_constant<int, 16 / V>{}, wpr);
+  auto pick = [&](auto wpr, auto al) -> hipError_t {
+    constexpr int W = decltype(wpr)::value;
     if constexpr (W <= 4)
-      return f(vec, integral_constant<int, 32 / V>{}, wpr);
-    return hipErrorInvalidValue;
+      if (H <= 64 * kVec * W) return f(al, integral_constant<int, 1>{}, wpr);
+    return f(al, integral_constant<int, 2>{}, wpr);
   };
-  auto vecs = [&](auto wpr) {
-    return H % 8 == 0 ? pick(wpr, integral_constant<int, 8>{})
-                      : pick(wpr, integral_constant<int, 1>{});
+  auto align = [&](auto wpr) {
+    return H % kVec == 0 ? pick(wpr, std::true_type{})
+                         : pick(wpr, std::false_type{});
   };
   const int w = ln_wpr(H);
-  if (w == 1) return vecs(integral_constant<int, 1>{});
-  if (w == 4) return vecs(integral_constant<int, 4>{});
-  return vecs(integral_constant<int, 16>{});
+  if (w == 1) return align(integral_constant<int, 1>{});
+  if (w == 4) return align(integral_constant<int, 4>{});
+  if (w == 8) return align(integral_constant<int, 8>{});
+  return align(integral_constant<int, 16>{});
 }
 
 template <typename XT>
@@ -410,10 +448,10 @@ hipError_t fwd(const void* x, const float* w, const float* b, void* y,
                float* mean, float* rstd, int64_t T, int H, float eps,
                hipStream_t stream) {
   KernelScope ks("layernorm_fwd", stream);
-  return dispatch(H, [&](auto vec, auto nv, auto wpr) {
-    constexpr int V = decltype(vec)::value, N = decltype(nv)::value,
-                  W = decltype(wpr)::value;
-    hipLaunchKernelGGL((ln_fwd_kernel<XT, V, N, W>), dim3(ln_fwd_grid(T, H)),
+  return dispatch(H, [&](auto al, auto nv, auto wpr) {
+    constexpr bool A = decltype(al)::value;
+    constexpr int N = decltype(nv)::value, W = decltype(wpr)::value;
+    hipLaunchKernelGGL((ln_fwd_kernel<XT, A, N, W>), dim3(ln_fwd_grid(T, H)),
                        dim3(ln_threads(W)), 0, stream,
                        static_cast<const XT*>(x), w, b,
                        static_cast<uint16_t*>(y), mean, rstd, T, H, eps);
@@ -427,10 +465,10 @@ hipError_t bwd(const void* dy, const void* x, const float* mean,
                float* part, float* dw, float* db, int64_t T, int H,
                hipStream_t stream) {
   KernelScope ks("layernorm_bwd", stream);
-  return dispatch(H, [&](auto vec, auto nv, auto wpr) {
-    constexpr int V = decltype(vec)::value, N = decltype(nv)::value,
-                  W = decltype(wpr)::value;
-    hipLaunchKernelGGL((ln_bwd_kernel<XT, V, N, W>), dim3(ln_bwd_grid(T, H)),
+  return dispatch(H, [&](auto al, auto nv, auto wpr) {
+    constexpr bool A = decltype(al)::value;
+    constexpr int N = decltype(nv)::value, W = decltype(wpr)::value;
+    hipLaunchKernelGGL((ln_bwd_kernel<XT, A, N, W>), dim3(ln_bwd_grid(T, H)),
                        dim3(ln_threads(W)), 0, stream,
                        static_cast<const uint16_t*>(dy),
                        static_cast<const XT*>(x), mean, rstd, w,
