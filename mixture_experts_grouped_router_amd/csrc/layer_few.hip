@@ -45,13 +45,23 @@ namespace {
 constexpr int32_t kDevErrExpertId = 1;   // include/moe.h MOE_DEVERR_*
 constexpr int32_t kDevErrLogits = 3;
 constexpr int kMaxPairs = kFewMaxTokens * 32;   // MOE_MAX_TOPK
-constexpr int kFuseTopk = 4;             // tokens whose experts every
-                                         // work-group picks for itself
-// Gate/up: from this many items on a wave takes whole items and the grid is
-// two work-groups per CU; below, four waves share each item and the grid is
-// at most three per CU (the register file's limit).  Qwen3-shaped bf16, one
-// token (768 items): 11.4 us against 14; 64 tokens (12288): 265 us for the
-// layer against 270.
+// Tokens whose experts every work-group picks for itself; with a launch of
+// its own one token takes 34.1 us for 27.8, two 52.9 for 48.6, four 77.8 for
+// 77.5 (128 experts, 2048 x 768, bf16).
+constexpr int kFuseTopk = 4;
+// Gate/up: four waves share each item and the grid is at most three
+// work-groups per CU (the register file's limit), which keeps the fewest
+// work-groups waiting at the end; or a wave takes whole items, with two
+// work-groups per CU, which needs no sums between waves.  Whole items against
+// shared ones, layer's time:
+//   MXFP4, 128 experts, 2048 x 768: 2 tokens (768 items) 20.4 us against
+//     18.4, 8 tokens (3072) 36.3 / 35.3, 12 tokens (4608) 44.8 / 45.4, 16
+//     tokens (6144) 53.4 / 58.4, 64 tokens 100 / 105; eight experts, 4096 x
+//     14336, one token (1792) 141 / 134
+//   bf16, 128 experts: one token 28.7 / 27.8, 8 tokens 121.9 / 119.0, 32
+//     tokens 222 / 215, 64 tokens 255 / 248; eight experts, five tokens
+//     431 / 421; with two column sets (64 tokens) 684 / 767
+// so shared for bf16 with one column set and for fewer items than this.
 constexpr int kWholeItems = 4096;
 
 struct FewParams {
@@ -770,7 +780,7 @@ hipError_t launch_experts(const FewParams& p, hipStream_t stream) {
     // items if every pair reached an expert of its own
     const int64_t items = (int64_t)std::min(P, p.E) *
                           ((p.F + kRows * RSF - 1) / (kRows * RSF));
-    if (items < kWholeItems)
+    if (items < kWholeItems || (FMT::kMfma == 1 && NS == 1))
       hipLaunchKernelGGL((few_gate_up_kernel<FMT, CT, NS, RSF, 4, UG4>),
                          dim3((unsigned)std::min<int64_t>(items, 768)),
                          dim3(256), 0, stream, p);

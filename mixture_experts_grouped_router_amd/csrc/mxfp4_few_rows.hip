@@ -28,15 +28,6 @@
 namespace moe {
 namespace {
 
-#ifndef FRGU
-#define FRGU 512
-#endif
-#ifndef FRG
-#define FRG 768
-#endif
-#ifndef FRD
-#define FRD 4
-#endif
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 struct RowsParams {
@@ -290,19 +281,22 @@ hipError_t launch_mx4_few_rows(const Mx4FewRows& a, hipStream_t stream) {
   d.z = static_cast<uint16_t*>(a.z);
   d.N = a.H;
   d.K = a.F;
-  const dim3 block(256);
+  // Items of eight row sets and two work-groups per CU for gate/up, of four
+  // row sets and three work-groups per CU for down.  77 tokens x 8 over 128
+  // experts, 2048 x 768: 75.9 us for the MLP; gate/up with three per CU 82.9;
+  // down with two 80.7, with four 77.4, with eight row sets 80.9.
+  const dim3 block(256), gu_grid(512), dn_grid(768);
   auto run = [&](auto ns) -> hipError_t {
     constexpr int NS = decltype(ns)::value;
     {
       KernelScope ks("mxfp4_few_rows_gate_up", stream);
-      hipLaunchKernelGGL((mx4_few_rows_kernel<true, 8, NS>), dim3(FRGU),
-                         block,
-                         0, stream, p);
+      hipLaunchKernelGGL((mx4_few_rows_kernel<true, 8, NS>), gu_grid,
+                         block, 0, stream, p);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
     KernelScope ks("mxfp4_few_rows_down", stream);
-    hipLaunchKernelGGL((mx4_few_rows_kernel<false, FRD, NS>), dim3(FRG), block,
+    hipLaunchKernelGGL((mx4_few_rows_kernel<false, 4, NS>), dn_grid, block,
                        0, stream, d);
     return hipGetLastError();
   };
