@@ -156,14 +156,15 @@ def test_mlp(m, sizes, H, F):
     assert torch.equal(z[0], z[1]) and torch.equal(z[0], z[2])
 
 
-# at most eight rows per expert on average: the kernels for few rows, with
+# at most twelve rows per expert on average: the kernels for few rows, with
 # entries of up to eight (five and fewer) or sixteen rows, experts that need
 # several entries, one expert, every K tail
 FEW = [([1], 128, 128), ([5, 0, 1, 12], 256, 384), ([8] * 16, 384, 256),
        ([1] * 40, 512, 640), ([64] + [0] * 15, 1280, 128),
        ([0, 3, 0, 61, 0, 0, 0, 0], 128, 1408), ([9, 16, 17, 1, 0, 5, 7, 8],
                                                 2048, 768),
-       ([2, 40, 0, 0, 0, 0, 1, 0], 640, 384), ([7], 256, 128), ([8], 128, 256)]
+       ([2, 40, 0, 0, 0, 0, 1, 0], 640, 384), ([7], 256, 128), ([8], 128, 256),
+       ([12] * 5, 256, 256), ([0, 33, 3], 384, 128)]
 
 
 @pytest.mark.parametrize("sizes,H,F", FEW)
