@@ -13,7 +13,6 @@
 #include <algorithm>
 
 #include "grouped_gemm.hpp"
-#include "mxfp4.hpp"
 
 namespace moe {
 namespace gg {
@@ -282,29 +281,6 @@ __device__ __forceinline__ void epilogue_w8_swiglu(const Params& p,
                              (uint32_t)(p.F / 128))] = (uint8_t)(sx + 127);
             if (p.cs_rm)
               p.cs_rm[row * (p.F / 32) + f / 32] = (uint8_t)(sx + 127);
-          }
-        }
-      }
-      if constexpr (EPI == EPI_SWIGLU_MX4) {
-        // F % 128 == 0, as above; two codes per byte
-        uint32_t am = 0;
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          am = max(am, __float_as_uint(v[c]) & 0x7fffffffu);
-        am = max(am, (uint32_t)__shfl_xor((int)am, 1, 64));
-        am = max(am, (uint32_t)__shfl_xor((int)am, 2, 64));
-        const int sx = mx4_exp_from_f32_amax(am);
-        const uint32_t w4 = e2m1x8_f32(v, mx_scale_f32(sx));
-        if (ok) {
-          *reinterpret_cast<uint32_t*>(p.cq + row * (p.F / 2) + f / 2) = w4;
-          if ((c8 & 3) == 0) {
-            const uint32_t kb = (uint32_t)(f / 32);
-            uint8_t* cs = p.cs + mx4_tile_off((uint32_t)row, kb,
-                                              (uint32_t)((p.F + 255) / 256));
-            cs[0] = (uint8_t)(sx + 127);
-            // the last K step's missing half: scale 1 for its zero codes
-            // (block kb + 4 lies two bytes on)
-            if ((p.F & 128) && kb + 4 >= (uint32_t)(p.F / 32)) cs[2] = 127;
           }
         }
       }

@@ -1,11 +1,12 @@
 // The MXFP4 forward grouped GEMMs (ragged M, K-contiguous operands, both
 // 4-bit): tile, wave shapes, five-buffer rotation, direct loads and
-// epilogues of the eight-wave 8-bit kernel (grouped_gemm_w8q.hpp) with
+// store epilogue of the eight-wave 8-bit kernel (grouped_gemm_w8q.hpp) with
 // v_mfma_scale_f32_32x32x64_f8f6f4 on E2M1 operands, which takes half the
 // cycles of the E4M3 form and half the operand bytes: a K step is again one
 // 128-byte row per operand (256 values), so LDS traffic and loads per MFMA
 // cycle are those of the 8-bit kernel and a step has half as much work per
-// K value.
+// K value.  (The 8-bit kernel's split of the last round's tiles along K gains
+// nothing here: Mixtral-shaped MLP 1531 us with it and without.)
 //
 // Operand layout of the MFMA (measured on the device): lane l holds row
 // l % 32 and, with g = l / 32, the 32 consecutive K values 32 g .. of the
@@ -46,12 +47,104 @@ __device__ __forceinline__ void issue4(const D& d, char* lds_tile, int s,
   }
 }
 
+// Epilogue of the gate/up product, without LDS.  The weights are the MFMA's
+// rows, so a lane holds one token's values: register r of acc[i][2 jj] (g)
+// and acc[i][2 jj + 1] (u) is f = f0 + 32 jj + 8 (r / 4) + 4 h + r % 4 of
+// row 32 i + lane % 32, with h = lane / 32.  A block of 32 f is 16 registers
+// of lanes l and l + 32: its largest magnitude takes one exchange between
+// them, its codes two more, after which lane half h holds the 16 bytes of
+// block jj = h and stores them and their scale.  (Through LDS, a quad of
+// lanes per block, the gate/up product took 1080 us for 1027 Mixtral-shaped,
+// 337 for 303 Qwen3-shaped and skewed.  The down product keeps its staging:
+// stored from transposed registers in 32-byte pieces per row it takes 292 us
+// for 274.)  The saves (g, u) and A go out in pieces of eight bytes: they
+// serve checks, not training.
+__device__ __forceinline__ void epilogue4_swiglu(const Params& p,
+                                                 const TileCoord& tc,
+                                                 f32x16_t (&acc)[2][4],
+                                                 int n0, int wm, int wn,
+                                                 int lane) {
+  const int h = lane >> 5;
+  const int f0 = n0 + 64 * wn;   // F % 128 == 0: whole runs
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int mrow = tc.m0 + wm * 64 + 32 * i + (lane & 31);
+    const bool ok = mrow < tc.seg_len;
+    const int64_t row = tc.seg0 + min(mrow, tc.seg_len - 1);
+    const float wr = p.w ? p.w[row] : 1.0f;
+    uint32_t c01[2], c23[2];   // codes of quads 0 and 1, 2 and 3 of block jj
+    int sx[2];
+#pragma unroll
+    for (int jj = 0; jj < 2; ++jj) {
+      const f32x16_t &g = acc[i][2 * jj], &u = acc[i][2 * jj + 1];
+      float v[16];
+      uint32_t am = 0;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        v[r] = (g[r] * fast_sigmoid(g[r])) * u[r] * wr;
+        am = max(am, __float_as_uint(v[r]) & 0x7fffffffu);
+      }
+      const auto sw = __builtin_amdgcn_permlane32_swap(am, am, false, false);
+      sx[jj] = mx4_exp_from_f32_amax(max(sw[0], sw[1]));
+      const float sc = mx_scale_f32(sx[jj]);
+      const float lo[8] = {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
+      const float hi[8] = {v[8],  v[9],  v[10], v[11],
+                           v[12], v[13], v[14], v[15]};
+      c01[jj] = e2m1x8_f32(lo, sc);
+      c23[jj] = e2m1x8_f32(hi, sc);
+      if (ok && p.c2) {
+        uint16_t* o = p.c2 + row * 2 * p.F + f0 + 32 * jj + 4 * h;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          *reinterpret_cast<uint2*>(o + 8 * q) =
+              make_uint2(pack_bf16x2(g[4 * q], g[4 * q + 1]),
+                         pack_bf16x2(g[4 * q + 2], g[4 * q + 3]));
+          *reinterpret_cast<uint2*>(o + p.F + 8 * q) =
+              make_uint2(pack_bf16x2(u[4 * q], u[4 * q + 1]),
+                         pack_bf16x2(u[4 * q + 2], u[4 * q + 3]));
+        }
+      }
+      if (ok && p.c) {
+        uint16_t* o = p.c + row * p.ldc + f0 + 32 * jj + 4 * h;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint2*>(o + 8 * q) =
+              make_uint2(pack_bf16x2(v[4 * q], v[4 * q + 1]),
+                         pack_bf16x2(v[4 * q + 2], v[4 * q + 3]));
+      }
+    }
+    // lane half 0 gives its codes of block 1 for the other's of block 0: [0]
+    // then holds what half 0 made, [1] what half 1 made
+    const auto s01 =
+        __builtin_amdgcn_permlane32_swap(c01[0], c01[1], false, false);
+    const auto s23 =
+        __builtin_amdgcn_permlane32_swap(c23[0], c23[1], false, false);
+    if (ok) {
+      const uint4 o = make_uint4(
+          (s01[0] & 0xffffu) | (s01[1] << 16),
+          (s01[0] >> 16) | (s01[1] & 0xffff0000u),
+          (s23[0] & 0xffffu) | (s23[1] << 16),
+          (s23[0] >> 16) | (s23[1] & 0xffff0000u));
+      *reinterpret_cast<uint4*>(p.cq + row * (p.F / 2) + f0 / 2 + 16 * h) = o;
+      const uint32_t kb = (uint32_t)(f0 / 32 + h);
+      uint8_t* cs = p.cs + mx4_tile_off((uint32_t)row, kb,
+                                        (uint32_t)((p.F + 255) / 256));
+      cs[0] = (uint8_t)((h ? sx[1] : sx[0]) + 127);
+      // the last K step's missing half: scale 1 for its zero codes (block
+      // kb + 4 lies two bytes on)
+      if ((p.F & 128) && kb + 4 >= (uint32_t)(p.F / 32)) cs[2] = 127;
+    }
+  }
+}
+
 template <int EPI>
 __global__ __launch_bounds__(kThreads8) void grouped_gemm_w8f4_kernel(
     Params p) {
   static_assert(EPI == EPI_STORE || EPI == EPI_SWIGLU_MX4, "forward epilogues");
   using S = Shape8<EPI>;
   constexpr int MI = S::MI, NJ = S::NJ;   // 32-row A / B blocks of a wave
+  // gate/up: the weights are the MFMA's rows (epilogue4_swiglu)
+  constexpr bool kTrans = EPI == EPI_SWIGLU_MX4;
   __shared__ __attribute__((aligned(1024))) char sA0[kTileBytes];
   __shared__ __attribute__((aligned(1024))) char sB0[kTileBytes];
   __shared__ __attribute__((aligned(1024))) char sA1[kTileBytes];
@@ -194,8 +287,12 @@ __global__ __launch_bounds__(kThreads8) void grouped_gemm_w8f4_kernel(
                                                 4, 5, 6, 7);
       const i32x8_t b = __builtin_shufflevector(f.b[j], i32x4_t{}, 0, 1, 2, 3,
                                                 4, 5, 6, 7);
-      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-          a, b, acc[i][j], 4, 4, KK, (int)sa[i], KK, (int)sb[j]);
+      if constexpr (kTrans)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            b, a, acc[i][j], 4, 4, KK, (int)sb[j], KK, (int)sa[i]);
+      else
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            a, b, acc[i][j], 4, 4, KK, (int)sa[i], KK, (int)sb[j]);
     }
   };
   using I0 = integral_constant<int, 0>;
@@ -303,17 +400,19 @@ __global__ __launch_bounds__(kThreads8) void grouped_gemm_w8f4_kernel(
   if (act) run(rstep);
   else run(rstep_idle);
 
-  // every wave is past its last read of the buffers (and every direct load
-  // has landed) before they become epilogue staging: 16 KiB per wave
-  __syncthreads();
-  if (!act) return;
-  char* wbuf = (wave < 2 ? sA0 : wave < 4 ? sB0 : wave < 6 ? sA1 : sB1) +
-               (wave & 1) * (kTileBytes / 2);
-  if constexpr (EPI == EPI_STORE)
+  if constexpr (EPI == EPI_SWIGLU_MX4) {
+    // (no wave ends with a direct load in flight)
+    __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0)
+    if (act) epilogue4_swiglu(p, tc, acc, n0, wm, wn, lane);
+  } else {
+    // every wave is past its last read of the buffers (and every direct load
+    // has landed) before they become epilogue staging: 16 KiB per wave
+    __syncthreads();
+    if (!act) return;
+    char* wbuf = (wave < 2 ? sA0 : wave < 4 ? sB0 : wave < 6 ? sA1 : sB1) +
+                 (wave & 1) * (kTileBytes / 2);
     epilogue_w8_store<RAGGED_M>(p, tc, acc, n0, wm, wn, lane, wbuf);
-  else   // routing weights in the fifth buffer (64 floats per wave)
-    epilogue_w8_swiglu<EPI>(p, tc, acc, n0, wm, wn, lane, wave, wbuf,
-                            reinterpret_cast<float*>(sX4) + 64 * wave);
+  }
 }
 
 template <int EPI>
