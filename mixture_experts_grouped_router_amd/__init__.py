@@ -265,11 +265,12 @@ def _context(device: torch.device) -> int:
 # the current stream's handle without building a torch.cuda.Stream object
 # (2.6 us of a 10 us call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream() -> int:
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_raw_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -280,7 +281,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 def _need(t: torch.Tensor, dtype, shape, name: str) -> None:
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    # (a torch.Size equals a tuple; copies only where they differ)
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a device tensor")
@@ -303,6 +305,14 @@ def _out_or_new(out: Optional[torch.Tensor], shape, dtype,
     if out is None:
         return torch.empty(shape, dtype=dtype, device=dev)
     _need_on(dev, out, dtype, shape, "out")
+    return out
+
+
+def _out_like(out: Optional[torch.Tensor], x: torch.Tensor) -> torch.Tensor:
+    """_out_or_new of contiguous x's shape and type."""
+    if out is None:
+        return torch.empty_like(x)
+    _need_on(x.device, out, x.dtype, x.shape, "out")
     return out
 
 
@@ -1129,8 +1139,8 @@ def mxfp4_quantize(src: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     if cols % 32:
         raise ValueError("the last dimension must be a multiple of 32")
     dev = src.device
-    codes = torch.empty(lead + (cols // 2,), dtype=torch.uint8, device=dev)
-    scales = torch.empty(lead + (cols // 32,), dtype=torch.uint8, device=dev)
+    codes = src.new_empty(lead + (cols // 2,), dtype=torch.uint8)
+    scales = src.new_empty(lead + (cols // 32,), dtype=torch.uint8)
     rows = src.numel() // cols if cols else 0
     _check(load_library().mxfp4_quantize(_context(dev), _ptr(src), rows, cols,
                                          _ptr(codes), _ptr(scales),
@@ -1222,7 +1232,7 @@ def moe_layer_few(x: torch.Tensor, w_gu: Optional[torch.Tensor] = None,
         _need_on(dev, w_dn, torch.bfloat16, (E, H, F), "w_dn")
         a.w_gu, a.w_dn = _ptr(w_gu), _ptr(w_dn)
     _need_on(dev, residual, torch.bfloat16, (T, H), "residual")
-    y = _out_or_new(out, (T, H), torch.bfloat16, dev)
+    y = _out_like(out, x)
     a.x, a.w_r, a.router_bias = _ptr(x), _ptr(w_r), _ptr(router_bias)
     a.topk_idx, a.topk_w = _ptr(topk_idx), _ptr(topk_w)
     a.residual, a.y = _ptr(residual), _ptr(y)
@@ -1257,11 +1267,12 @@ def moe_layernorm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     dev = x.device
     _need_on(dev, weight, torch.float32, (H,), "weight")
     _need_on(dev, bias, torch.float32, (H,), "bias")
-    y = _out_or_new(out, (T, H), torch.bfloat16, dev)
+    y = _out_like(out, x) if x.dtype == torch.bfloat16 else \
+        _out_or_new(out, (T, H), torch.bfloat16, dev)
     mean = rstd = None
     if save:
         mean = torch.empty(T, dtype=torch.float32, device=dev)
-        rstd = torch.empty(T, dtype=torch.float32, device=dev)
+        rstd = torch.empty_like(mean)
     _check(load_library().moe_layernorm_fwd(
         _context(dev), _ptr(x), int(x.dtype == torch.float32), _ptr(weight),
         _ptr(bias), T, H, float(eps), _ptr(y), _ptr(mean), _ptr(rstd),
@@ -1291,9 +1302,12 @@ def moe_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
     _need_on(dev, dresidual, x.dtype, (T, H), "dresidual")
     if not (want_dx or want_dw or want_db):
         raise ValueError("no gradient asked for")
-    dx = _out_or_new(out, (T, H), x.dtype, dev) if want_dx else None
+    dx = _out_like(out, x) if want_dx else None
     dw = torch.empty(H, dtype=torch.float32, device=dev) if want_dw else None
-    db = torch.empty(H, dtype=torch.float32, device=dev) if want_db else None
+    db = None
+    if want_db:
+        db = torch.empty(H, dtype=torch.float32, device=dev) \
+            if dw is None else torch.empty_like(dw)
     lib = load_library()
     n = _c_sz(0)
     _check(lib.moe_layernorm_bwd_workspace_size(
