@@ -55,7 +55,7 @@ constexpr int kFuseTopk = 4;
 // work-groups per CU, which needs no sums between waves.  Whole items against
 // shared ones, layer's time:
 //   MXFP4, 128 experts, 2048 x 768: 2 tokens (768 items) 20.4 us against
-//     18.4, 8 tokens (3072) 36.3 / 35.3, 12 tokens (4608) 44.8 / 45.4, 16
+//     18.4, 8 tokens 36.3 / 35.3, 12 tokens (4608) 44.8 / 45.4, 16
 //     tokens (6144) 53.4 / 58.4, 64 tokens 100 / 105; eight experts, 4096 x
 //     14336, one token (1792) 141 / 134
 //   bf16, 128 experts: one token 28.7 / 27.8, 8 tokens 121.9 / 119.0, 32
