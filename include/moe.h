@@ -822,7 +822,8 @@ moe_status_t mxfp4_dequantize(moe_ctx_t ctx, const uint8_t* codes,
  * router_bias summed in float64 and rounded to float32, then the rule of
  * moe_route_topk with `renormalize`.  Without w_r they are inputs (from
  * moe_route_scored, say); an expert may be named twice by a token, an id
- * outside [0, E) is skipped and recorded as MOE_DEVERR_EXPERT_ID.
+ * outside [0, E) is skipped, its weight unread, and recorded as
+ * MOE_DEVERR_EXPERT_ID.
  * Weights: MOE_PREC_BF16 (w_gu, w_dn) or MOE_PREC_MXFP4 (w_gu_q / w_gu_s /
  * w_dn_q / w_dn_s as mxfp4_quantize returns them, x and a stay bf16).
  * Limits: T <= MOE_FEW_MAX_TOKENS; H and F multiples of 8 (MXFP4: of 32); an

@@ -588,14 +588,23 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(
   float* head = z + P * kRows;                      // [waves][kCols][8]
   int* ent = reinterpret_cast<int*>(head + kDownWaves * kCols * kRows);
   int* lst = ent + P;
-  int* hent = lst + P;                              // [waves] entry or -1
+  float* wt = reinterpret_cast<float*>(lst + P);    // [P] routing weights
+  int* hent = reinterpret_cast<int*>(wt + P);       // [waves] entry or -1
   const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
   const int n = uniform(p.plan[0]);
   for (int i = t; i < P; i += kThreads) {
     ent[i] = p.plan[4 + i];
     lst[i] = p.plan[4 + P + i];
+    // (a skipped pair's z stays zero and its weight may be anything)
+    wt[i] = (uint32_t)p.idx[i] < (uint32_t)p.E ? p.w[i] : 0.0f;
   }
   for (int i = t; i < P * kRows; i += kThreads) z[i] = 0.0f;
+  // thread t's output at the end: row r of token tok
+  static_assert(kThreads >= kFewMaxTokens * kRows, "an output per thread");
+  const int tok = t / kRows, r = t % kRows;
+  const int64_t at_y = (int64_t)tok * p.H + blockIdx.x * kRows + r;
+  const float res =
+      p.res && tok < p.T ? bf16_to_f32(p.res[at_y]) : 0.0f;
   __syncthreads();
 
   const int row = (lane & 15) >> 1;
@@ -706,13 +715,11 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(
     }
   }
   __syncthreads();
-  for (int o = t; o < p.T * kRows; o += kThreads) {
-    const int tok = o / kRows, r = o % kRows;
-    const int64_t at_y = (int64_t)tok * p.H + h0 + r;
+  if (t < p.T * kRows) {
     float v = 0.0f;
     for (int j = 0; j < p.k; ++j)
-      v = fmaf(p.w[tok * p.k + j], z[(tok * p.k + j) * kRows + r], v);
-    if (p.res) v += bf16_to_f32(p.res[at_y]);
+      v = fmaf(wt[tok * p.k + j], z[(tok * p.k + j) * kRows + r], v);
+    if (p.res) v += res;
     p.y[at_y] = (uint16_t)f32_to_bf16(v);
   }
 }
@@ -793,8 +800,8 @@ hipError_t launch_experts(const FewParams& p, hipStream_t stream) {
   KernelScope ks("few_down", stream);
   auto* down = &few_down_kernel<FMT, CT, NS, UD>;
   const size_t lds = ((size_t)P * kRows + kDownWaves * CT * NS * kRows +
-                      2 * P + kDownWaves) * 4;
-  if (lds > 65536) {   // (more than 1300 pairs)
+                      3 * P + kDownWaves) * 4;
+  if (lds > 65536) {   // (more than about 1300 pairs)
     const hipError_t e = hipFuncSetAttribute(
         reinterpret_cast<const void*>(down),
         hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);

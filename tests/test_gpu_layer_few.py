@@ -185,6 +185,19 @@ def test_repeated_and_bad_ids(m, T, fmt):
     assert m.check_device_status() == 1
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_weights_of_skipped_pairs_are_not_used(m, fmt):
+    """Padding by ids outside [0, E), whose weights may be anything."""
+    d = make(7, 64, 64, 5, 3, 19)
+    d["idx"][2] = [-1, 4, 5]
+    d["w"][2] = [np.nan, 0.5, np.inf]
+    d["idx"][5] = -1
+    d["w"][5] = [np.inf, -np.inf, np.nan]
+    y = check(m, d, fmt)["y"]
+    assert torch.equal(y[5], bf(d["res"])[5])
+    assert m.check_device_status() == 1
+
+
 def test_infinite_and_nan_weights_stay_with_their_tokens(m):
     d = make(6, 64, 64, 5, 1, 9)
     d["idx"][:, 0] = [0, 1, 2, 0, 1, 3]
