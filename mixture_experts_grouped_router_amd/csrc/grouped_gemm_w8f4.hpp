@@ -325,7 +325,8 @@ __global__ __launch_bounds__(kThreads8) void grouped_gemm_w8f4_kernel(
     mma(I0{}, f0, I0{}, I8{});
     sched_vmem_reads_mfma<4, 6, 8, 1>();
     __builtin_amdgcn_sched_barrier(0);
-    // (the scales a slice later: 1640 -> 1597 us, Mixtral-shaped MLP)
+    // (the scales a slice later: 1640 -> 1597 us, Mixtral-shaped MLP; two
+    // steps' scales in one load of eight bytes: no gain, 1553 -> 1559)
     load_scales(min(k + 1, nk - 1));
     read(f0, a, b, 2);
     mma(I1{}, f1, I0{}, I8{});
