@@ -1217,25 +1217,23 @@ def moe_layer_few(x: torch.Tensor, w_gu: Optional[torch.Tensor] = None,
         _need_on(dev, topk_w, torch.float32, (T, k), "topk_w")
     _need_i32(T, H, F, E)
     _need_i32(k, int(precision))
-    a = _LayerFewArgs()
-    a.T, a.H, a.F, a.E, a.k = T, H, F, E, k
-    a.precision, a.renormalize = int(precision), int(bool(renormalize))
     if mx4:
         _need_mx(w_gu_q, (E, 2 * F, H), 2, dev, "w_gu_q")
         _need_mx(w_dn_q, (E, H, F), 2, dev, "w_dn_q")
-        a.w_gu_q, a.w_gu_s = _ptr(w_gu_q[0]), _ptr(w_gu_q[1])
-        a.w_dn_q, a.w_dn_s = _ptr(w_dn_q[0]), _ptr(w_dn_q[1])
+        # (w_gu, w_dn, then codes and scales)
+        weights = (None, None, _ptr(w_gu_q[0]), _ptr(w_gu_q[1]),
+                   _ptr(w_dn_q[0]), _ptr(w_dn_q[1]))
     else:
         if w_gu_q is not None or w_dn_q is not None:
             raise ValueError("quantised weights need PREC_MXFP4")
         _need_on(dev, w_gu, torch.bfloat16, (E, 2 * F, H), "w_gu")
         _need_on(dev, w_dn, torch.bfloat16, (E, H, F), "w_dn")
-        a.w_gu, a.w_dn = _ptr(w_gu), _ptr(w_dn)
+        weights = (_ptr(w_gu), _ptr(w_dn), None, None, None, None)
     _need_on(dev, residual, torch.bfloat16, (T, H), "residual")
     y = _out_like(out, x)
-    a.x, a.w_r, a.router_bias = _ptr(x), _ptr(w_r), _ptr(router_bias)
-    a.topk_idx, a.topk_w = _ptr(topk_idx), _ptr(topk_w)
-    a.residual, a.y = _ptr(residual), _ptr(y)
+    a = _LayerFewArgs(T, H, F, E, k, int(precision), int(bool(renormalize)),
+                      _ptr(x), _ptr(w_r), _ptr(router_bias), _ptr(topk_idx),
+                      _ptr(topk_w), *weights, _ptr(residual), _ptr(y))
     lib = load_library()
     n = _c_sz(0)
     _check(lib.moe_layer_few_workspace_size(ctypes.byref(a), ctypes.byref(n)))
