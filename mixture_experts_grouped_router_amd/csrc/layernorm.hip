@@ -16,6 +16,10 @@
 // Work-groups are persistent: weights are read once per lane, not once per
 // row, and the backward keeps one sum of dw and db per lane over all of its
 // rows; a second launch adds the work-groups' sums in their order.
+//
+// Measured: forward 16384 x 2048 bf16 25.7 us (5.2 TB/s); backward 32768 x
+// 2048 bf16 with a residual's gradient 93 + 5.6 us (5.8 TB/s); 1001 x 1035
+// float32 10.4 + 4.6; one row of 2048 forward 2.2.
 #include <algorithm>
 
 #include "common.hpp"

@@ -17,6 +17,9 @@
 // from the caches again.  An item is 8 RS weight rows of one entry; each
 // wave takes an equal run of the items and keeps two batches of loads going
 // across them.
+//
+// Measured, 77 tokens x 8 over 128 experts, 2048 x 768: gate/up 44.6 us (4.8
+// TB/s), down 25.6 (4.2), entries and x 4.7.
 #include <algorithm>
 
 #include "common.hpp"
