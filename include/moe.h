@@ -635,6 +635,10 @@ moe_status_t moe_fp8_tensor_quantize(moe_ctx_t ctx, const void* src,
  * same way for the down GEMM; h1_save / a_save hold the bf16 values.
  * x_perm_scale, w_gu_s and w_dn_s must be NULL; the weights may come
  * pre-quantised (w_gu_q + w_gu_ts, w_dn_q + w_dn_ts, below).
+ * MXFP4 (MOE_PREC_MXFP4, forward only): as MXFP8 with the elements and scales
+ * of mxfp4_quantize, x_perm and W_gu along H, a (from float32) and W_dn along
+ * F.  NaN or infinity in x_perm, in a weight or in a makes NaN of the outputs
+ * that its block reaches, and of no others.
  * Sizes: 1 <= E <= 1024; H and F multiples of 64 (bf16) or 128 (8-bit);
  * one expert's operands must stay below 4 GiB (byte offsets are 32-bit).
  * Errors: MOE_ERR_INVALID_ARG (null required pointer, bad sizes),
@@ -787,13 +791,15 @@ moe_status_t moe_grouped_mlp_bwd(moe_ctx_t ctx, const moe_mlp_bwd_args* args,
  * mxfp4_quantize: s = floor(log2 amax) - 2 clamped to [-127, 127] (-127 for
  * an all-zero block), scale byte s + 127; element = v 2^-s rounded to the
  * nearest E2M1 value (ties to the even code), magnitudes beyond 6 become 6,
- * a zero keeps its sign.  Code bit 3 is the sign; element 2 i of a row is
- * the low half of byte i.  src: bf16 [rows, cols], finite, cols % 32 == 0;
+ * a zero keeps its sign.  A block that holds NaN or infinity gets the scale
+ * byte 255 (NaN); its codes mean nothing.  Code bit 3 is the sign; element
+ * 2 i of a row is the low half of byte i.  src: bf16 [rows, cols], cols % 32
+ * == 0;
  * codes uint8 [rows, cols / 2] (16-byte aligned); scales uint8 [rows,
  * cols / 32].
  * mxfp4_dequantize: dst bf16 [rows, cols] = element 2^(scale - 127), exact
- * (magnitudes past the bf16 range become infinite).  A scale byte of 255
- * stands for no number: its block's values are undefined.
+ * (magnitudes past the bf16 range become infinite); NaN under the scale byte
+ * 255.
  * Errors: MOE_ERR_INVALID_ARG (negative size, null pointer),
  * MOE_ERR_UNSUPPORTED (cols % 32, alignment, rows * cols >= 2^62),
  * MOE_ERR_HIP.

@@ -3,14 +3,18 @@
 // the low half).  Scale exponent s = floor(log2 amax) - 2 clamped to
 // [-127, 127] (an all-zero block: -127), scale byte s + 127; elements v 2^-s
 // to the nearest E2M1 value, ties to the even code, magnitudes beyond 6 to
-// 6, the sign kept on zero.
+// 6, the sign kept on zero.  A block that holds NaN or infinity has the scale
+// byte 255, E8M0's NaN, which the conversions back and the scaled MFMAs carry
+// on (both measured on the device); its codes mean nothing.
 #pragma once
 #include "common.hpp"
 
 namespace moe {
 
-// floor(log2 amax) - 2, clamped, from the bf16 / float32 pattern of a finite
-// amax with the sign cleared
+// floor(log2 amax) - 2, clamped, from the bf16 / float32 pattern of amax with
+// the sign cleared (as integers, NaN and infinity are above every finite
+// magnitude); no finite amax: 128, scale byte 255
+constexpr int kMx4NaN = 128;
 MOE_HD inline int mx4_clamp(int fl) {
   const int s = fl - 2;
   return s < -127 ? -127 : (s > 127 ? 127 : s);
@@ -19,12 +23,12 @@ MOE_HD inline int mx4_exp_from_bf16_amax(uint32_t a) {
   const int be = (int)((a >> 7) & 0xFF);
   // subnormal: man 2^-133; zero gives -133, clamped
   const int msb = 31 - moe_clz32((a & 0x7Fu) | 1u);
-  return mx4_clamp(be != 0 ? be - 127 : msb - 133);
+  return be == 255 ? kMx4NaN : mx4_clamp(be != 0 ? be - 127 : msb - 133);
 }
 MOE_HD inline int mx4_exp_from_f32_amax(uint32_t a) {
   const int be = (int)((a >> 23) & 0xFF);
   const int msb = 31 - moe_clz32((a & 0x7FFFFFu) | 1u);
-  return mx4_clamp(be != 0 ? be - 127 : msb - 149);
+  return be == 255 ? kMx4NaN : mx4_clamp(be != 0 ? be - 127 : msb - 149);
 }
 
 // Scales in the layout of the 4-bit GEMM: rows r with K values each, nks =
@@ -69,7 +73,8 @@ __device__ __forceinline__ uint32_t e2m1x8_f32(const float (&v)[8],
   return r;
 }
 
-// scale byte -> float (0: the subnormal 2^-127; 255 has no finite value)
+// scale byte -> float (0: the subnormal 2^-127; 255: the exponent that the
+// conversions take for NaN)
 __device__ __forceinline__ float mx4_scale_of(uint32_t byte) {
   return byte ? __uint_as_float(byte << 23) : __uint_as_float(0x00400000u);
 }
