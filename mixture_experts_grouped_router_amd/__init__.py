@@ -939,7 +939,7 @@ def moe_grouped_mlp_fwd(x_perm: torch.Tensor, w_gu: Optional[torch.Tensor],
     else:
         _need(x_perm, torch.uint8, (rows, H // 2 if mx4 else H), "x_perm")
         _need(x_perm_scale, torch.uint8, (rows, H // 32), "x_perm_scale")
-    if precision == PREC_MXFP8 and w_gu is None:
+    if precision == PREC_MXFP8 and (w_gu is None or w_dn is None):
         _need_mx(w_gu_q, (E, 2 * F, H), 1, dev, "w_gu_q")
         _need_mx(w_dn_q, (E, H, F), 1, dev, "w_dn_q")
     if mx4:
