@@ -997,9 +997,7 @@ def moe_grouped_mlp_fwd(x_perm: torch.Tensor, w_gu: Optional[torch.Tensor],
     nbytes = _c_sz(0)
     _check(lib.moe_grouped_mlp_fwd_workspace_size(ctypes.byref(args),
                                                   ctypes.byref(nbytes)))
-    if ws is None or ws.numel() < int(nbytes.value):
-        ws = torch.empty(max(int(nbytes.value), 256), dtype=torch.uint8,
-                         device=dev)
+    ws = _workspace(ws, int(nbytes.value) or 256, dev)
     args.ws, args.ws_bytes = _ptr(ws), ws.numel()
     _check(lib.moe_grouped_mlp_fwd(_context(dev), ctypes.byref(args),
                                    _stream()))
@@ -1053,9 +1051,7 @@ def moe_expert_loop_mlp_fwd(x_perm: torch.Tensor, w_gu: torch.Tensor,
     nbytes = _c_sz(0)
     _check(lib.moe_expert_loop_mlp_fwd_workspace_size(ctypes.byref(args),
                                                       ctypes.byref(nbytes)))
-    if ws is None or ws.numel() < int(nbytes.value):
-        ws = torch.empty(max(int(nbytes.value), 256), dtype=torch.uint8,
-                         device=dev)
+    ws = _workspace(ws, int(nbytes.value) or 256, dev)
     args.ws, args.ws_bytes = _ptr(ws), ws.numel()
     _check(lib.moe_expert_loop_mlp_fwd(_context(dev), ctypes.byref(args),
                                        _stream()))
@@ -1116,9 +1112,7 @@ def moe_grouped_mlp_bwd(dz_perm: torch.Tensor, x_perm: torch.Tensor,
     nbytes = _c_sz(0)
     _check(lib.moe_grouped_mlp_bwd_workspace_size(ctypes.byref(args),
                                                   ctypes.byref(nbytes)))
-    if ws is None or ws.numel() < int(nbytes.value):
-        ws = torch.empty(max(int(nbytes.value), 256), dtype=torch.uint8,
-                         device=dev)
+    ws = _workspace(ws, int(nbytes.value) or 256, dev)
     args.ws, args.ws_bytes = _ptr(ws), ws.numel()
     _check(lib.moe_grouped_mlp_bwd(_context(dev), ctypes.byref(args),
                                    _stream()))

@@ -1,7 +1,7 @@
-"""CPU checks of what moe_grouped_mlp_fwd's binding hands to the library:
-quantised weights that replace bf16 ones have the sizes that the kernels read.
-Meta tensors stand for device tensors; the library is replaced by a
-recorder."""
+"""CPU checks of what the expert MLP's binding hands to the library:
+quantised weights that replace bf16 ones have the sizes that the kernels read,
+and a workspace is the caller's only where it can serve as one.  Meta tensors
+stand for device tensors; the library is replaced by a recorder."""
 import ctypes
 
 import pytest
@@ -25,9 +25,14 @@ class Recorder:
         n._obj.value = NEED
         return 0
 
+    moe_expert_loop_mlp_fwd_workspace_size = \
+        moe_grouped_mlp_bwd_workspace_size = moe_grouped_mlp_fwd_workspace_size
+
     def moe_grouped_mlp_fwd(self, ctx, args, stream):
         self.args = args._obj
         return 0
+
+    moe_expert_loop_mlp_fwd = moe_grouped_mlp_bwd = moe_grouped_mlp_fwd
 
 
 @pytest.fixture
@@ -76,3 +81,37 @@ def test_codes_in_place_of_weights(lib, prec, per, given):
         with pytest.raises((ValueError, TypeError)):
             call(prec, given, bad)
     assert lib.args is None
+
+
+X, OFF = t(BF, ROWS, H), t(I32, E + 1)
+CALLS = {
+    "mxfp4": lambda ws: call(m.PREC_MXFP4, (None, None), codes(2), ws=ws),
+    "bf16": lambda ws: call(m.PREC_BF16, ("gu", "dn"), {}, ws=ws),
+    "loop": lambda ws: m.moe_expert_loop_mlp_fwd(
+        X, WEIGHTS["gu"], WEIGHTS["dn"], OFF, ws=ws),
+    "backward": lambda ws: m.moe_grouped_mlp_bwd(
+        X, X, WEIGHTS["gu"], WEIGHTS["dn"], OFF, t(BF, ROWS, 2 * F),
+        t(BF, ROWS, F), ws=ws)}
+
+
+@pytest.mark.parametrize("entry", CALLS)
+@pytest.mark.parametrize("ws", [
+    t(U8, NEED - 1), t(U8, 2 * NEED)[::2], t(F32, NEED),
+    torch.empty(2 * NEED, dtype=U8)])
+def test_unfit_workspaces_are_not_used(lib, monkeypatch, ws, entry):
+    """Too small, strided, of another type, on another device: another one
+    takes its place."""
+    sent = []
+    monkeypatch.setattr(m, "_ptr", lambda x: sent.append(x) or 0)
+    CALLS[entry](ws)
+    assert not any(x is ws for x in sent)
+    assert lib.args.ws_bytes >= NEED
+
+
+@pytest.mark.parametrize("entry", CALLS)
+def test_a_fitting_workspace_is_used(lib, monkeypatch, entry):
+    sent = []
+    monkeypatch.setattr(m, "_ptr", lambda x: sent.append(x) or 0)
+    ws = t(U8, NEED)
+    CALLS[entry](ws)
+    assert any(x is ws for x in sent) and lib.args.ws_bytes == NEED
