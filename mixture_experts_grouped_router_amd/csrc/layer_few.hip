@@ -27,9 +27,9 @@
 // costs less than a launch of its own; one of them leaves the plan for the
 // second product.
 //
-// Launches: router logits (if asked for; with more than kFuseTopk tokens
-// also moe_route_topk's kernel, below that every work-group picks the
-// experts for itself), gate/up, down with the combine.
+// Launches: router logits (if asked for; then moe_route_topk's kernel, or,
+// with few tokens over few experts, every work-group picks the experts for
+// itself, few_plan.hpp), gate/up, down with the combine.
 //
 // Measured, weights from HBM: one token of 128 experts of 2048 x 768, k 8,
 // bf16, with the router 27.7 us (logits 4, gate/up 14.4 = 3.5 TB/s, down
@@ -38,6 +38,7 @@
 #include <algorithm>
 
 #include "common.hpp"
+#include "few_plan.hpp"
 #include "few_tile.hpp"
 #include "kernels.hpp"
 #include "lanes.hpp"
@@ -50,10 +51,6 @@ namespace {
 constexpr int32_t kDevErrExpertId = 1;   // include/moe.h MOE_DEVERR_*
 constexpr int32_t kDevErrLogits = 3;
 constexpr int kMaxPairs = kFewMaxTokens * 32;   // MOE_MAX_TOPK
-// Tokens whose experts every work-group picks for itself; with a launch of
-// its own one token takes 34.1 us for 27.8, two 52.9 for 48.6, four 77.8 for
-// 77.5 (128 experts, 2048 x 768, bf16).
-constexpr int kFuseTopk = 4;
 // Gate/up: four waves share each item and the grid is at most three
 // work-groups per CU (the register file's limit), which keeps the fewest
 // work-groups waiting at the end; or a wave takes whole items, with two
@@ -321,7 +318,8 @@ __device__ __forceinline__ void pick_experts(const FewParams& p, PlanLds& s,
     __syncthreads();
   }
   if (!out) return;
-  const int tok = t >> 6;   // kFuseTopk = 4 tokens, four waves
+  static_assert(kFuseTokens <= 4, "a wave per token");
+  const int tok = t >> 6;
   if (tok >= p.T) return;
   const float* row = p.logits + (int64_t)tok * E;
   const double top = (double)row[s.sidx[tok * k]];
@@ -442,8 +440,9 @@ __global__ __launch_bounds__(256) void few_gate_up_kernel(FewParams p) {
   __shared__ PlanLds s;
   // the picked experts' keys; then the four waves' sums, two turns
   constexpr int kRed = KS > 1 ? 2 * 4 * RS * NS * 64 : 0;
+  constexpr int kKeys = kFuseExperts + 2;
   __shared__ __attribute__((aligned(16))) uint64_t
-      scratch[kRed / 2 > 1026 ? kRed / 2 : 1026];
+      scratch[kRed / 2 > kKeys ? kRed / 2 : kKeys];
   const int n = build_plan(p, s, scratch, B::kCols);
   const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
   const int row = (lane & 15) >> 1;
@@ -862,7 +861,7 @@ hipError_t launch_layer_few(const LayerFew& a, hipStream_t stream) {
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
-    if (a.T <= kFuseTopk) {
+    if (few_fuse_topk(a.T, a.E)) {
       p.logits = logits;
     } else {
       const hipError_t e =
