@@ -3,6 +3,8 @@
 #pragma once
 #include <stdint.h>
 
+#include <algorithm>
+
 namespace moe {
 
 // Every work-group of the first product picks the experts for itself instead
@@ -26,6 +28,65 @@ constexpr int kFuseExperts = 256;
 constexpr int kFuseLogits = 512;
 inline bool few_fuse_topk(int T, int E) {
   return T <= kFuseTokens && E <= kFuseExperts && T * E <= kFuseLogits;
+}
+
+// The products' kernels.  words: MXFP4 scales are read as dwords.  ct, ns: an
+// entry has up to ns sets of ct pairs.  whole: a wave takes whole items of
+// the gate/up product, instead of four waves sharing each; groups:
+// work-groups of that product.
+struct FewForm {
+  bool words;
+  int ct, ns;
+  bool whole;
+  int groups;
+};
+
+// Columns of an entry: twice the mean of an expert's pairs (never more than
+// the tokens); the few experts that exceed it make another entry.  MXFP4,
+// Qwen3-shaped, one call: 8 tokens 35.0 us with two columns, 38.7 with four,
+// 39.2 with eight; 16 tokens 50.7 / 50.4 / 52.3; 32 tokens 76.5 / 72.7 / 71.5;
+// 64 tokens 125 / 103 / 100.  Mixtral-shaped, 32 tokens: eight columns 338 us,
+// sixteen 326.
+//
+// Gate/up: four waves share each item and the grid is at most three
+// work-groups per CU, which keeps the fewest work-groups waiting at the end;
+// or a wave takes whole items, with two work-groups per CU, which needs no
+// sums between waves.  Whole items against shared ones, layer's time:
+//   MXFP4, 128 experts, 2048 x 768: 2 tokens (768 items) 20.4 us against
+//     18.4, 8 tokens 36.3 / 35.3, 12 tokens (4608) 44.8 / 45.4, 16
+//     tokens (6144) 53.4 / 58.4, 64 tokens 100 / 105; eight experts, 4096 x
+//     14336, one token (1792) 141 / 134
+//   bf16, 128 experts: one token 28.7 / 27.8, 8 tokens 121.9 / 119.0, 32
+//     tokens 222 / 215, 64 tokens 255 / 248; eight experts, five tokens
+//     431 / 421; with two column sets (64 tokens) 684 / 767
+// so shared for bf16 with one column set and for fewer items than kWholeItems.
+constexpr int kWholeItems = 4096;
+inline FewForm few_form(int T, int H, int F, int E, int k, bool mx4,
+                        bool scale_dwords) {
+  const int most = std::min(T, std::max(1, 2 * T * k / E));
+  FewForm f{};
+  if (mx4) {
+    // (rows of whole dwords)
+    f.words = scale_dwords && H % 128 == 0 && F % 128 == 0;
+    if (!f.words) {
+      f.ct = T <= 2 ? 2 : 8;
+      f.ns = 1;
+    } else {
+      f.ct = most <= 3 || T <= 2 ? 2 : 8;
+      f.ns = most <= 1 || T <= 2 ? 1 : most <= 3 ? 2 : most <= 8 ? 1 : 2;
+    }
+  } else {
+    f.ct = 8;
+    f.ns = most <= 8 ? 1 : most <= 16 ? 2 : 4;
+  }
+  // items if every pair reached an expert of its own: 16 (bf16: eight) FFN
+  // columns of an expert
+  const int cols = mx4 ? 16 : 8;
+  const int64_t items =
+      (int64_t)std::min(T * k, E) * (((int64_t)F + cols - 1) / cols);
+  f.whole = items >= kWholeItems && (mx4 || f.ns > 1);
+  f.groups = f.whole ? 512 : (int)std::min<int64_t>(items, 768);
+  return f;
 }
 
 }  // namespace moe

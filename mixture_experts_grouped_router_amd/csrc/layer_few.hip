@@ -51,20 +51,6 @@ namespace {
 constexpr int32_t kDevErrExpertId = 1;   // include/moe.h MOE_DEVERR_*
 constexpr int32_t kDevErrLogits = 3;
 constexpr int kMaxPairs = kFewMaxTokens * 32;   // MOE_MAX_TOPK
-// Gate/up: four waves share each item and the grid is at most three
-// work-groups per CU (the register file's limit), which keeps the fewest
-// work-groups waiting at the end; or a wave takes whole items, with two
-// work-groups per CU, which needs no sums between waves.  Whole items against
-// shared ones, layer's time:
-//   MXFP4, 128 experts, 2048 x 768: 2 tokens (768 items) 20.4 us against
-//     18.4, 8 tokens 36.3 / 35.3, 12 tokens (4608) 44.8 / 45.4, 16
-//     tokens (6144) 53.4 / 58.4, 64 tokens 100 / 105; eight experts, 4096 x
-//     14336, one token (1792) 141 / 134
-//   bf16, 128 experts: one token 28.7 / 27.8, 8 tokens 121.9 / 119.0, 32
-//     tokens 222 / 215, 64 tokens 255 / 248; eight experts, five tokens
-//     431 / 421; with two column sets (64 tokens) 684 / 767
-// so shared for bf16 with one column set and for fewer items than this.
-constexpr int kWholeItems = 4096;
 
 struct FewParams {
   const char* x;            // bf16 [T, H]
@@ -781,23 +767,19 @@ __global__ __launch_bounds__(256) void few_logits_kernel(
 }
 
 // CT, NS: column sets; UG1 / UG4: chunks per batch of the gate/up product
-// with one and four waves per item, UD: of the down product
+// with one (0: never) and four waves per item, UD: of the down product
 template <class FMT, int CT, int NS, int UG1, int UG4, int UD>
-hipError_t launch_experts(const FewParams& p, hipStream_t stream) {
+hipError_t launch_experts(const FewParams& p, const FewForm& form,
+                          hipStream_t stream) {
   constexpr int RSF = FMT::kMfma > 1 ? 2 : 1;
   const int P = p.T * p.k;
   {
     KernelScope ks("few_gate_up", stream);
-    // items if every pair reached an expert of its own
-    const int64_t items = (int64_t)std::min(P, p.E) *
-                          ((p.F + kRows * RSF - 1) / (kRows * RSF));
-    if (items < kWholeItems || (FMT::kMfma == 1 && NS == 1))
-      hipLaunchKernelGGL((few_gate_up_kernel<FMT, CT, NS, RSF, 4, UG4>),
-                         dim3((unsigned)std::min<int64_t>(items, 768)),
-                         dim3(256), 0, stream, p);
-    else
-      hipLaunchKernelGGL((few_gate_up_kernel<FMT, CT, NS, RSF, 1, UG1>),
-                         dim3(512), dim3(256), 0, stream, p);
+    auto* gate_up = &few_gate_up_kernel<FMT, CT, NS, RSF, 4, UG4>;
+    if constexpr (UG1 > 0)
+      if (form.whole) gate_up = &few_gate_up_kernel<FMT, CT, NS, RSF, 1, UG1>;
+    hipLaunchKernelGGL(gate_up, dim3((unsigned)form.groups), dim3(256), 0,
+                       stream, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -888,31 +870,29 @@ hipError_t launch_layer_few(const LayerFew& a, hipStream_t stream) {
   p.E = a.E;
   p.k = a.k;
   p.status = a.status;
-  // Columns of an entry: twice the mean of an expert's pairs (never more than
-  // the tokens); the few experts that exceed it make another entry.  MXFP4,
-  // Qwen3-shaped, one call: 8 tokens 35.0 us with two columns, 38.7 with
-  // four, 39.2 with eight; 16 tokens 50.7 / 50.4 / 52.3; 32 tokens 76.5 /
-  // 72.7 / 71.5; 64 tokens 125 / 103 / 100.  Mixtral-shaped, 32 tokens: eight
-  // columns 338 us, sixteen 326.
-  const int most = std::min(a.T, std::max(1, 2 * a.T * a.k / a.E));
-  if (a.s_gu) {
-    const auto at = reinterpret_cast<uintptr_t>(a.s_gu) |
-                    reinterpret_cast<uintptr_t>(a.s_dn);
-    if (a.H % 128 != 0 || a.F % 128 != 0 || (at & 3) != 0) {
-      using Fmt = FmtMx4<false>;
-      return a.T <= 2 ? launch_experts<Fmt, 2, 1, 2, 1, 3>(p, stream)
-                      : launch_experts<Fmt, 8, 1, 2, 1, 3>(p, stream);
-    }
-    using Fmt = FmtMx4<true>;
-    return most <= 1 || a.T <= 2
-               ? launch_experts<Fmt, 2, 1, 2, 2, 3>(p, stream)
-           : most <= 3 ? launch_experts<Fmt, 2, 2, 2, 1, 3>(p, stream)
-           : most <= 8 ? launch_experts<Fmt, 8, 1, 2, 1, 3>(p, stream)
-                       : launch_experts<Fmt, 8, 2, 1, 1, 2>(p, stream);
+  const auto at = reinterpret_cast<uintptr_t>(a.s_gu) |
+                  reinterpret_cast<uintptr_t>(a.s_dn);
+  const FewForm form =
+      few_form(a.T, a.H, a.F, a.E, a.k, a.s_gu != nullptr, (at & 3) == 0);
+  if (a.s_gu && !form.words) {
+    using Fmt = FmtMx4<false>;
+    return form.ct == 2 ? launch_experts<Fmt, 2, 1, 2, 1, 3>(p, form, stream)
+                        : launch_experts<Fmt, 8, 1, 2, 1, 3>(p, form, stream);
   }
-  return most <= 8    ? launch_experts<FmtBf16, 8, 1, 4, 2, 4>(p, stream)
-         : most <= 16 ? launch_experts<FmtBf16, 8, 2, 4, 2, 4>(p, stream)
-                      : launch_experts<FmtBf16, 8, 4, 2, 2, 2>(p, stream);
+  if (a.s_gu) {
+    using Fmt = FmtMx4<true>;
+    return form.ct == 2
+               ? form.ns == 1
+                     ? launch_experts<Fmt, 2, 1, 2, 2, 3>(p, form, stream)
+                     : launch_experts<Fmt, 2, 2, 2, 1, 3>(p, form, stream)
+           : form.ns == 1
+               ? launch_experts<Fmt, 8, 1, 2, 1, 3>(p, form, stream)
+               : launch_experts<Fmt, 8, 2, 1, 1, 2>(p, form, stream);
+  }
+  return form.ns == 1 ? launch_experts<FmtBf16, 8, 1, 0, 2, 4>(p, form, stream)
+         : form.ns == 2
+             ? launch_experts<FmtBf16, 8, 2, 4, 2, 4>(p, form, stream)
+             : launch_experts<FmtBf16, 8, 4, 2, 2, 2>(p, form, stream);
 }
 
 }  // namespace moe

@@ -4,8 +4,9 @@ import numpy as np
 import pytest
 import torch
 
-from few_layer_shapes import PICKS
+from few_layer_shapes import FORMS, PICKS
 from oracle import moe_oracle as O
+import test_gpu_layer_few as few
 from test_gpu_layer_few import bf, check, make, up, weights
 
 pytestmark = pytest.mark.gpu
@@ -42,3 +43,27 @@ def test_picked_experts(m, T, E, k, renorm):
     given = m.moe_layer_few(bf(d["x"]), topk_idx=r["topk_idx"],
                             topk_w=r["topk_w"], **kw)
     assert torch.equal(r["y"], given["y"])
+
+
+@pytest.mark.parametrize("T,H,F,E,k,fmt,dwords", FORMS)
+def test_forms(m, T, H, F, E, k, fmt, dwords, monkeypatch):
+    """Experts as drawn, then with most pairs on one of them (it makes several
+    entries), one named twice by a token and one id that is none."""
+    d = make(T, H, F, E, k, 7 * T + F)
+    kw, gu, dn = weights(m, d, fmt)
+    if not dwords:
+        for n in ("w_gu_q", "w_dn_q"):
+            c, s = kw[n]
+            buf = torch.empty(s.numel() + 1, dtype=torch.uint8, device="cuda")
+            buf[1:] = s.reshape(-1)
+            kw[n] = (c, buf[1:].view(s.shape))
+    # (the oracle's weights once)
+    monkeypatch.setattr(few, "weights", lambda m, d, fmt: (dict(kw), gu, dn))
+    check(m, d, fmt)
+    d["idx"][: T // 2 + 1, 0] = E // 2
+    if k > 1:
+        d["idx"][T - 1, :2] = 0
+        d["idx"][T // 2, 1] = -1
+        d["w"][T // 2, 1] = np.nan
+    check(m, d, fmt, res=False)
+    assert m.check_device_status() == (1 if k > 1 else 0)
