@@ -69,11 +69,20 @@ struct RowsBatch {
   }
 };
 
+// Work-groups that a CU holds at once: the grids are whole rounds of them
+// (launch_mx4_few_rows), so the kernels are held to the registers that leaves
+// (unbounded, gate/up with two column sets took 290 of them and ran its grid in
+// two halves: 100 tokens x 8 over 128 experts 86.7 us, 73.3 now; with one
+// work-group per CU and a grid of those 79.7; 40 tokens x 2 Mixtral-shaped
+// 185.7 / 166.3 / 186.6).
+constexpr int few_rows_per_cu(bool gate_up) { return gate_up ? 2 : 3; }
+
 // GU: gate/up with the SwiGLU, the routing weight and A's quantisation; row
 // sets come in pairs (gate rows, up rows of the same eight f), RS = 8: the
 // 32 f of a quantisation block.  Else: down, bf16 outputs.  A wave per item.
 template <bool GU, int RS, int NS>
-__global__ __launch_bounds__(256) void mx4_few_rows_kernel(RowsParams p) {
+__global__ __launch_bounds__(256, few_rows_per_cu(GU)) void
+mx4_few_rows_kernel(RowsParams p) {
   static_assert(!GU || RS == 8, "a quantisation block per item");
   using B = RowsBatch<RS, NS>;
   const int lane = threadIdx.x & 63;
@@ -288,7 +297,9 @@ hipError_t launch_mx4_few_rows(const Mx4FewRows& a, hipStream_t stream) {
   // row sets and three work-groups per CU for down.  77 tokens x 8 over 128
   // experts, 2048 x 768: 75.9 us for the MLP; gate/up with three per CU 82.9;
   // down with two 80.7, with four 77.4, with eight row sets 80.9.
-  const dim3 block(256), gu_grid(512), dn_grid(768);
+  constexpr int kCus = 256;
+  const dim3 block(256), gu_grid(kCus * few_rows_per_cu(true)),
+      dn_grid(kCus * few_rows_per_cu(false));
   auto run = [&](auto ns) -> hipError_t {
     constexpr int NS = decltype(ns)::value;
     {
