@@ -20,12 +20,13 @@ namespace {
 
 // Rows per expert, on average, up to which the few-rows kernels run.  128
 // experts, 2048 x 768, few-rows kernels against tiled ones: 77 tokens x 8
-// (4.8 rows) 75.9 us against 108.0, 200 x 8 (12.5) 102 against 111, 256 x 8
-// (16) 125 against 112; eight experts, 4096 x 14336: 48 x 2 (12) 199 against
-// 227, 64 x 2 (16) 245 against 227.  The host knows the mean only: with all
-// rows on a few experts (192 x 8 on eight of 128) the few-rows kernels take
-// 68.5 us against 43.0.
-constexpr int kFewRows = 12;
+// (4.8 rows) 70.4 us against 101, 200 x 8 (12.5) 82.0 / 106, 256 x 8 (16)
+// 101 / 106, 288 x 8 (18) 110 / 107; eight experts, 4096 x 14336: 48 x 2
+// (12) 175 / 219, 64 x 2 (16) 201 / 220, 80 x 2 (20) 251 / 220; 32 experts,
+// 2048 x 1408: 120 x 4 (15) 46.8 / 47.6, 160 x 4 (20) 60.7 / 48.0.  The host
+// knows the mean only: with all rows on a few experts (192 x 8 on eight of
+// 128) the few-rows kernels take 50.6 us against 41.3.
+constexpr int kFewRows = 16;
 bool few_rows(int E, int64_t rows) { return rows <= (int64_t)kFewRows * E; }
 
 struct Mx4Ws {
