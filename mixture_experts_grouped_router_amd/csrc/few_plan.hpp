@@ -48,10 +48,9 @@ struct FewForm {
 // 64 tokens 125 / 103 / 100.  Mixtral-shaped, 32 tokens: eight columns 338 us,
 // sixteen 326.
 //
-// Gate/up: four waves share each item and the grid is at most three
-// work-groups per CU, which keeps the fewest work-groups waiting at the end;
-// or a wave takes whole items, with two work-groups per CU, which needs no
-// sums between waves.  Whole items against shared ones, layer's time:
+// Gate/up: four waves share each item, which keeps the fewest work-groups
+// waiting at the end, or a wave takes whole items, which needs no sums between
+// waves.  Whole items against shared ones, layer's time:
 //   MXFP4, 128 experts, 2048 x 768: 2 tokens (768 items) 20.4 us against
 //     18.4, 8 tokens 36.3 / 35.3, 12 tokens (4608) 44.8 / 45.4, 16
 //     tokens (6144) 53.4 / 58.4, 64 tokens 100 / 105; eight experts, 4096 x
@@ -61,6 +60,15 @@ struct FewForm {
 //     431 / 421; with two column sets (64 tokens) 684 / 767
 // so shared for bf16 with one column set and for fewer items than kWholeItems.
 constexpr int kWholeItems = 4096;
+
+// Work-groups of the gate/up product that a CU holds at once; its grid is one
+// round of them, each with an equal run of the items.  Shared items leave
+// registers for three, with the most columns for two (three to a CU made a
+// second round that left a third of the chip idle: eight experts, 4096 x 4096,
+// 36 tokens in MXFP4 106.9 us against 95.3, 2048 x 2048 in bf16 53.2 / 44.9).
+constexpr int few_per_cu(bool mx4, int ct, int ns, bool whole) {
+  return whole || ct * ns >= (mx4 ? 16 : 32) ? 2 : 3;
+}
 inline FewForm few_form(int T, int H, int F, int E, int k, bool mx4,
                         bool scale_dwords) {
   const int most = std::min(T, std::max(1, 2 * T * k / E));
@@ -85,7 +93,9 @@ inline FewForm few_form(int T, int H, int F, int E, int k, bool mx4,
   const int64_t items =
       (int64_t)std::min(T * k, E) * (((int64_t)F + cols - 1) / cols);
   f.whole = items >= kWholeItems && (mx4 || f.ns > 1);
-  f.groups = f.whole ? 512 : (int)std::min<int64_t>(items, 768);
+  constexpr int kCus = 256;
+  f.groups = (int)std::min<int64_t>(
+      items, kCus * few_per_cu(mx4, f.ct, f.ns, f.whole));
   return f;
 }
 

@@ -69,8 +69,10 @@ def test_every_form_is_there(plan):
 
 
 def test_work_groups(plan):
+    """One round of what the chip holds at once, at most an item each."""
     for s, g in zip(FORMS, ask_forms(plan, FORMS)):
         T, _, F, E, k, fmt, _ = s
         cols = 16 if fmt == "mxfp4" else 8
         items = min(T * k, E) * -(-F // cols)
-        assert g[4] == (512 if g[3] else min(items, 768))
+        full = g[1] * g[2] == (16 if fmt == "mxfp4" else 32)
+        assert g[4] == min(items, 256 * (2 if g[3] or full else 3))

@@ -41,3 +41,16 @@ def test_mxfp4_few_rows():
         for name, per_cu in (("true, 8", 2), ("false, 4", 3)):
             waves, scratch = k["mx4_few_rows_kernel<%s, %d>" % (name, ns)]
             assert waves >= per_cu and scratch == 0, (name, ns)
+
+
+def test_layer_few():
+    """The gate/up kernels: three work-groups per unit, two with a wave per
+    item or with the most columns (few_per_cu of few_plan.hpp)."""
+    k = {n: v for n, v in kernels("layer_few.hip").items()
+         if n.startswith("few_gate_up_kernel")}
+    assert len(k) == 17
+    for name, (waves, scratch) in k.items():
+        fmt, ct, ns, _, ks, _ = [a.strip() for a in
+                                 name[name.index("<") + 1:-1].rsplit(",", 5)]
+        full = int(ct) * int(ns) == (32 if "Bf16" in fmt else 16)
+        assert scratch == 0 and waves >= (2 if ks == "1" or full else 3), name
