@@ -10,16 +10,19 @@
 // registers, so the variance is the sum of squares around the mean (no
 // E[x^2] - mean^2 cancellation), and everything is float32.  A row belongs
 // to one wave (H <= 1024), four (H <= 4096), eight or sixteen (H <= 16384):
-// at most 16 values per lane, which leaves room for the backward's sums of
-// dw and db, its weights and the next row's loads with three or more waves
-// on a SIMD.
+// at most 16 values per lane, which leaves the forward four and more waves on
+// a SIMD, and the backward, with its sums of dw and db, its weights and the
+// next row's loads, three or more in bf16 and two or three in float32 with two
+// chunks per lane.  Sixteen waves per row leave 128 registers: there the
+// backward loads nothing ahead and up to 16 of its registers live in scratch.
 // Work-groups are persistent: weights are read once per lane, not once per
 // row, and the backward keeps one sum of dw and db per lane over all of its
 // rows; a second launch adds the work-groups' sums in their order.
 //
 // Measured: forward 16384 x 2048 bf16 25.7 us (5.2 TB/s); backward 32768 x
 // 2048 bf16 with a residual's gradient 93 + 5.6 us (5.8 TB/s); 1001 x 1035
-// float32 10.4 + 4.6; one row of 2048 forward 2.2.
+// float32 10.4 + 4.6; one row of 2048 forward 2.2; backward 4096 x 16384 (both
+// launches) bf16 97 us (4.2 TB/s), float32 158 (4.2).
 #include <algorithm>
 
 #include "common.hpp"
@@ -416,12 +419,23 @@ int ln_fwd_grid(int64_t T, int H) {
   return ln_grid(T, H, H <= 4096 ? 4 : H <= 8192 ? 2 : 1);
 }
 // The backward's work-groups each leave 2 H partial sums, so they are as few
-// as keep the loads going (32768 x 2048: one per CU 120.6 us, two 101.6,
-// three 106.1; 16384 x 4096: 96.5, 108.0, 112.9) and take four rows each at
-// least (512 x 2048: 9.3 us, with one row each 13.8).
+// as keep the loads going.  One, two or three per CU, both launches, us:
+//   bf16     65536 x 256 53.1, 37.1, 34.2; x 512 57.9, 44.1, 43.0; 16384 x 512
+//     19.7, 18.7, 20.0; 65536 x 768 73.1, 60.4, 62.4; 16384 x 1024 26.6, 28.0,
+//     29.6; 32768 x 2048 120.6, 101.6, 106.1; 16384 x 4096 82.9, 82.2, 86.9;
+//     8192 x 8192 81.2, 86.4, 91.4; 4096 x 16384 97.2, 106.4, 121
+//   float32  65536 x 256 60.9, 43.0, 40.7; 16384 x 512 23.0, 23.2, 25.2;
+//     16384 x 768 30.8, 32.4, 39.2; x 1024 34.0, 37.6, 44.7; 16384 x 2048
+//     72.5, 72.2, 73.4; x 4096 120.6, 133.7, 133.9; 8192 x 8192 133, 138, 145
+// They take four rows each at least.  Four, two or one, us: 512 x 2048 9.3,
+// 9.9, 13.7; 1001 x 2048 12.2, 16.0, 14.4; 1001 x 1035 14.3, 15.6, 14.2; 256 x
+// 8192 13.4, 13.6, 16.6; but 512 x 256 8.4, 6.7, 6.6; 64 x 2048 7.5, 6.8, 5.7;
+// 16 x 16384 15.2, 10.8, 9.4 (float32 21.6, 14.2, 11.1): right for rows wider
+// than 1024 from some 512 of them on, and for a few dozen rows up to half of
+// the time too long.
 int ln_bwd_grid(int64_t T, int H) {
   const int rows = ln_rows(ln_wpr(H)) * 4;
-  const int per_cu = H > 1024 && H <= 2048 ? 2 : 1;
+  const int per_cu = H <= 512 || (H > 1024 && H <= 2048) ? 2 : 1;
   return (int)std::min<int64_t>((T + rows - 1) / rows,
                                 (int64_t)kCus * per_cu);
 }
