@@ -676,7 +676,7 @@ typedef struct moe_mlp_fwd_args {
   void* z_perm;                  /* out: bf16 [rows, H] */
   void* h1_save;                 /* out, nullable: bf16 [rows, 2F] (g, u) */
   void* a_save;                  /* out, nullable: bf16 [rows, F] */
-  void* ws;                      /* workspace */
+  void* ws;                      /* workspace (MXFP4: 16-byte aligned) */
   size_t ws_bytes;
   /* MXFP8 only, out, nullable: A's E4M3 codes [rows, F] (16-byte aligned)
    * and E8M0 scales [rows, F/32] (row-major), as the down GEMM reads them */

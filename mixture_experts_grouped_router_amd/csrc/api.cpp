@@ -855,6 +855,9 @@ moe_status_t moe_grouped_mlp_fwd(moe_ctx_t ctx, const moe_mlp_fwd_args* a,
                 "w_dn_s or none");
     MOE_REQUIRE(aligned16(a->h1_save) && aligned16(a->a_save),
                 MOE_ERR_UNSUPPORTED, "saves must be 16-byte aligned");
+    // (codes and scales in it are read 16 and 4 bytes at a time)
+    MOE_REQUIRE(aligned16(a->ws), MOE_ERR_UNSUPPORTED,
+                "the workspace must be 16-byte aligned");
   }
   const bool preq = (mx || f8t || mx4) && a->w_gu_q != nullptr &&
                     a->w_dn_q != nullptr;

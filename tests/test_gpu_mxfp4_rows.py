@@ -36,3 +36,13 @@ def test_mlp(m, sizes, H, F):
     assert torch.equal(z[0], z[1]) and torch.equal(z[0], z[2])
     tiled = run(m, d, "codes", save=True)["z"]
     assert O.rel_err(host(tiled), ref) < 5e-3
+
+
+def test_misaligned_workspace_is_refused(m):
+    d = make([3, 40], 256, 128, 3)
+    ref = run(m, d, "codes")["z"]
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    for at in (1, 4, 8):
+        with pytest.raises(m.MoEError):
+            run(m, d, "codes", ws=ws[at:])
+    assert torch.equal(run(m, d, "codes", ws=ws[16:])["z"], ref)
