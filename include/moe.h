@@ -639,11 +639,14 @@ moe_status_t moe_fp8_tensor_quantize(moe_ctx_t ctx, const void* src,
  * of mxfp4_quantize, x_perm and W_gu along H, a (from float32) and W_dn along
  * F.  NaN or infinity in x_perm, in a weight or in a makes NaN of the outputs
  * that its block reaches, and of no others.
- * Sizes: 1 <= E <= 1024; H and F multiples of 64 (bf16) or 128 (8-bit);
+ * Up to sixteen rows per expert on average run on other kernels than more
+ * rows and than calls with h1_save or a_save: their sums have another order,
+ * and z may differ in its last bits between a call with saves and one without.
+ * Sizes: 1 <= E <= 1024; H and F multiples of 64 (bf16) or 128 (others);
  * one expert's operands must stay below 4 GiB (byte offsets are 32-bit).
  * Errors: MOE_ERR_INVALID_ARG (null required pointer, bad sizes),
  * MOE_ERR_UNSUPPORTED (size limits, misaligned pointers: operands 16-byte,
- * MXFP8 scale arrays 4-byte), MOE_ERR_WORKSPACE (ws NULL or smaller than
+ * MX scale arrays 4-byte), MOE_ERR_WORKSPACE (ws NULL or smaller than
  * moe_grouped_mlp_fwd_workspace_size), MOE_ERR_HIP.  The workspace is
  * scratch owned by the caller; its contents after the call are undefined
  * (besides tile tables and quantised operands it holds the float32 partial
@@ -833,7 +836,8 @@ moe_status_t mxfp4_dequantize(moe_ctx_t ctx, const uint8_t* codes,
  * Weights: MOE_PREC_BF16 (w_gu, w_dn) or MOE_PREC_MXFP4 (w_gu_q / w_gu_s /
  * w_dn_q / w_dn_s as mxfp4_quantize returns them, x and a stay bf16).
  * Limits: T <= MOE_FEW_MAX_TOKENS; H and F multiples of 8 (MXFP4: of 32); an
- * expert's W_gu in bf16 and all of a below 4 GiB.  y may be the residual.
+ * expert's W_gu in bf16 and all of a below 4 GiB, E (F + 16) <= 2^27 - 8.
+ * y may be the residual.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE,
  * MOE_ERR_HIP.
  * ---------------------------------------------------------------------- */

@@ -902,7 +902,7 @@ moe_status_t moe_grouped_mlp_fwd(moe_ctx_t ctx, const moe_mlp_fwd_args* a,
         xq ? static_cast<const uint8_t*>(a->x_perm) : nullptr,
         a->x_perm_scale, a->w_gu, a->w_dn, a->w_gu_q, a->w_gu_s, a->w_dn_q,
         a->w_dn_s, a->w_perm, a->offsets, a->z_perm, a->h1_save, a->a_save,
-        a->ws, ctx->cu_count, ctx->status, as_stream(stream));
+        a->ws, ctx->status, as_stream(stream));
   } else if (!mx) {
     e = moe::launch_mlp_fwd_bf16(a->E, a->H, a->F, a->rows, a->x_perm, a->w_gu,
                                  a->w_dn, a->w_perm, a->offsets, a->z_perm,
@@ -1216,8 +1216,9 @@ moe_status_t moe_layer_few_workspace_size(const moe_layer_few_args* a,
   const int q = a->precision == MOE_PREC_BF16 ? 8 : 32;
   MOE_REQUIRE(a->H % q == 0 && a->F % q == 0, MOE_ERR_UNSUPPORTED,
               "H and F must be multiples of %d", q);
-  // operands are addressed with 32-bit byte offsets; a launch holds fewer
-  // than 2^32 threads (32 per FFN column and expert)
+  // operands are addressed with 32-bit byte offsets; the gate/up items are
+  // numbered in 32 bits (at most 64 min(k, 32) entries of F / 8 tiles, which
+  // the last line keeps to 2^30)
   const int64_t lim = ((int64_t)1 << 32) - 256;
   MOE_REQUIRE((int64_t)a->F * 4 <= lim / a->H &&
                   (int64_t)MOE_FEW_MAX_TOKENS * a->H * 2 <= lim &&

@@ -82,8 +82,7 @@ hipError_t launch_mlp_fwd_mx4(int E, int H, int F, int64_t rows,
                               const uint8_t* w_dn_s, const float* w_perm,
                               const int32_t* offsets, void* z_perm,
                               void* h1_save, void* a_save, void* ws,
-                              int cu_count, int32_t* status,
-                              hipStream_t stream) {
+                              int32_t* status, hipStream_t stream) {
   if (rows == 0) return hipSuccess;
   const bool quant_x = xq == nullptr;
   const bool quant_w = w_gu_q == nullptr || w_dn_q == nullptr;

@@ -288,8 +288,7 @@ hipError_t launch_mlp_fwd_mx4(int E, int H, int F, int64_t rows,
                               const uint8_t* w_dn_s, const float* w_perm,
                               const int32_t* offsets, void* z_perm,
                               void* h1_save, void* a_save, void* ws,
-                              int cu_count, int32_t* status,
-                              hipStream_t stream);
+                              int32_t* status, hipStream_t stream);
 
 // the whole layer for a few tokens (layer_few.hip).  w_r null: topk_idx and
 // topk_w are inputs; s_gu / s_dn null: bf16 weights, else MXFP4 codes
