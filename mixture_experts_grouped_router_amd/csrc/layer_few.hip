@@ -31,10 +31,15 @@
 // with few tokens over few experts, every work-group picks the experts for
 // itself, few_plan.hpp), gate/up, down with the combine.
 //
+// a is rounded to bf16 because the second product multiplies bf16 (with
+// MXFP4 weights too, which are exact in it): 0.0023 of the outputs against 64
+// bits instead of the 0.0017 of y's own rounding, where no residual hides it.
+//
 // Measured, weights from HBM: one token of 128 experts of 2048 x 768, k 8,
-// bf16, with the router 27.7 us (logits 4, gate/up 14.4 = 3.5 TB/s, down
-// 7.4); 16 tokens in MXFP4 50.5 us (30.9 and 20.6: 4.1 and 3.0 TB/s); five
-// tokens of eight experts of 4096 x 14336, bf16: gate/up 6.1 TB/s, down 5.8.
+// bf16, with the router 24.2 us a call in a run of calls, 25.7 in a captured
+// one (kernels traced alone: logits 4.6, gate/up 13.5 = 3.7 TB/s, down 7.7); 16
+// tokens in MXFP4 50.1 us (31.1 and 21.2: 4.1 and 3.0 TB/s); five tokens of
+// eight experts of 4096 x 14336, bf16: gate/up 6.1 TB/s, down 5.8.
 #include <algorithm>
 
 #include "common.hpp"

@@ -20,8 +20,8 @@
 // rows; a second launch adds the work-groups' sums in their order.
 //
 // Measured: forward 16384 x 2048 bf16 25.7 us (5.2 TB/s); backward 32768 x
-// 2048 bf16 with a residual's gradient 93 + 5.6 us (5.8 TB/s); 1001 x 1035
-// float32 10.4 + 4.6; one row of 2048 forward 2.2; backward 4096 x 16384 (both
+// 2048 bf16 with a residual's gradient 93 + 5.4 us (5.8 TB/s); 1001 x 1035
+// float32 10.7 + 4.3; one row of 2048 forward 2.2; backward 4096 x 16384 (both
 // launches) bf16 97 us (4.2 TB/s), float32 158 (4.2).
 #include <algorithm>
 

@@ -18,8 +18,10 @@
 // wave takes an equal run of the items and keeps two batches of loads going
 // across them.
 //
-// Measured, 77 tokens x 8 over 128 experts, 2048 x 768: gate/up 44.6 us (4.8
-// TB/s), down 25.6 (4.2), entries and x 4.7.
+// Measured, 128 experts, 2048 x 768, k 8: 77 tokens gate/up 43.9 us (4.9
+// TB/s), down 26.5 (4.0), entries and x 5.0; 100 tokens 45.8, 27.9 and 4.9; 256
+// tokens (sixteen rows per expert, nearly half of the experts with a second
+// entry) 62.3, 38.4 and 5.8.
 #include <algorithm>
 
 #include "common.hpp"
