@@ -180,3 +180,31 @@ def test_layer_few(m, T, H, F, k):
         n[2, H - 2, F - 1] = bad
         n[2, 3, 31] = bad
         same_but(run(gu, n), clean, hit, [3, H - 2])
+
+
+@pytest.mark.parametrize("T,H,F,k", [(2, 96, 64, 2), (2, 256, 128, 3),
+                                     (9, 128, 256, 2), (12, 256, 128, 1),
+                                     (40, 128, 256, 2)])
+def test_layer_few_keeps_tokens_apart(m, T, H, F, k):
+    """NaN in one token's activations, next to others in its
+    column sets."""
+    rng = np.random.default_rng(T + F)
+    E = 6
+    x = normal(rng, (T, H))
+    idx = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    q = [m.mxfp4_quantize(bf(normal(rng, s, 0.05)))
+         for s in ((E, 2 * F, H), (E, H, F))]
+    w = up(rng.random((T, k)).astype(np.float32))
+
+    def run(x):
+        return m.moe_layer_few(bf(x), topk_idx=up(idx), topk_w=w,
+                               precision=m.PREC_MXFP4, w_gu_q=q[0],
+                               w_dn_q=q[1])["y"]
+    clean = run(x)
+    for t in sorted({0, T // 2, T - 1}):
+        bad = x.copy()
+        bad[t] = NAN
+        same_but(run(bad), clean, [t])
+        bad = x.copy()
+        bad[t, H - 3] = NAN
+        same_but(run(bad), clean, [t])
